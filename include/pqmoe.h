@@ -546,6 +546,152 @@ pqm_status pqm_moe_combine(const uint16_t *y_rows, const int32_t *slot,
                            const uint16_t *shared, int64_t tokens, int64_t k, int64_t N,
                            uint16_t *out, hipStream_t stream);
 
+/*
+ * RMS norm with the residual's addition, and the row-wise MXFP8 encoding of
+ * its output: the activation in front of an expert layer, normalised and
+ * quantized where it is produced ([BW] Format background: MXFP8; [MT] 5.3: an
+ * operand is quantized without another pass over it).  Per row:
+ *   sum = bf16(x + residual), added in binary32   (residual NULL: sum = x)
+ *   rstd = 1 / sqrt(mean(sum^2) + eps)
+ *   y = bf16(sum rstd weight)
+ *   q, s = pqm_quantize_mxfp8 (row-wise) of y, the same bytes
+ *   x [rows, cols] bf16, row stride ldx; residual likewise with ldr (device)
+ *   weight [cols] in weight_dtype (bf16 or binary32)                (device)
+ *   sum, y [rows, cols] bf16; q [rows, cols] E4M3; s [rows, cols/32] E8M0;
+ *   rstd [rows] binary32, for the backward pass                     (device)
+ * sum, y and rstd may be NULL, and so may the pair q, s; one of y and q is
+ * required (PQM_ERR_NULL).  sum may be the memory of x or of residual (with
+ * a row stride of cols) and is then updated in place; no other output may
+ * overlap an input.  Sums are binary32; rows whose squares leave binary32
+ * (values from about 2^63 on) are handled.  x + residual and y must stay
+ * within the bf16 range.
+ * Requires cols % 8 == 0 (% 32 with q, s), cols <= 16384, rows < 2^31,
+ * ldx, ldr >= cols, 2^-100 <= eps < infinity (PQM_ERR_SHAPE); x, residual,
+ * weight, sum, y and the strides 16-byte aligned, q 8-byte, rstd 4-byte
+ * (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint16_t *residual,
+                                      int64_t ldr, const void *weight, pqm_dtype weight_dtype,
+                                      int64_t rows, int64_t cols, float eps, uint16_t *sum,
+                                      uint16_t *y, uint8_t *q, uint8_t *s, float *rstd,
+                                      hipStream_t stream);
+
+/*
+ * Gradients of that norm, straight through the rounding and the encoding:
+ * with g = dy weight and h = x rstd (x: the `sum` of the forward call),
+ *   dx = bf16(rstd (g - h mean(g h)) + d_sum)   per row: the gradient of x
+ *        and of residual alike; d_sum (bf16 [rows, cols], may be NULL) is the
+ *        gradient that reaches sum past the norm;
+ *   dweight[c] = sum over rows of dy h, binary32, in a fixed order.
+ * dy, x, d_sum, dx bf16 [rows, cols] contiguous, rstd binary32 [rows],
+ * dweight binary32 [cols] (device).  dx may be the memory of d_sum, and no
+ * other output may overlap an input.  workspace (device, 16-byte aligned,
+ * contents irrelevant): pqm_rmsnorm_backward_workspace bytes; calls that may
+ * run at the same time need separate ones.  rows == 0 writes dweight = 0.
+ * Requires cols % 8 == 0, cols <= 16384, rows < 2^31 (PQM_ERR_SHAPE); dy, x,
+ * weight, d_sum, dx 16-byte aligned (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_rmsnorm_backward(const uint16_t *dy, const uint16_t *x, const void *weight,
+                                pqm_dtype weight_dtype, const float *rstd, const uint16_t *d_sum,
+                                int64_t rows, int64_t cols, uint16_t *dx, float *dweight,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t pqm_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * The router's gate: the k experts of each token, their probabilities, and
+ * the balance loss that keeps the experts' loads alike (the topk_ids and prob
+ * that pqm_moe_route and pqm_swiglu_prob take).
+ *   v = softmax(z) or sigmoid(z) of a token's logits z; p = v / sum(v)
+ *   topk_ids[t, j]: the expert of the j-th largest logit, equal logits in the
+ *       order of their index;
+ *   prob[t, j] = scale v_j / sum of the chosen v  (renormalize 1), or
+ *       scale v_j (renormalize 0);
+ *   counts[e] = valid tokens that chose e, counts[E] = their number Tv;
+ *   prob_sum[e] = sum of p over the valid tokens;
+ *   loss = loss_coef E sum_e (counts[e] / (k Tv)) (prob_sum[e] / Tv), 0 when
+ *       no token is valid.
+ *   logits [tokens, E] bf16 or binary32 (logits_dtype); topk_ids int32 and
+ *   prob binary32 [tokens, k]; counts int32 [E + 1], prob_sum binary32 [E],
+ *   loss binary32 [1]                                               (device)
+ * mask (device, uint8 [tokens], NULL: all valid): the logits of a token with
+ * mask 0 are not read; its prob is 0, it takes no part in counts, prob_sum or
+ * loss, and its ids are (t k + j) mod E, so that padding loads every expert
+ * alike in pqm_moe_route.  A logit of -inf closes an expert to a token
+ * (chosen last, prob 0; a row of -inf alone gives prob 0).  NaN and +inf are
+ * outside the contract (the ids stay in [0, E)).  The arithmetic is binary32.
+ * counts, prob_sum and loss go together: all NULL skips the loss, and
+ * workspace is then not needed.  workspace (device, 4-byte aligned, contents
+ * irrelevant): pqm_moe_gate_workspace bytes; calls that may run at the same
+ * time need separate ones.
+ * Requires 1 <= k <= 16, k <= num_experts <= 1024, tokens (k + 1) < 2^31
+ * (PQM_ERR_SHAPE); logits aligned to their element (PQM_ERR_ALIGN);
+ * renormalize 0 or 1 (PQM_ERR_ENUM).
+ */
+typedef enum pqm_score {
+    PQM_SCORE_SOFTMAX = 0,
+    PQM_SCORE_SIGMOID = 1
+} pqm_score;
+pqm_status pqm_moe_gate(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
+                        int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,
+                        int renormalize, float scale, int32_t *topk_ids, float *prob,
+                        float loss_coef, int32_t *counts, float *prob_sum, float *loss,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts);
+
+/*
+ * Gradient of the gate with respect to its logits: d_prob (binary32
+ * [tokens, k], NULL: none) through the chosen probabilities and d_loss
+ * (binary32 [1] on the device) through the loss.  The choice and the counts
+ * are held fixed; counts is the forward call's [E + 1], and counts and d_loss
+ * go together (both NULL: no loss).  The other arguments are the forward
+ * call's.  d_logits [tokens, E] in d_logits_dtype (rounded once), zero for
+ * masked tokens; it may not overlap logits.  topk_ids may hold any experts (an id twice adds
+ * up); ids outside [0, E) add nothing.  Same limits and errors.
+ */
+pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
+                                 int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,
+                                 int renormalize, float scale, const int32_t *topk_ids,
+                                 const float *d_prob, float loss_coef, const int32_t *counts,
+                                 const float *d_loss, void *d_logits, pqm_dtype d_logits_dtype,
+                                 hipStream_t stream);
+
+/*
+ * The experts' products for a few routed rows (decode): bf16 activations
+ * times NVFP4 weights ([BW] Format background: NVFP4; [MT] 2.2 decode), with
+ * neither routing nor activation quantization before it.  Row r belongs to
+ * expert e = ids[r]:
+ *   out[r, n] = s_g sum_k x[r / divisor, k] q[e, n, k] s_b[e, n, k / 16]
+ *   x bf16 [ceil(rows / divisor), K] contiguous; ids int32 [rows]   (device)
+ *   w_q [G, N, K/2], w_scale [G, N, K/16], w_outer [G N / w_rows_per_scale]
+ *       as pqm_quantize_nvfp4_per_token makes them                  (device)
+ *   out [rows, N] bf16 (rounded once) or binary32 per out_dtype     (device)
+ * With topk_ids [T, k] as ids: divisor = k for the first projection (x holds
+ * the tokens), 1 for the second (x holds one row per assignment).  Any order
+ * and any repetition of ids is legal; a row whose id lies outside [0, G) gives
+ * zeros.  The operand values are exact, sums are binary32, the outer scale is
+ * applied to the sum.  Nothing may overlap out.
+ * Requires rows <= 4096 (more: pqm_moe_route and pqm_moe_grouped_gemm),
+ * 1 <= divisor <= 4096, 1 <= G <= 4096, N <= 2^20, K % 32 == 0, 32 <= K <=
+ * 2^20, w_rows_per_scale >= 1 dividing G N (PQM_ERR_SHAPE); x, w_q and out
+ * 16-byte aligned, the others 4-byte (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_moe_gemv_nvfp4(const uint16_t *x, const int32_t *ids, int64_t rows, int64_t divisor,
+                              const uint8_t *w_q, const uint8_t *w_scale, const float *w_outer,
+                              int64_t w_rows_per_scale, int64_t G, int64_t N, int64_t K, void *out,
+                              pqm_dtype out_dtype, hipStream_t stream);
+
+/*
+ * The same for the gate_up projection, with the weighted SwiGLU in its
+ * epilogue: w_q [G, 2 inter, K/2] (gate rows, then up rows), prob binary32
+ * [rows], d bf16 [rows, inter] = bf16(silu(gate) up prob[r]).  gate and up
+ * stay in binary32 (pqm_swiglu_prob takes them rounded to bf16).
+ */
+pqm_status pqm_moe_gemv_swiglu_nvfp4(const uint16_t *x, const int32_t *ids, const float *prob,
+                                     int64_t rows, int64_t divisor, const uint8_t *w_q,
+                                     const uint8_t *w_scale, const float *w_outer,
+                                     int64_t w_rows_per_scale, int64_t G, int64_t inter, int64_t K,
+                                     uint16_t *d, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(HERE, "libpqmoe.so")
 FMT_BF16, FMT_MXFP8, FMT_NVFP4, FMT_FP8_BLOCK = 0, 1, 2, 3
 GEMM_FPROP, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
 OUT_BF16, OUT_FP32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _STATUS = {0: "ok", 1: "PQM_ERR_NULL", 2: "PQM_ERR_SHAPE", 3: "PQM_ERR_ALIGN",
            4: "PQM_ERR_ENUM", 5: "PQM_ERR_WORKSPACE", 6: "PQM_ERR_HIP"}
@@ -26,6 +27,7 @@ class PqmError(RuntimeError):
 _lib = None
 
 P, I64, SZ, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+F32 = ctypes.c_float
 
 # name -> argtypes; every entry point declared in include/pqmoe.h
 SIGNATURES = {
@@ -55,6 +57,15 @@ SIGNATURES = {
     "pqm_swiglu_prob_quantize_nvfp4": ([P, P, P, I64, I64, P, P, P, P, P], I32),
     "pqm_moe_combine": ([P, P, P, I64, I64, I64, P, P], I32),
     "pqm_validate_offsets": ([P, I64, I64, I64, P, P], I32),
+    "pqm_rmsnorm_quantize_mxfp8": ([P, I64, P, I64, P, I32, I64, I64, F32, P, P, P, P, P, P], I32),
+    "pqm_rmsnorm_backward": ([P, P, P, I32, P, P, I64, I64, P, P, P, SZ, P], I32),
+    "pqm_rmsnorm_backward_workspace": ([I64, I64], SZ),
+    "pqm_moe_gate": ([P, I32, P, I64, I64, I64, I32, I32, F32, P, P, F32, P, P, P, P, SZ, P], I32),
+    "pqm_moe_gate_workspace": ([I64, I64], SZ),
+    "pqm_moe_gate_backward": ([P, I32, P, I64, I64, I64, I32, I32, F32, P, P, F32, P, P, P, I32,
+                               P], I32),
+    "pqm_moe_gemv_nvfp4": ([P, P, I64, I64, P, P, P, I64, I64, I64, I64, P, I32, P], I32),
+    "pqm_moe_gemv_swiglu_nvfp4": ([P, P, P, I64, I64, P, P, P, I64, I64, I64, I64, P, P], I32),
 }
 
 
@@ -86,6 +97,38 @@ def _ptr(t):
 
 def _stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(name: str, dev: torch.device, *args):
+    """The entry point `name` on dev's current stream, with dev current: a
+    kernel is launched on the current device."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), name)
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape, dev: torch.device) -> torch.Tensor:
+    """t, checked: a contiguous tensor of that type and shape on dev."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{what}: on {t.device}, expected {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t
+
+
+def _bf16_or_f32(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    if t.dtype == torch.float32:
+        return OUT_FP32
+    raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
 
 
 def _bf16_2d(x: torch.Tensor) -> torch.Tensor:
@@ -177,6 +220,68 @@ def dequantize(fmt: int, q: torch.Tensor, s_block: torch.Tensor,
     return y
 
 
+# ---------------------------------------------------------------- norm
+
+def rmsnorm_quantize_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                           residual: torch.Tensor | None = None, keep_y: bool = False,
+                           quantize: bool = True, inplace: bool = False):
+    """RMS norm of x (+ residual), its output encoded in MXFP8 row-wise; see
+    pqm_rmsnorm_quantize_mxfp8 in pqmoe.h.  x, residual bf16 [R, C]; weight
+    bf16 or float32 [C].  Returns (q, s, y, sum, rstd): q, s None without
+    quantize; y (bf16) None unless keep_y or not quantize; sum = x + residual
+    in bf16, x itself without a residual, and written into residual's memory
+    with inplace; rstd float32 [R]."""
+    x = _bf16_2d(x)
+    R, C = x.shape
+    dev = x.device
+    wdt = _bf16_or_f32(weight, "weight")
+    _want(weight, "weight", weight.dtype, (C,), dev)
+    total = x
+    if residual is not None:
+        _bf16_2d(residual)
+        if residual.shape != x.shape or residual.device != dev:
+            raise ValueError("residual: expected x's shape and device")
+        if inplace and not residual.is_contiguous():
+            raise ValueError("residual: must be contiguous to be updated in place")
+        total = residual if inplace else torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+    q = s = y = None
+    if quantize:
+        q = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        s = torch.empty((R, C // 32), dtype=torch.uint8, device=dev)
+    if keep_y or not quantize:
+        y = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+    rstd = torch.empty((R,), dtype=torch.float32, device=dev)
+    _call("pqm_rmsnorm_quantize_mxfp8", dev, _ptr(x), x.stride(0) if R > 1 else C, _ptr(residual),
+          residual.stride(0) if residual is not None and R > 1 else C, _ptr(weight), wdt, R, C,
+          eps, None if residual is None else _ptr(total), _ptr(y), _ptr(q), _ptr(s), _ptr(rstd))
+    return q, s, y, total, rstd
+
+
+def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     d_sum: torch.Tensor | None = None):
+    """Gradients of rmsnorm_quantize_mxfp8; see pqm_rmsnorm_backward in
+    pqmoe.h.  dy the gradient of y, x the forward call's sum, d_sum what
+    reaches that sum past the norm.  Returns (dx bf16 [R, C], the gradient of
+    x and of residual; dweight float32 [C])."""
+    dy = _bf16_2d(dy)
+    R, C = dy.shape
+    dev = dy.device
+    _want(dy, "dy", torch.bfloat16, (R, C), dev)
+    _want(x, "x", torch.bfloat16, (R, C), dev)
+    wdt = _bf16_or_f32(weight, "weight")
+    _want(weight, "weight", weight.dtype, (C,), dev)
+    _want(rstd, "rstd", torch.float32, (R,), dev)
+    if d_sum is not None:
+        _want(d_sum, "d_sum", torch.bfloat16, (R, C), dev)
+    dx = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+    dw = torch.empty((C,), dtype=torch.float32, device=dev)
+    ws_bytes = lib().pqm_rmsnorm_backward_workspace(R, C)
+    ws = torch.empty((max(ws_bytes, 16),), dtype=torch.uint8, device=dev)
+    _call("pqm_rmsnorm_backward", dev, _ptr(dy), _ptr(x), _ptr(weight), wdt, _ptr(rstd),
+          _ptr(d_sum), R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws_bytes)
+    return dx, dw
+
+
 # ---------------------------------------------------------------- GEMM
 
 def moe_grouped_gemm(fmt: int, kind: int, a, b, offsets: torch.Tensor, N: int, K: int,
@@ -254,7 +359,129 @@ def moe_fc2_online_nvfp4_split(p: torch.Tensor, w_q, w_scale, w_outer, offsets: 
     return (y, gs, q, sb, ratio) if encodings else (y, gs)
 
 
+def _gemv_args(x, ids, rows_n, w_q, w_scale, w_outer, w_rows_per_scale, divisor):
+    """Checked sizes of a few-row product: (rows, K, G, rows per scale) for
+    weights of rows_n rows per expert."""
+    x = _bf16_2d(x)
+    K, dev = x.shape[1], x.device
+    rows = ids.numel()
+    if divisor < 1 or rows_n < 1 or K < 32 or K % 32:
+        raise PqmError(2, "pqm_moe_gemv_nvfp4")
+    _want(ids, "ids", torch.int32, ids.shape, dev)
+    _want(x, "x", torch.bfloat16, (-(-rows // divisor), K), dev)
+    G = w_q.numel() // (rows_n * (K // 2))
+    _want(w_q, "w_q", torch.uint8, w_q.shape, dev)
+    _want(w_scale, "w_scale", torch.uint8, w_scale.shape, dev)
+    _want(w_outer, "w_outer", torch.float32, w_outer.shape, dev)
+    rps = w_rows_per_scale or rows_n
+    if (w_q.numel() != G * rows_n * (K // 2) or w_scale.numel() != G * rows_n * (K // 16)
+            or w_outer.numel() * rps != G * rows_n):
+        raise ValueError("w_q, w_scale, w_outer: sizes do not belong together")
+    return rows, K, G, rps
+
+
+def moe_gemv_nvfp4(x: torch.Tensor, ids: torch.Tensor, w_q, w_scale, w_outer, N: int,
+                   w_rows_per_scale: int = 0, divisor: int = 1, out_dtype: int = OUT_BF16):
+    """A few routed rows times NVFP4 expert weights [G * N, K/2]; see
+    pqm_moe_gemv_nvfp4 in pqmoe.h.  x bf16 [rows / divisor, K], ids int32 (any
+    shape, one expert per row).  Returns [rows, N]."""
+    rows, K, G, rps = _gemv_args(x, ids, N, w_q, w_scale, w_outer, w_rows_per_scale, divisor)
+    dev = x.device
+    odt = torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16
+    out = torch.empty((rows, N), dtype=odt, device=dev)
+    _call("pqm_moe_gemv_nvfp4", dev, _ptr(x), _ptr(ids), rows, divisor, _ptr(w_q), _ptr(w_scale),
+          _ptr(w_outer), rps, G, N, K, _ptr(out), out_dtype)
+    return out
+
+
+def moe_gemv_swiglu_nvfp4(x: torch.Tensor, ids: torch.Tensor, prob: torch.Tensor, w_q, w_scale,
+                          w_outer, inter: int, w_rows_per_scale: int = 0, divisor: int = 1):
+    """The gate_up product of a few routed rows with SwiGLU x prob in its
+    epilogue, weights [G * 2 inter, K/2]; see pqm_moe_gemv_swiglu_nvfp4 in
+    pqmoe.h.  prob float32, one per row.  Returns d bf16 [rows, inter]."""
+    rows, K, G, rps = _gemv_args(x, ids, 2 * inter, w_q, w_scale, w_outer, w_rows_per_scale,
+                                 divisor)
+    dev = x.device
+    _want(prob, "prob", torch.float32, prob.shape, dev)
+    if prob.numel() != rows:
+        raise ValueError("prob: expected one value per row")
+    d = torch.empty((rows, inter), dtype=torch.bfloat16, device=dev)
+    _call("pqm_moe_gemv_swiglu_nvfp4", dev, _ptr(x), _ptr(ids), _ptr(prob), rows, divisor,
+          _ptr(w_q), _ptr(w_scale), _ptr(w_outer), rps, G, inter, K, _ptr(d))
+    return d
+
+
 # ---------------------------------------------------------------- MoE glue
+
+def moe_gate(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renormalize: bool = True,
+             scale: float = 1.0, mask: torch.Tensor | None = None,
+             loss_coef: float | None = None):
+    """The router's gate; see pqm_moe_gate in pqmoe.h.  logits bf16 or float32
+    [T, E]; mask uint8 or bool [T], zero for tokens to leave out.  Returns
+    (topk_ids int32 [T, k], prob float32 [T, k], counts int32 [E + 1],
+    prob_sum float32 [E], loss float32 [1]), the last three None without a
+    loss_coef."""
+    T, E = logits.shape
+    dev = logits.device
+    zdt = _bf16_or_f32(logits, "logits")
+    if not logits.is_cuda:
+        raise TypeError("expected a device tensor")
+    _want(logits, "logits", logits.dtype, (T, E), dev)
+    if mask is not None:
+        _want(mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, (T,), dev)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    prob = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    counts = prob_sum = loss = ws = None
+    ws_bytes = 0
+    if loss_coef is not None:
+        counts = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        prob_sum = torch.empty((E,), dtype=torch.float32, device=dev)
+        loss = torch.empty((1,), dtype=torch.float32, device=dev)
+        ws_bytes = lib().pqm_moe_gate_workspace(T, E)
+        ws = torch.empty((max(ws_bytes, 4),), dtype=torch.uint8, device=dev)
+    _call("pqm_moe_gate", dev, _ptr(logits), zdt, _ptr(mask), T, E, k, score, int(renormalize),
+          scale, _ptr(ids), _ptr(prob), loss_coef or 0.0, _ptr(counts), _ptr(prob_sum), _ptr(loss),
+          _ptr(ws), ws_bytes)
+    return ids, prob, counts, prob_sum, loss
+
+
+def moe_gate_backward(logits: torch.Tensor, ids: torch.Tensor, d_prob: torch.Tensor | None,
+                      score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
+                      mask: torch.Tensor | None = None, loss_coef: float | None = None,
+                      counts: torch.Tensor | None = None, d_loss: torch.Tensor | None = None,
+                      out_dtype: int | None = None):
+    """Gradient of moe_gate with respect to its logits; see
+    pqm_moe_gate_backward in pqmoe.h.  d_prob float32 [T, k] or None; counts
+    the forward call's and d_loss float32 [1], or both None.  Returns d_logits
+    [T, E], in the logits' type unless out_dtype says otherwise."""
+    T, E = logits.shape
+    dev = logits.device
+    zdt = _bf16_or_f32(logits, "logits")
+    if not logits.is_cuda:
+        raise TypeError("expected a device tensor")
+    _want(logits, "logits", logits.dtype, (T, E), dev)
+    k = ids.shape[-1]
+    _want(ids, "ids", torch.int32, (T, k), dev)
+    if d_prob is not None:
+        _want(d_prob, "d_prob", torch.float32, (T, k), dev)
+    if mask is not None:
+        _want(mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, (T,), dev)
+    if counts is not None:
+        _want(counts, "counts", torch.int32, (E + 1,), dev)
+        if loss_coef is None:
+            raise ValueError("counts: needs the forward call's loss_coef")
+    if d_loss is not None:
+        _want(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
+        if d_loss.numel() != 1:
+            raise ValueError("d_loss: expected one value")
+    odt = zdt if out_dtype is None else out_dtype
+    dz = torch.empty((T, E), dtype=torch.float32 if odt == OUT_FP32 else torch.bfloat16,
+                     device=dev)
+    _call("pqm_moe_gate_backward", dev, _ptr(logits), zdt, _ptr(mask), T, E, k, score,
+          int(renormalize), scale, _ptr(ids), _ptr(d_prob), loss_coef or 0.0, _ptr(counts),
+          _ptr(d_loss), _ptr(dz), odt)
+    return dz
+
 
 def moe_route(topk_ids: torch.Tensor, num_experts: int, shared_expert: bool = False):
     """Counting sort of assignments by expert.  topk_ids int32 [T, k].

@@ -24,7 +24,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "quantize_mxfp8.hip", "quantize_nvfp4.hip", "quantize_fp8_block.hip",
            "dequantize.hip",
-           "grouped_gemm.hip", "moe_glue.hip"]
+           "grouped_gemm.hip", "moe_glue.hip", "rmsnorm.hip", "moe_gate.hip",
+           "gemv_nvfp4.hip"]
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-ffp-contract=off", "-fno-fast-math",

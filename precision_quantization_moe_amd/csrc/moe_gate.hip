@@ -1,0 +1,481 @@
+// moe_gate.hip -- the router's gate: from logits [T, E] to the k experts of
+// each token and their probabilities, the per-expert counts and the balance
+// loss, and the gradient of both with respect to the logits.
+//
+// v = softmax(z) or sigmoid(z); p = v / sum_e v (a token's shares; softmax: v).
+// The choice is the k largest logits, ties to the lowest index: v grows with
+// z, so no rounding of v decides it.  prob_j = scale v_j / sum over the
+// chosen (renormalised) or scale v_j.  With c_e the valid tokens that chose e,
+// P_e = sum of p over the valid tokens, Tv their number:
+//   loss = coef E / (k Tv^2) sum_e c_e P_e.
+// Gradient, the counts held fixed: u_e = d prob / d v at the chosen experts,
+// h_e = d_loss coef E c_e / (k Tv^2) at every expert's share:
+//   softmax: dz = p (u + h - sum p (u + h))
+//   sigmoid: dz = v (1 - v) (u + (h - sum p h) / sum v).
+#include "pqm_device.hpp"
+#include "pqm_internal.hpp"
+#include "pqmoe.h"
+
+namespace pqm {
+
+namespace {
+
+constexpr int GATE_MAX_EXPERTS = 1024;
+constexpr int GATE_MAX_K = 16;
+constexpr int64_t GATE_GROUPS = 256;  // workgroups whose partial sums the last kernel joins
+
+// Reductions over the LPT lanes (16 or 64) that hold one token.
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = LPT / 2; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ int group_min(int v) {
+#pragma unroll
+  for (int o = LPT / 2; o >= 1; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+template <bool ZF32>
+__device__ __forceinline__ float load_logit(const void *z, int64_t i) {
+  if constexpr (ZF32) return static_cast<const float *>(z)[i];
+  return __uint_as_float((uint32_t) static_cast<const uint16_t *>(z)[i] << 16);
+}
+
+// Order-preserving key of a logit, never 0 (0 marks "no expert here" and
+// "already chosen").  -0 counts as +0; a NaN, outside the contract, ranks as
+// -inf, so that the ids stay experts whatever the logits hold.
+__device__ __forceinline__ uint32_t logit_key(float z) {
+  const uint32_t u = __float_as_uint(z == z ? z + 0.0f : -__builtin_inff());
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+}  // namespace
+
+// LPT lanes hold one token, VPL logits each (expert i LPT + lane).  SUMS: each
+// workgroup also leaves its counts and share sums in part_cnt / part_sum
+// [gridDim.x][E] (and its valid tokens in part_valid).
+template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
+__global__ __launch_bounds__(512) void k_moe_gate(
+    const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
+    int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ prob,
+    int32_t *__restrict__ part_cnt, float *__restrict__ part_sum, int32_t *__restrict__ part_valid) {
+  extern __shared__ int32_t sh[];  // SUMS: counts [E], share sums [waves][E]
+  const int l = threadIdx.x % LPT;
+  const int groups = blockDim.x / LPT;
+  float acc[VPL] = {};
+  int nvalid = 0;
+  if constexpr (SUMS) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sh[e] = 0;
+    __syncthreads();
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < T; t0 += (int64_t)gridDim.x * groups) {
+    const int64_t t = t0 + threadIdx.x / LPT;
+    const bool live = t < T;
+    const bool valid = live && (!mask || mask[t]);
+    float v[VPL];
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * LPT + l;
+      const bool in = e < E;
+      v[i] = in && valid ? load_logit<ZF32>(z, t * E + e) : -__builtin_inff();
+      key[i] = in ? logit_key(v[i]) : 0u;
+    }
+    int my_id = 0;
+    float my_z = -__builtin_inff(), top = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) m = max(m, key[i]);
+      m = group_max<LPT>(m);
+      int at = INT32_MAX;
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? i * LPT + l : at;
+      at = group_min<LPT>(at);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = i * LPT + l == at ? 0u : key[i];
+      if (j == 0) top = key_logit(m);
+      if (l == j) {
+        my_id = at;
+        my_z = key_logit(m);
+      }
+    }
+    // shares: exp(z - top) or sigmoid(z), and their sum; an all -inf row has none
+    if (!(top > -__builtin_inff())) top = 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = SOFTMAX ? expf(v[i] - top) : sigmoid(v[i]);
+      if (i * LPT + l >= E) v[i] = 0.0f;
+      sum += v[i];
+    }
+    sum = group_sum<LPT>(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    float w = l < k ? (SOFTMAX ? expf(my_z - top) : sigmoid(my_z)) : 0.0f;
+    if (renorm) {
+      const float total = group_sum<LPT>(w);
+      w = total > 0.0f ? w / total : 0.0f;
+    } else if (SOFTMAX) {
+      w *= inv;
+    }
+    if (live && l < k) {
+      // a token that the mask leaves out is not read: experts in turn, so that
+      // padding loads all of them alike, and no weight
+      ids[t * k + l] = valid ? my_id : (int32_t)((t * k + l) % E);
+      prob[t * k + l] = valid ? w * scale : 0.0f;
+    }
+    if constexpr (SUMS) {
+      if (valid) {
+        if (l < k) atomicAdd(&sh[my_id], 1);
+        if (l == 0) ++nvalid;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += v[i] * inv;
+      }
+    }
+  }
+  if constexpr (SUMS) {
+    float *shs = reinterpret_cast<float *>(sh + E);
+    const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+#pragma unroll
+      for (int o = LPT; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
+      const int e = i * LPT + l;
+      if ((threadIdx.x & 63) < LPT && e < E) shs[wave * E + e] = acc[i];
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) nvalid += __shfl_xor(nvalid, o, 64);
+    int32_t *shv = sh + E + nw * E;
+    if ((threadIdx.x & 63) == 0) shv[wave] = nvalid;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      float s = 0.0f;
+      for (int w = 0; w < nw; ++w) s += shs[w * E + e];
+      part_sum[(int64_t)blockIdx.x * E + e] = s;
+      part_cnt[(int64_t)blockIdx.x * E + e] = sh[e];
+    }
+    if (threadIdx.x == 0) {
+      int n = 0;
+      for (int w = 0; w < nw; ++w) n += shv[w];
+      part_valid[blockIdx.x] = n;
+    }
+  }
+}
+
+// One workgroup joins the P workgroups' sums, in a fixed order, and forms the
+// loss.  256 threads a column group: 4 row groups of 256 columns.
+__global__ __launch_bounds__(1024) void k_moe_balance(
+    const int32_t *__restrict__ part_cnt, const float *__restrict__ part_sum,
+    const int32_t *__restrict__ part_valid, int P, int E, int k, float coef,
+    int32_t *__restrict__ counts, float *__restrict__ prob_sum, float *__restrict__ loss) {
+  __shared__ float fs[1024];
+  __shared__ int32_t is[1024];
+  int nv = 0;
+  for (int p = threadIdx.x; p < P; p += 1024) nv += part_valid[p];
+  is[threadIdx.x] = nv;
+  __syncthreads();
+  for (int w = 512; w > 0; w >>= 1) {
+    if ((int)threadIdx.x < w) is[threadIdx.x] += is[threadIdx.x + w];
+    __syncthreads();
+  }
+  const int valid = is[0];
+  __syncthreads();
+  const int col = threadIdx.x & 255, grp = threadIdx.x >> 8;
+  float dot = 0.0f;
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + col;
+    float s = 0.0f;
+    int c = 0;
+    if (e < E)
+      for (int p = grp; p < P; p += 4) {
+        s += part_sum[(int64_t)p * E + e];
+        c += part_cnt[(int64_t)p * E + e];
+      }
+    fs[threadIdx.x] = s;
+    is[threadIdx.x] = c;
+    __syncthreads();
+    if (grp == 0 && e < E) {
+      s = (fs[col] + fs[col + 256]) + (fs[col + 512] + fs[col + 768]);
+      c = is[col] + is[col + 256] + is[col + 512] + is[col + 768];
+      prob_sum[e] = s;
+      counts[e] = c;
+      // the share of the assignments times the mean share of the probability
+      if (valid) dot += (float)c / ((float)k * (float)valid) * (s / (float)valid);
+    }
+    __syncthreads();
+  }
+  fs[threadIdx.x] = dot;
+  __syncthreads();
+  for (int w = 512; w > 0; w >>= 1) {
+    if ((int)threadIdx.x < w) fs[threadIdx.x] += fs[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    counts[E] = valid;
+    loss[0] = coef * (float)E * fs[0];
+  }
+}
+
+template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
+__global__ __launch_bounds__(256) void k_moe_gate_backward(
+    const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
+    int renorm, float scale, float coef, const int32_t *__restrict__ ids,
+    const float *__restrict__ d_prob, const int32_t *__restrict__ counts,
+    const float *__restrict__ d_loss, void *__restrict__ d_z, int out_f32) {
+  const int l = threadIdx.x % LPT;
+  constexpr int groups = 256 / LPT;
+  const int base = (threadIdx.x & 63) / LPT * LPT;  // the token's first lane in its wave
+  float h[VPL];
+  float hc = 0.0f;
+  if (counts && counts[E] > 0) {
+    const float tv = (float)counts[E];
+    hc = d_loss[0] * coef * (float)E / (float)k / tv / tv;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * LPT + l;
+    h[i] = counts && e < E ? hc * (float)counts[e] : 0.0f;
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < T; t0 += (int64_t)gridDim.x * groups) {
+    const int64_t t = t0 + threadIdx.x / LPT;
+    const bool live = t < T;
+    const bool valid = live && (!mask || mask[t]);
+    float v[VPL];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * LPT + l;
+      v[i] = e < E && valid ? load_logit<ZF32>(z, t * E + e) : -__builtin_inff();
+      top = fmaxf(top, v[i]);
+    }
+    int my_id = -1;
+    float my_v = 0.0f, my_d = 0.0f;
+    if (valid && l < k) {
+      const int id = ids[t * k + l];
+      if (id >= 0 && id < E) {
+        my_id = id;
+        my_v = load_logit<ZF32>(z, t * E + id);
+        my_d = d_prob ? d_prob[t * k + l] * scale : 0.0f;
+      }
+    }
+    if constexpr (SOFTMAX) {
+#pragma unroll
+      for (int o = LPT / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      if (!(top > -__builtin_inff())) top = 0.0f;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = SOFTMAX ? expf(v[i] - top) : sigmoid(v[i]);
+      if (i * LPT + l >= E) v[i] = 0.0f;
+      sum += v[i];
+    }
+    sum = group_sum<LPT>(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    if (SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] *= inv;
+    }
+    if (my_id >= 0) my_v = SOFTMAX ? expf(my_v - top) * inv : sigmoid(my_v);
+    else my_v = 0.0f;
+    if (renorm) {
+      const float total = group_sum<LPT>(my_v);
+      const float dot = group_sum<LPT>(my_d * my_v);
+      const float it = total > 0.0f ? 1.0f / total : 0.0f;
+      my_d = (my_d - dot * it) * it;
+    }
+    float u[VPL] = {};
+    for (int j = 0; j < k; ++j) {
+      const int id = __shfl(my_id, base + j, 64);
+      const float d = __shfl(my_d, base + j, 64);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) u[i] += i * LPT + l == id ? d : 0.0f;
+    }
+    float dot = 0.0f;  // softmax: sum p (u + h); sigmoid: sum p h
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dot += SOFTMAX ? v[i] * (u[i] + h[i]) : v[i] * inv * h[i];
+    dot = group_sum<LPT>(dot);
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * LPT + l;
+      if (e >= E) continue;
+      float g = SOFTMAX ? v[i] * (u[i] + h[i] - dot)
+                        : v[i] * (1.0f - v[i]) * (u[i] + (h[i] - dot) * inv);
+      if (!valid) g = 0.0f;
+      if (out_f32) static_cast<float *>(d_z)[t * E + e] = g;
+      else static_cast<uint16_t *>(d_z)[t * E + e] = (uint16_t)pk_bf16_rne(g, 0.0f);
+    }
+  }
+}
+
+namespace {
+
+int64_t gate_groups(int64_t T, int64_t E) {
+  const int64_t per = 512 / (E <= 256 ? 16 : 64);
+  const int64_t g = (T + per - 1) / per;
+  return g < 1 ? 1 : g < GATE_GROUPS ? g : GATE_GROUPS;
+}
+
+size_t gate_workspace_bytes(int64_t T, int64_t E) {
+  const int64_t P = gate_groups(T, E);
+  return (size_t)(P * E * 8 + P * 4);
+}
+
+struct GateArgs {
+  const void *z;
+  const uint8_t *mask;
+  int64_t T;
+  int E, k, renorm;
+  float scale, coef;
+  int32_t *ids;
+  float *prob;
+  int32_t *counts;
+  float *prob_sum, *loss;
+  void *ws;
+  hipStream_t st;
+};
+
+template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
+hipError_t go_gate(const GateArgs &a) {
+  const int64_t P = gate_groups(a.T, a.E);
+  if (!a.loss) {
+    // no sums to join: as many workgroups as there are tokens for
+    const int64_t per = 256 / LPT, g = (a.T + per - 1) / per;
+    hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, false>), dim3((unsigned)g), dim3(256),
+                       0, a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob,
+                       (int32_t *)nullptr, (float *)nullptr, (int32_t *)nullptr);
+    return hipGetLastError();
+  }
+  float *ps = static_cast<float *>(a.ws);
+  int32_t *pc = reinterpret_cast<int32_t *>(ps + P * a.E), *pv = pc + P * a.E;
+  const size_t lds = (size_t)(a.E * 9 + 8) * 4;
+  hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, true>), dim3((unsigned)P), dim3(512), lds,
+                     a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob, pc, ps, pv);
+  hipLaunchKernelGGL(k_moe_balance, dim3(1), dim3(1024), 0, a.st, pc, ps, pv, (int)P, a.E, a.k,
+                     a.coef, a.counts, a.prob_sum, a.loss);
+  return hipGetLastError();
+}
+
+struct GateBackArgs {
+  const void *z;
+  const uint8_t *mask;
+  int64_t T;
+  int E, k, renorm;
+  float scale, coef;
+  const int32_t *ids;
+  const float *d_prob;
+  const int32_t *counts;
+  const float *d_loss;
+  void *d_z;
+  int out_f32;
+  hipStream_t st;
+};
+
+template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
+hipError_t go_gate_back(const GateBackArgs &a) {
+  const int64_t per = 256 / LPT, g = (a.T + per - 1) / per;
+  hipLaunchKernelGGL((k_moe_gate_backward<LPT, VPL, ZF32, SOFTMAX>),
+                     dim3((unsigned)(g < 8192 ? g : 8192)), dim3(256), 0, a.st, a.z, a.mask, a.T,
+                     a.E, a.k, a.renorm, a.scale, a.coef, a.ids, a.d_prob, a.counts, a.d_loss,
+                     a.d_z, a.out_f32);
+  return hipGetLastError();
+}
+
+// Sixteen lanes a token up to 256 experts (their reductions take four lane
+// steps instead of six, for four tokens at once), a wave a token beyond.
+#define PQM_GATE_PICK2(FN, Z, S, A)                \
+  (A.E <= 64    ? FN<16, 4, Z, S>(A)               \
+   : A.E <= 128 ? FN<16, 8, Z, S>(A)               \
+   : A.E <= 256 ? FN<16, 16, Z, S>(A)              \
+   : A.E <= 512 ? FN<64, 8, Z, S>(A)               \
+                : FN<64, 16, Z, S>(A))
+#define PQM_GATE_PICK(FN, F32, SM, A)                                                   \
+  ((F32) ? ((SM) ? PQM_GATE_PICK2(FN, true, true, A) : PQM_GATE_PICK2(FN, true, false, A)) \
+         : ((SM) ? PQM_GATE_PICK2(FN, false, true, A) : PQM_GATE_PICK2(FN, false, false, A)))
+
+bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; }
+
+// What the forward and the backward call check alike.
+pqm_status gate_shape(pqm_dtype dtype, pqm_score score, int64_t T, int64_t E, int64_t k,
+                      int renorm) {
+  if (dtype != PQM_OUT_BF16 && dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
+  if (score != PQM_SCORE_SOFTMAX && score != PQM_SCORE_SIGMOID) return PQM_ERR_ENUM;
+  if (renorm != 0 && renorm != 1) return PQM_ERR_ENUM;
+  if (T < 0 || E < 1 || E > GATE_MAX_EXPERTS || k < 1 || k > GATE_MAX_K || k > E)
+    return PQM_ERR_SHAPE;
+  if (T * (k + 1) > (int64_t)0x7FFFFFFF) return PQM_ERR_SHAPE;
+  return PQM_OK;
+}
+
+}  // namespace
+}  // namespace pqm
+
+extern "C" {
+
+size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts) {
+  if (tokens < 0 || num_experts < 1 || num_experts > pqm::GATE_MAX_EXPERTS) return 0;
+  return pqm::gate_workspace_bytes(tokens, num_experts);
+}
+
+pqm_status pqm_moe_gate(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
+                        int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,
+                        int renormalize, float scale, int32_t *topk_ids, float *prob,
+                        float loss_coef, int32_t *counts, float *prob_sum, float *loss,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  using namespace pqm;
+  const pqm_status bad = gate_shape(logits_dtype, score, tokens, num_experts, k, renormalize);
+  if (bad != PQM_OK) return bad;
+  if (tokens > 0 && (!logits || !topk_ids || !prob)) return PQM_ERR_NULL;
+  const bool sums = counts || prob_sum || loss;
+  if (sums && (!counts || !prob_sum || !loss || !workspace)) return PQM_ERR_NULL;
+  if (sums && workspace_bytes < gate_workspace_bytes(tokens, num_experts)) return PQM_ERR_WORKSPACE;
+  if (!al(logits, logits_dtype == PQM_OUT_FP32 ? 4 : 2) || !al(topk_ids, 4) || !al(prob, 4) ||
+      !al(counts, 4) || !al(prob_sum, 4) || !al(loss, 4) || (sums && !al(workspace, 4)))
+    return PQM_ERR_ALIGN;
+  if (tokens == 0 && !sums) return PQM_OK;
+  const GateArgs a = {logits, mask, tokens, (int)num_experts, (int)k, renormalize, scale,
+                      loss_coef, topk_ids, prob, counts, prob_sum, loss, workspace, stream};
+  return st_of(PQM_GATE_PICK(go_gate, logits_dtype == PQM_OUT_FP32, score == PQM_SCORE_SOFTMAX, a));
+}
+
+pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
+                                 int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,
+                                 int renormalize, float scale, const int32_t *topk_ids,
+                                 const float *d_prob, float loss_coef, const int32_t *counts,
+                                 const float *d_loss, void *d_logits, pqm_dtype d_logits_dtype,
+                                 hipStream_t stream) {
+  using namespace pqm;
+  const pqm_status bad = gate_shape(logits_dtype, score, tokens, num_experts, k, renormalize);
+  if (bad != PQM_OK) return bad;
+  if (d_logits_dtype != PQM_OUT_BF16 && d_logits_dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
+  if (tokens == 0) return PQM_OK;
+  if (!logits || !topk_ids || !d_logits || (!d_prob && !counts)) return PQM_ERR_NULL;
+  if ((counts == nullptr) != (d_loss == nullptr)) return PQM_ERR_NULL;
+  if (!al(logits, logits_dtype == PQM_OUT_FP32 ? 4 : 2) ||
+      !al(d_logits, d_logits_dtype == PQM_OUT_FP32 ? 4 : 2) || !al(topk_ids, 4) || !al(d_prob, 4) || !al(counts, 4) ||
+      !al(d_loss, 4))
+    return PQM_ERR_ALIGN;
+  const GateBackArgs a = {logits, mask, tokens, (int)num_experts, (int)k, renormalize, scale,
+                          loss_coef, topk_ids, d_prob, counts, d_loss, d_logits,
+                          d_logits_dtype == PQM_OUT_FP32, stream};
+  return st_of(
+      PQM_GATE_PICK(go_gate_back, logits_dtype == PQM_OUT_FP32, score == PQM_SCORE_SOFTMAX, a));
+}
+
+}  // extern "C"

@@ -1,0 +1,379 @@
+// rmsnorm.hip -- the norm in front of an expert layer: residual addition, RMS
+// norm and the row-wise MXFP8 encoding of its output in one pass, and the
+// gradients of that norm.
+//
+// Forward, one row of C values:  s = bf16(x + r);  rstd = 1 / sqrt(mean(s^2) +
+// eps);  y = bf16(s rstd w);  (q, E8M0) = MXFP8 1x32 blocks of y.  The sum is
+// rounded first because that rounded sum is what the residual stream carries
+// on and what the backward pass reads again; y is rounded to bf16 before the
+// encoding, so that the bytes are those of pqm_quantize_mxfp8 of the y that a
+// caller may keep.  Squares and their sum are binary32.
+//
+// Backward (straight through both roundings), g = dy w, h = s rstd:
+//   dx = rstd (g - h mean(g h)) + d_sum,   dw_c = sum over rows of dy h.
+#include "pqm_device.hpp"
+#include "pqm_internal.hpp"
+#include "pqmoe.h"
+
+namespace pqm {
+
+namespace {
+
+// 8 weights from column c on, as binary32.
+template <bool WF32>
+__device__ __forceinline__ void load_w8(const void *__restrict__ w, int64_t c, float (&o)[8]) {
+  if constexpr (WF32) {
+    const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c);
+    const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + 4);
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + c);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = bf16_lo_f32(u[i]);
+      o[2 * i + 1] = bf16_hi_f32(u[i]);
+    }
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sum over the TPR threads of a row (64: one wave; 256: the workgroup, through
+// `red`, 4 slots).  Every thread of the workgroup must call it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+  v = wave_sum(v);
+  if constexpr (TPR == 64) return v;
+  __syncthreads();  // the slots' last readers are done
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+}  // namespace
+
+// One row per TPR threads, NC chunks of 8 values per thread, kept in registers
+// between the sum of squares and the scaling, so each input is read once.
+// `sum` may be x or r itself: a thread reads what it overwrites before it does.
+template <int TPR, int NC, bool WF32>
+__global__ __launch_bounds__(256) void k_rmsnorm_quant(
+    const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
+    int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *__restrict__ y,
+    uint8_t *__restrict__ q, uint8_t *__restrict__ s, float *__restrict__ rstd_out) {
+  __shared__ float red[4];
+  const int l = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const bool live = row < rows;  // with 64 threads a row: the last workgroup's spare waves
+  uint32_t v[NC][4];
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t c = ((int64_t)i * TPR + l) * 8;
+    uint4 a = make_uint4(0, 0, 0, 0);
+    if (live && c < C) {
+      a = *reinterpret_cast<const uint4 *>(x + row * ldx + c);
+      if (r) {
+        const uint4 b = *reinterpret_cast<const uint4 *>(r + row * ldr + c);
+        a.x = pk_bf16_rne(bf16_lo_f32(a.x) + bf16_lo_f32(b.x), bf16_hi_f32(a.x) + bf16_hi_f32(b.x));
+        a.y = pk_bf16_rne(bf16_lo_f32(a.y) + bf16_lo_f32(b.y), bf16_hi_f32(a.y) + bf16_hi_f32(b.y));
+        a.z = pk_bf16_rne(bf16_lo_f32(a.z) + bf16_lo_f32(b.z), bf16_hi_f32(a.z) + bf16_hi_f32(b.z));
+        a.w = pk_bf16_rne(bf16_lo_f32(a.w) + bf16_lo_f32(b.w), bf16_hi_f32(a.w) + bf16_hi_f32(b.w));
+      }
+    }
+    v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = bf16_lo_f32(v[i][j]), hi = bf16_hi_f32(v[i][j]);
+      sq += lo * lo;
+      sq += hi * hi;
+    }
+  }
+  if (sum) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      if (live && c < C)
+        *reinterpret_cast<uint4 *>(sum + row * C + c) =
+            make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    }
+  }
+  const float total = row_sum<TPR>(sq, red);
+  float rstd = 1.0f / sqrtf(total / (float)C + eps);
+  // Values from about 2^63 on square beyond binary32: sum (s 2^-80)^2 then,
+  // at most 2^15 (2^48)^2; eps is far below the last bit of such a mean.
+  if (!(total < __builtin_inff())) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = bf16_lo_f32(v[i][j]) * 0x1p-80f, hi = bf16_hi_f32(v[i][j]) * 0x1p-80f;
+        t += lo * lo;
+        t += hi * hi;
+      }
+    // with one wave a row the other waves' rows need not take this branch
+    t = row_sum<TPR>(t, red);
+    rstd = 0x1p-80f / sqrtf(t / (float)C);
+  }
+  if (!live) return;
+  if (rstd_out && l == 0) rstd_out[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t c = ((int64_t)i * TPR + l) * 8;
+    if (c >= C) continue;  // whole quads: C is a multiple of 32 where q is written
+    float wf[8];
+    load_w8<WF32>(w, c, wf);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pk_bf16_rne(bf16_lo_f32(v[i][j]) * rstd * wf[2 * j],
+                         bf16_hi_f32(v[i][j]) * rstd * wf[2 * j + 1]);
+    if (y) *reinterpret_cast<uint4 *>(y + row * C + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (q) {
+      uint32_t mm = pk_max_u16(pk_max_u16(o[0] & 0x7FFF7FFFu, o[1] & 0x7FFF7FFFu),
+                               pk_max_u16(o[2] & 0x7FFF7FFFu, o[3] & 0x7FFF7FFFu));
+      mm = max(mm & 0xFFFFu, mm >> 16);
+      mm = max(mm, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mm, 0xB1, 0xF, 0xF, false));
+      mm = max(mm, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mm, 0x4E, 0xF, 0xF, false));
+      const uint32_t b = mx_scale_byte(mm);
+      const float scale = __uint_as_float(b << 23);
+      *reinterpret_cast<uint2 *>(q + row * C + c) =
+          make_uint2(cvt4_e4m3_bf16(o[0], o[1], scale), cvt4_e4m3_bf16(o[2], o[3], scale));
+      if ((threadIdx.x & 3) == 0) s[row * (C / 32) + c / 32] = (uint8_t)b;
+    }
+  }
+}
+
+// Gradients.  A workgroup takes rows blockIdx.x, + gridDim.x, ... (4 at a time
+// with one wave a row); a thread owns the same columns of every row, so dw's
+// sums stay in registers and leave once, as the workgroup's row of `part`.
+template <int TPR, int NC, bool WF32>
+__global__ __launch_bounds__(256) void k_rmsnorm_backward(
+    const uint16_t *__restrict__ dy, const uint16_t *__restrict__ sx, const void *__restrict__ w,
+    const float *__restrict__ rstd, const uint16_t *dsum, int64_t rows, int64_t C, uint16_t *dx,
+    float *__restrict__ part) {
+  constexpr int RPB = 256 / TPR;
+  extern __shared__ float lds[];  // [4][C] with one wave a row
+  __shared__ float red[4];
+  const int l = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  float acc[NC][8] = {};
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + sub;
+    const bool live = row < rows;
+    const float rs = live ? rstd[row] : 0.0f;
+    uint4 gv[NC], sv[NC];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      gv[i] = sv[i] = make_uint4(0, 0, 0, 0);
+      if (live && c < C) {
+        gv[i] = *reinterpret_cast<const uint4 *>(dy + row * C + c);
+        sv[i] = *reinterpret_cast<const uint4 *>(sx + row * C + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      if (c >= C) continue;
+      float wf[8];
+      load_w8<WF32>(w, c, wf);
+      const uint32_t gu[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
+      const uint32_t su[4] = {sv[i].x, sv[i].y, sv[i].z, sv[i].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = j & 1 ? bf16_hi_f32(gu[j / 2]) : bf16_lo_f32(gu[j / 2]);
+        const float h = (j & 1 ? bf16_hi_f32(su[j / 2]) : bf16_lo_f32(su[j / 2])) * rs;
+        const float t = d * h;
+        acc[i][j] += t;
+        dot += t * wf[j];
+      }
+    }
+    const float m = row_sum<TPR>(dot, red) / (float)C;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      if (!live || c >= C) continue;
+      float wf[8];
+      load_w8<WF32>(w, c, wf);
+      const uint32_t gu[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
+      const uint32_t su[4] = {sv[i].x, sv[i].y, sv[i].z, sv[i].w};
+      uint4 dv = make_uint4(0, 0, 0, 0);
+      if (dsum) dv = *reinterpret_cast<const uint4 *>(dsum + row * C + c);
+      const uint32_t du[4] = {dv.x, dv.y, dv.z, dv.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = rs * (bf16_lo_f32(gu[j]) * wf[2 * j] - bf16_lo_f32(su[j]) * rs * m);
+        const float hi = rs * (bf16_hi_f32(gu[j]) * wf[2 * j + 1] - bf16_hi_f32(su[j]) * rs * m);
+        o[j] = pk_bf16_rne(lo + bf16_lo_f32(du[j]), hi + bf16_hi_f32(du[j]));
+      }
+      *reinterpret_cast<uint4 *>(dx + row * C + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if constexpr (TPR == 256) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      if (c >= C) continue;
+      float *p = part + blockIdx.x * C + c;
+      *reinterpret_cast<float4 *>(p) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4 *>(p + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i * TPR + l) * 8;
+      if (c >= C) continue;
+      float *p = lds + sub * C + c;
+      *reinterpret_cast<float4 *>(p) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4 *>(p + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < C; c += 256)
+      part[blockIdx.x * C + c] = (lds[c] + lds[C + c]) + (lds[2 * C + c] + lds[3 * C + c]);
+  }
+}
+
+// dw = sum of the P rows of part, always in the same order: 16 columns x 16
+// row groups a workgroup, the groups' sums joined through LDS.
+__global__ __launch_bounds__(256) void k_rmsnorm_dw(const float *__restrict__ part, int64_t P,
+                                                    int64_t C, float *__restrict__ dw) {
+  __shared__ float sh[16][17];
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + col;
+  float a = 0.0f;
+  if (c < C)
+    for (int64_t p = grp; p < P; p += 16) a += part[p * C + c];
+  sh[grp][col] = a;
+  __syncthreads();
+  if (grp == 0 && c < C) {
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) t += sh[g][col];
+    dw[c] = t;
+  }
+}
+
+namespace {
+
+constexpr int64_t NORM_MAX_COLS = 16384;  // 8 chunks of 8 values for each of 256 threads
+
+// Workgroups of the backward kernel, i.e. rows of its partial sums of dw.
+int64_t norm_backward_groups(int64_t rows, int64_t C) {
+  const int64_t per = C <= 2048 ? 4 : 1;
+  const int64_t g = (rows + per - 1) / per;
+  return g < 512 ? g : 512;
+}
+
+template <int TPR, int NC>
+hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr,
+                    const void *w, int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *y,
+                    uint8_t *q, uint8_t *s, float *rstd, hipStream_t st) {
+  const dim3 grid((unsigned)((rows + 256 / TPR - 1) / (256 / TPR)));
+  if (wf32)
+    hipLaunchKernelGGL((k_rmsnorm_quant<TPR, NC, true>), grid, dim3(256), 0, st, x, ldx, r, ldr, w,
+                       rows, C, eps, sum, y, q, s, rstd);
+  else
+    hipLaunchKernelGGL((k_rmsnorm_quant<TPR, NC, false>), grid, dim3(256), 0, st, x, ldx, r, ldr, w,
+                       rows, C, eps, sum, y, q, s, rstd);
+  return hipGetLastError();
+}
+
+template <int TPR, int NC>
+hipError_t go_back(bool wf32, const uint16_t *dy, const uint16_t *x, const void *w,
+                   const float *rstd, const uint16_t *dsum, int64_t rows, int64_t C, uint16_t *dx,
+                   float *part, hipStream_t st) {
+  const dim3 grid((unsigned)norm_backward_groups(rows, C));
+  const size_t lds = TPR == 64 ? 4 * C * sizeof(float) : 0;
+  if (wf32)
+    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, true>), grid, dim3(256), lds, st, dy, x, w,
+                       rstd, dsum, rows, C, dx, part);
+  else
+    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, false>), grid, dim3(256), lds, st, dy, x, w,
+                       rstd, dsum, rows, C, dx, part);
+  return hipGetLastError();
+}
+
+// One wave a row up to 2048 columns (no barrier between a row's sum and its
+// use), the workgroup a row beyond (a wave would hold over 32 values a lane
+// of each tensor).
+#define PQM_NORM_PICK(FN, ...)                               \
+  (C <= 512     ? FN<64, 1>(__VA_ARGS__)                     \
+   : C <= 1024  ? FN<64, 2>(__VA_ARGS__)                     \
+   : C <= 2048  ? FN<64, 4>(__VA_ARGS__)                     \
+   : C <= 4096  ? FN<256, 2>(__VA_ARGS__)                    \
+   : C <= 8192  ? FN<256, 4>(__VA_ARGS__)                    \
+                : FN<256, 8>(__VA_ARGS__))
+
+bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; }
+
+}  // namespace
+}  // namespace pqm
+
+extern "C" {
+
+pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint16_t *residual,
+                                      int64_t ldr, const void *weight, pqm_dtype weight_dtype,
+                                      int64_t rows, int64_t cols, float eps, uint16_t *sum,
+                                      uint16_t *y, uint8_t *q, uint8_t *s, float *rstd,
+                                      hipStream_t stream) {
+  using namespace pqm;
+  if (weight_dtype != PQM_OUT_BF16 && weight_dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
+  if (rows < 0 || cols < 0 || cols % 8 || cols > NORM_MAX_COLS || rows >= ((int64_t)1 << 31))
+    return PQM_ERR_SHAPE;
+  if (ldx < cols || (residual && ldr < cols)) return PQM_ERR_SHAPE;
+  if ((q || s) && cols % 32) return PQM_ERR_SHAPE;
+  if (!(eps >= 0x1p-100f) || !(eps < __builtin_inff())) return PQM_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return PQM_OK;
+  if (!x || !weight || (!q && !y) || (q == nullptr) != (s == nullptr)) return PQM_ERR_NULL;
+  if (!al(x, 16) || ldx % 8 || !al(weight, 16) || !al(sum, 16) || !al(y, 16) || !al(q, 8) ||
+      !al(rstd, 4))
+    return PQM_ERR_ALIGN;
+  if (residual && (!al(residual, 16) || ldr % 8)) return PQM_ERR_ALIGN;
+  const int64_t C = cols;
+  return st_of(PQM_NORM_PICK(go_quant, weight_dtype == PQM_OUT_FP32, x, ldx, residual, ldr, weight,
+                             rows, C, eps, sum, y, q, s, rstd, stream));
+}
+
+size_t pqm_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols > pqm::NORM_MAX_COLS) return 0;
+  return (size_t)(pqm::norm_backward_groups(rows, cols) * cols) * sizeof(float);
+}
+
+pqm_status pqm_rmsnorm_backward(const uint16_t *dy, const uint16_t *x, const void *weight,
+                                pqm_dtype weight_dtype, const float *rstd, const uint16_t *d_sum,
+                                int64_t rows, int64_t cols, uint16_t *dx, float *dweight,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  using namespace pqm;
+  if (weight_dtype != PQM_OUT_BF16 && weight_dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
+  if (rows < 0 || cols < 0 || cols % 8 || cols > NORM_MAX_COLS || rows >= ((int64_t)1 << 31))
+    return PQM_ERR_SHAPE;
+  if (cols == 0) return PQM_OK;
+  if (!dweight || (rows > 0 && (!dy || !x || !weight || !rstd || !dx || !workspace)))
+    return PQM_ERR_NULL;
+  if (workspace_bytes < pqm_rmsnorm_backward_workspace(rows, cols)) return PQM_ERR_WORKSPACE;
+  if (!al(dy, 16) || !al(x, 16) || !al(weight, 16) || !al(rstd, 4) || !al(d_sum, 16) ||
+      !al(dx, 16) || !al(dweight, 4) || !al(workspace, 16))
+    return PQM_ERR_ALIGN;
+  const int64_t C = cols;
+  float *part = static_cast<float *>(workspace);
+  if (rows > 0) {
+    const hipError_t e = PQM_NORM_PICK(go_back, weight_dtype == PQM_OUT_FP32, dy, x, weight, rstd,
+                                       d_sum, rows, C, dx, part, stream);
+    if (e != hipSuccess) return PQM_ERR_HIP;
+  }
+  // no rows: the sum over none of them is zero
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((C + 15) / 16)), dim3(256), 0, stream, part,
+                     rows > 0 ? norm_backward_groups(rows, C) : 0, C, dweight);
+  return st_of(hipGetLastError());
+}
+
+}  // extern "C"

@@ -93,9 +93,16 @@ def mxfp8_moe_forward(x, topk_ids, prob_flat, w1q, w1s, w2q, w2s, num_experts: i
     materialised (bf16; d and its MXFP8 encoding in one fused pass);
     without, the gate_up GEMM's epilogue produces the MXFP8 encoding of d
     directly and c, d are None (same bytes)."""
-    T, H = x.shape
-    off, src, tok, slot = b.moe_route(topk_ids, num_experts)
     qx, sx, _, _ = b.quantize_mxfp8(x, colwise=False)
+    return _mxfp8_experts(qx, sx, topk_ids, prob_flat, w1q, w1s, w2q, w2s, num_experts, inter,
+                          keep_intermediates)
+
+
+def _mxfp8_experts(qx, sx, topk_ids, prob_flat, w1q, w1s, w2q, w2s, num_experts: int, inter: int,
+                   keep_intermediates: bool):
+    """The routed experts on tokens already in row-wise MXFP8 (qx, sx)."""
+    H = qx.shape[1]
+    off, src, tok, slot = b.moe_route(topk_ids, num_experts)
     qa = b.moe_gather_rows(qx, tok)
     sa = b.moe_gather_rows(sx, tok)
     if keep_intermediates or inter % 128 or H % 128 or H > 2048:
@@ -137,3 +144,91 @@ def nvfp4_moe_forward(x, topk_ids, prob_all, w1q, w1b, w1g, w2q, w2b, w2g, num_e
     out = b.moe_combine(y[:T * k], slot, shared=y[T * k:])
     return dict(off=off, src=src, tok=tok, slot=slot, qa=qa, sba=sba, sga=sga, c=c, d=d,
                 qd=qd, sbd=sbd, sgd=sgd, y=y, out=out)
+
+
+def block_plan(tokens: int, k: int, device):
+    """The index tensors that the block passes below need for `tokens` tokens,
+    made once: off [2] the one group of all tokens, slot [tokens, k] each
+    assignment's own row, row [tokens, 1] each token's own row."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return dict(off=torch.tensor([0, tokens], dtype=torch.int64, device=device),
+                slot=torch.arange(tokens * k, **i32).view(tokens, k),
+                row=torch.arange(tokens, **i32).view(tokens, 1))
+
+
+def _router_logits(y, gate_w, off):
+    """y [T, H] times the router's weight [E, H], both bf16, in binary32."""
+    E, H = gate_w.shape
+    return b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_FPROP, y, gate_w, off, E, H,
+                              out_dtype=b.OUT_FP32)
+
+
+def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, k: int,
+                     inter: int, plan=None, score: int = b.SCORE_SOFTMAX,
+                     renormalize: bool = True, scale: float = 1.0, eps: float = 1e-6):
+    """One decode step of an expert layer with NVFP4 weights for a few tokens
+    (T * k <= 4096): residual addition and RMS norm, router gate, gate_up with
+    SwiGLU, down projection, combine.  Activations stay in bf16, and nothing
+    is sorted or gathered.  x, residual [T, H] bf16 (residual may be None);
+    gate_w [E, H] bf16, E % 8 == 0; the weights as
+    quantize_expert_weights_nvfp4 returns them; plan from block_plan(T, k,
+    device).  Returns dict(out [T, H] bf16, h (the new residual stream), y,
+    ids, prob, d)."""
+    T, H = x.shape
+    plan = plan or block_plan(T, k, x.device)
+    _, _, y, h, _ = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, quantize=False)
+    logits = _router_logits(y, gate_w, plan["off"])
+    ids, prob, _, _, _ = b.moe_gate(logits, k, score, renormalize, scale)
+    d = b.moe_gemv_swiglu_nvfp4(y, ids, prob, w1q, w1b, w1g, inter, divisor=k)
+    rows = b.moe_gemv_nvfp4(d, ids, w2q, w2b, w2g, H)
+    out = b.moe_combine(rows, plan["slot"])
+    return dict(out=out, h=h, y=y, ids=ids, prob=prob, d=d)
+
+
+def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: int, inter: int,
+                            loss_coef: float = 0.01, mask=None, plan=None,
+                            score: int = b.SCORE_SOFTMAX, renormalize: bool = True,
+                            scale: float = 1.0, eps: float = 1e-6):
+    """An expert layer's training forward pass from the residual stream on:
+    residual addition, RMS norm and MXFP8 encoding in one pass, router gate
+    with its balance loss, then the experts of mxfp8_moe_forward.  mask [T]
+    marks padding with 0.  Returns the experts' dict and h, y, rstd, logits,
+    ids, prob, counts, prob_sum, loss."""
+    T = x.shape[0]
+    plan = plan or block_plan(T, k, x.device)
+    qx, sx, y, h, rstd = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, keep_y=True)
+    logits = _router_logits(y, gate_w, plan["off"])
+    ids, prob, counts, prob_sum, loss = b.moe_gate(logits, k, score, renormalize, scale, mask,
+                                                   loss_coef)
+    r = _mxfp8_experts(qx, sx, ids, prob.view(-1), w1q, w1s, w2q, w2s, gate_w.shape[0], inter,
+                       True)
+    r.update(h=h, y=y, rstd=rstd, logits=logits, ids=ids, prob=prob, counts=counts,
+             prob_sum=prob_sum, loss=loss)
+    return r
+
+
+def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
+                       loss_coef: float = 0.01, mask=None, plan=None,
+                       score: int = b.SCORE_SOFTMAX, renormalize: bool = True,
+                       scale: float = 1.0):
+    """The gradients of a block's gate and norm, behind the experts' own
+    backward pass.  saved: what mxfp8_moe_block_forward returned.
+      dy [T, H] bf16     gradient of y through the experts
+      d_prob [T, k] f32  gradient of the routing probabilities
+      d_loss [1] f32     gradient of the balance loss
+      d_h [T, H] bf16    gradient of h past the norm (may be None)
+    Returns dict(dx [T, H] bf16, the gradient of x and of residual; d_norm_w
+    [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
+    T, H = dy.shape
+    E = gate_w.shape[0]
+    plan = plan or block_plan(T, saved["ids"].shape[1], dy.device)
+    off = plan["off"]
+    dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,
+                             mask, loss_coef, saved["counts"], d_loss, out_dtype=b.OUT_BF16)
+    d_gate_w = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_WGRAD, dz, saved["y"], off, E, H,
+                                  out_dtype=b.OUT_FP32)[0]
+    through_gate = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_DGRAD, dz, gate_w, off, H, E,
+                                      out_dtype=b.OUT_BF16)
+    dy = b.moe_combine(through_gate, plan["row"], shared=dy)
+    dx, d_norm_w = b.rmsnorm_backward(dy, saved["h"], norm_w, saved["rstd"], d_sum=d_h)
+    return dict(dx=dx, d_norm_w=d_norm_w, d_gate_w=d_gate_w, d_logits=dz)

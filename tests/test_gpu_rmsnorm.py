@@ -1,0 +1,195 @@
+"""RMS norm with residual and MXFP8 output, and its gradients, on the GPU
+against binary64.
+
+Bounds.  rstd: every thread adds at most 64 squares, then at most 9 joins and
+the division, square root and reciprocal; of C non-negative terms the relative
+error is at most (64 + 1 + 9) U in the mean, half of it after the root, and a
+few U more: 42 U.  y adds two products: |y - y64| <= 2^-8 |y64| + 44 U |y64|.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import operators_ref as ref
+import oracle
+import precision_quantization_moe_amd as pqm
+from gpu_util import assert_bytes_equal, host, host_u16, requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+
+def inputs(rows, cols, wf32, residual, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, cols, generator=g) * torch.exp(torch.randn(rows, 1, generator=g))
+         ).to(torch.bfloat16)
+    r = torch.randn(rows, cols, generator=g).to(torch.bfloat16) if residual else None
+    w = 1 + 0.3 * torch.randn(cols, generator=g)
+    w = w if wf32 else w.to(torch.bfloat16)
+    return x, r, w
+
+
+def cu(t):
+    return None if t is None else t.cuda()
+
+
+def check(x, r, w, eps, out):
+    q, s, y, total, rstd = out
+    want = x if r is None else (x.float() + r.float()).to(torch.bfloat16)
+    assert torch.equal(total.cpu(), want)
+    y64, r64 = ref.norm(ref.f64(want), ref.f64(w), eps)
+    assert ((ref.f64(rstd) - r64).abs() <= 42 * ref.U * r64).all()
+    if y is not None:
+        d = (ref.f64(y) - y64).abs()
+        assert (d <= (ref.HALF_BF16 + 44 * ref.U) * y64.abs() + 2.0 ** -133).all()
+        if q is not None:
+            oq, os_ = oracle.quantize_mxfp8_rowwise(host_u16(y))
+            assert_bytes_equal(host(q), oq, "q")
+            assert_bytes_equal(host(s), os_, "s")
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 32), (5, 96), (3, 512), (7, 544), (9, 1024), (33, 1056),
+                                       (6, 2048), (5, 2080), (4, 4096), (3, 4128), (131, 7168),
+                                       (2, 8192), (2, 8224), (3, 16384)])
+@pytest.mark.parametrize("wf32", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward(rows, cols, wf32, residual):
+    x, r, w = inputs(rows, cols, wf32, residual, rows * 100 + cols)
+    check(x, r, w, 1e-6, pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 1e-6, residual=cu(r),
+                                                    keep_y=True))
+
+
+def test_without_y_gives_the_same_bytes():
+    x, r, w = inputs(37, 2048, False, True, 1)
+    a = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), residual=cu(r), keep_y=True)
+    b = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), residual=cu(r))
+    assert b[2] is None
+    for i in (0, 1, 3, 4):
+        assert torch.equal(a[i], b[i]), i
+    c = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), residual=cu(r), quantize=False)
+    assert c[0] is None and c[1] is None and torch.equal(a[2], c[2])
+
+
+@pytest.mark.parametrize("cols", [8, 40, 1000, 5000])
+def test_norm_alone_takes_any_multiple_of_eight(cols):
+    x, r, w = inputs(3, cols, False, True, cols)
+    check(x, r, w, 1e-5, pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 1e-5, residual=cu(r),
+                                                    quantize=False))
+
+
+def test_row_strides_and_update_in_place():
+    x, r, w = inputs(11, 256, False, True, 2)
+    xs = torch.zeros(11, 320, dtype=torch.bfloat16).cuda()
+    xs[:, :256] = cu(x)
+    rs = torch.zeros(11, 264, dtype=torch.bfloat16).cuda()
+    rs[:, :256] = cu(r)
+    check(x, r, w, 1e-6, pqm.rmsnorm_quantize_mxfp8(xs[:, :256], cu(w), residual=rs[:, :256],
+                                                    keep_y=True))
+    mine = cu(r)
+    out = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), residual=mine, keep_y=True, inplace=True)
+    assert out[3].data_ptr() == mine.data_ptr()
+    check(x, r, w, 1e-6, out)
+    with pytest.raises(ValueError):
+        pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), residual=rs[:, :256], inplace=True)
+    with pytest.raises(ValueError):
+        pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w[:128]))
+    with pytest.raises(ValueError):
+        pqm.rmsnorm_quantize_mxfp8(cu(x).t(), cu(w))
+
+
+@pytest.mark.parametrize("cols", [96, 2048, 7168])
+def test_zero_tiny_and_huge_rows(cols):
+    """Zero rows, rows far below eps, and rows whose squares leave binary32."""
+    x, _, w = inputs(8, cols, True, False, 5)
+    w = w.abs()
+    x[0] = 0
+    x[1] = x[1] * 2.0 ** -100
+    x[2] = torch.where(x[2] < 0, -1.0, 1.0) * torch.finfo(torch.bfloat16).max
+    x[3] = torch.sign(x[3]) * 2.0 ** 64
+    x[4] = 0
+    x[4, 5] = 2.0 ** 100
+    x[5] = x[5] * 2.0 ** 60
+    out = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 1e-6, keep_y=True)
+    check(x, None, w, 1e-6, out)
+    assert not out[2][0].any() and not out[1][0].any()
+
+
+def test_no_rows():
+    x = torch.zeros(0, 64, dtype=torch.bfloat16).cuda()
+    w = torch.ones(64).cuda()
+    q, s, y, total, rstd = pqm.rmsnorm_quantize_mxfp8(x, w, keep_y=True)
+    assert q.shape == (0, 64) and s.shape == (0, 2) and rstd.numel() == 0
+    dx, dw = pqm.rmsnorm_backward(x, x, w, rstd)
+    assert dx.shape == (0, 64) and not dw.any()
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 8), (3, 96), (5, 512), (1030, 544), (33, 1024),
+                                       (2300, 2048), (3, 2056), (70, 4096), (600, 7168), (5, 8192),
+                                       (9, 16384)])
+@pytest.mark.parametrize("wf32", [False, True])
+@pytest.mark.parametrize("d_sum", [False, True])
+def test_backward(rows, cols, wf32, d_sum):
+    x, ds, w = inputs(rows, cols, wf32, d_sum, rows + cols)
+    g = torch.Generator().manual_seed(rows)
+    dy = torch.randn(rows, cols, generator=g).to(torch.bfloat16)
+    rstd = ref.norm(ref.f64(x), ref.f64(w), 1e-6)[1].float()
+    dx, dw = pqm.rmsnorm_backward(cu(dy), cu(x), cu(w), cu(rstd), d_sum=cu(ds))
+    want, want_dw, bound, size_dw = ref.norm_backward(
+        ref.f64(dy), ref.f64(x), ref.f64(w), ref.f64(rstd), None if ds is None else ref.f64(ds))
+    assert ((ref.f64(dx) - want).abs() <= ref.HALF_BF16 * want.abs() + bound).all()
+    # dw: two roundings a term, rows additions in whatever order
+    assert ((ref.f64(dw) - want_dw).abs() <= (rows + 3) * ref.U * size_dw).all()
+    again = pqm.rmsnorm_backward(cu(dy), cu(x), cu(w), cu(rstd), d_sum=cu(ds))
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def test_backward_follows_the_forward_pass_along_directions():
+    """The kernel's gradients against differences of the binary64 objective
+    sum(y dy) + sum(x ds) along random directions."""
+    x, ds, w = inputs(64, 1024, True, True, 9)
+    g = torch.Generator().manual_seed(9)
+    dy = torch.randn(64, 1024, generator=g).to(torch.bfloat16)
+    _, _, _, total, rstd = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 1e-3, keep_y=True)
+    dx, dw = pqm.rmsnorm_backward(cu(dy), total, cu(w), rstd, d_sum=cu(ds))
+    x64, w64 = ref.f64(x), ref.f64(w)
+
+    def objective(a, b):
+        return (ref.norm(a, b, 1e-3)[0] * ref.f64(dy)).sum() + (a * ref.f64(ds)).sum()
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed)
+        vx = torch.randn(64, 1024, generator=g, dtype=torch.float64)
+        vw = torch.randn(1024, generator=g, dtype=torch.float64)
+        h = 1e-5
+        diff = (objective(x64 + h * vx, w64 + h * vw) - objective(x64 - h * vx, w64 - h * vw)) / (2 * h)
+        got = (ref.f64(dx) * vx).sum() + (ref.f64(dw) * vw).sum()
+        # dx is rounded to bf16: at most half a step of each product
+        bound = ref.HALF_BF16 * (ref.f64(dx) * vx).abs().sum()
+        assert abs(float(got - diff)) <= float(bound)
+
+
+def test_other_stream_and_graph_replay():
+    x, r, w = inputs(64, 2048, False, True, 12)
+    xg, rg, wg = cu(x), cu(r), cu(w)
+    dy = torch.randn(64, 2048).to(torch.bfloat16).cuda()
+    want = pqm.rmsnorm_quantize_mxfp8(xg, wg, residual=rg, keep_y=True)
+    want_b = pqm.rmsnorm_backward(dy, want[3], wg, want[4], d_sum=rg)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = pqm.rmsnorm_quantize_mxfp8(xg, wg, residual=rg, keep_y=True)
+        got_b = pqm.rmsnorm_backward(dy, got[3], wg, got[4], d_sum=rg)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want + want_b, got + got_b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pqm.rmsnorm_quantize_mxfp8(xg, wg, residual=rg, keep_y=True)
+        out_b = pqm.rmsnorm_backward(dy, out[3], wg, out[4], d_sum=rg)
+    for i in range(3):
+        for t in out + out_b:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want + want_b, out + out_b)), i
+        pqm.rmsnorm_backward(dy, want[3], wg, want[4])
+        torch.cuda.synchronize()
