@@ -668,8 +668,11 @@ pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, con
  * With topk_ids [T, k] as ids: divisor = k for the first projection (x holds
  * the tokens), 1 for the second (x holds one row per assignment).  Any order
  * and any repetition of ids is legal; a row whose id lies outside [0, G) gives
- * zeros.  The operand values are exact, sums are binary32, the outer scale is
- * applied to the sum.  Nothing may overlap out.
+ * zeros.  Sums are binary32, the outer scale is applied to the sum.  The
+ * weights are exact; so are x's values down to 2^-31 of the largest of their
+ * row, and smaller ones are off by less than 2^-38 of that largest value (large
+ * calls hold x in scaled binary16).  A row's result depends on its own x and
+ * on the call's sizes alone.  Nothing may overlap out.
  * Requires rows <= 4096 (more: pqm_moe_route and pqm_moe_grouped_gemm),
  * 1 <= divisor <= 4096, 1 <= G <= 4096, N <= 2^20, K % 32 == 0, 32 <= K <=
  * 2^20, w_rows_per_scale >= 1 dividing G N (PQM_ERR_SHAPE); x, w_q and out

@@ -83,6 +83,59 @@ def test_swiglu(T, k, G, I, K):
     check_act(acts(T, K, I + K), ids, prob, weights(G, 2 * I, K, K), I, k)
 
 
+# N / 128 (swiglu: / 64) tiles times min(rows, G) reach 160 workgroups here: the
+# kernel that stages x, with one to four rows a wave, blocks and turns of
+# scales cut short (K % 512, K % 1024) and ragged tiles
+@pytest.mark.parametrize("T,k,G,N,K", [(40, 1, 40, 520, 64), (41, 4, 41, 500, 448), (24, 8, 8, 2600, 576),
+                                       (400, 1, 40, 513, 1088), (1, 8, 9, 2561, 2304),
+                                       (170, 3, 160, 20, 1024)])
+def test_many_workgroups(T, k, G, N, K):
+    g = torch.Generator().manual_seed(T + N)
+    ids = torch.randint(-1, G, (T, k), generator=g, dtype=torch.int32)
+    w = weights(G, N, K, K)
+    check_plain(acts(T, K, N + K), ids, w, N, k)
+    check_plain(acts(T * k, K, N + K), ids, w, N, 1)
+
+
+@pytest.mark.parametrize("T,k,G,I,K", [(40, 1, 40, 260, 64), (41, 4, 41, 250, 448), (60, 8, 16, 700, 1600)])
+def test_many_workgroups_swiglu(T, k, G, I, K):
+    g = torch.Generator().manual_seed(T + I)
+    ids = torch.randint(0, G, (T, k), generator=g, dtype=torch.int32)
+    check_act(acts(T, K, I + K), ids, torch.rand(T, k, generator=g), weights(G, 2 * I, K, K), I, k)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "spikes", "tiny", "zero"])
+def test_rows_of_wide_range(order):
+    """x whose magnitude changes by 2^60 along the row, in both kernels: what a
+    scaled binary16 loses is bounded by 2^-38 of the row's largest value."""
+    for G, N in ((3, 20), (40, 640)):
+        K, rows = 2048, 45
+        ids = torch.arange(rows, dtype=torch.int32) % G
+        g = torch.Generator().manual_seed(7)
+        x = torch.randn(rows, K, generator=g)
+        step = torch.linspace(-30, 30, K)
+        if order == "rising":
+            x = x * torch.exp2(step)
+        elif order == "falling":
+            x = x * torch.exp2(-step)
+        elif order == "spikes":
+            x[:, 1000::700] *= 2.0 ** 40
+        elif order == "tiny":
+            x = x * 2.0 ** -120
+        else:
+            x[::2] = 0
+        x = x.to(torch.bfloat16)
+        q, sb, sg, rps = weights(G, N, K, 7)
+        want, size = ref.gemv(x, ids, q, sb, sg, N, rps, 1)
+        top = ref.f64(x).abs().amax(1, keepdim=True)
+        ones = torch.ones(rows, K, dtype=torch.bfloat16)
+        # sum of |w|: the size of a product with ones
+        weight = ref.gemv(ones, ids, q, sb, sg, N, rps, 1)[1]
+        got = run_plain(x, ids, (q, sb, sg, rps), N)
+        bound = ref.gemv_bound(size, K) + 2.0 ** -38 * top * weight + 2.0 ** -149
+        assert ((ref.f64(got) - want).abs() <= bound).all()
+
+
 def test_large_gates_do_not_overflow():
     q, sb, sg, rps = weights(2, 64, 256, 3)
     x = acts(4, 256, 4) * 3000
@@ -125,28 +178,35 @@ def test_most_rows_that_are_taken():
     check_plain(acts(4096, 64, 1), ids, weights(6, 16, 64, 1), 16)
 
 
-def test_a_row_depends_on_its_own_values_alone():
+@pytest.mark.parametrize("N", [32, 7000])
+def test_a_row_depends_on_its_own_values_alone(N):
     """NaN and infinities in one row of x stay in the rows computed from it."""
     ids = torch.tensor([2, 2, 2, 1, 2], dtype=torch.int32)
     x = acts(5, 128, 2)
-    w = weights(3, 32, 128, 2)
-    want = run_plain(x, ids, w, 32)
+    w = weights(3, N, 128, 2)
+    want = run_plain(x, ids, w, N)
     bad = x.clone()
     bad[1] = float("nan")
     bad[3, 7] = float("inf")
-    got = run_plain(bad, ids, w, 32)
+    got = run_plain(bad, ids, w, N)
     keep = [0, 2, 4]
     assert torch.equal(got[keep], want[keep])
     assert not torch.isfinite(got[1]).any()
 
 
-def test_same_result_whatever_else_is_in_the_batch():
-    w = weights(20, 96, 256, 5)
+@pytest.mark.parametrize("N", [96, 2050])
+def test_same_result_whatever_else_is_in_the_batch(N):
+    """The same number of rows, the others' experts and values changed."""
+    w = weights(20, N, 256, 5)
     x = acts(30, 256, 5)
-    ids = torch.randint(0, 20, (30,), generator=torch.Generator().manual_seed(5), dtype=torch.int32)
-    whole = run_plain(x, ids, w, 96)
+    g = torch.Generator().manual_seed(5)
+    ids = torch.randint(0, 20, (30,), generator=g, dtype=torch.int32)
+    whole = run_plain(x, ids, w, N)
     for r in (0, 7, 29):
-        assert torch.equal(run_plain(x[r:r + 1], ids[r:r + 1], w, 96)[0], whole[r])
+        other, elsewhere = acts(30, 256, r + 50) * 1000, torch.randint(-1, 20, (30,), generator=g,
+                                                                        dtype=torch.int32)
+        other[r], elsewhere[r] = x[r], ids[r]
+        assert torch.equal(run_plain(other, elsewhere, w, N)[r], whole[r])
 
 
 def test_nothing_behind_the_rows_is_written():
