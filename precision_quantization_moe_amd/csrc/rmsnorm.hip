@@ -19,6 +19,8 @@ namespace pqm {
 
 namespace {
 
+typedef uint32_t nb_u4 __attribute__((ext_vector_type(4)));
+
 // 8 weights from column c on, as binary32.
 template <bool WF32>
 __device__ __forceinline__ void load_w8(const void *__restrict__ w, int64_t c, float (&o)[8]) {
@@ -61,6 +63,8 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // One row per TPR threads, NC chunks of 8 values per thread, kept in registers
 // between the sum of squares and the scaling, so each input is read once.
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
+// Bound by memory: 16384 x 2048 with residual, 235 MB, 44 us (5.4 TB/s); 8 x
+// 2048 takes 4.7 us, the time of a launch.
 template <int TPR, int NC, bool WF32>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
@@ -150,74 +154,112 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
   }
 }
 
-// Gradients.  A workgroup takes rows blockIdx.x, + gridDim.x, ... (4 at a time
-// with one wave a row); a thread owns the same columns of every row, so dw's
-// sums stay in registers and leave once, as the workgroup's row of `part`.
+// Gradients.  One workgroup a CU takes rows blockIdx.x, + gridDim.x, ... (four
+// at a time with one wave a row); a thread owns the same columns of every row,
+// so dw's sums and the weights stay in registers, and the sums leave once, as
+// the workgroup's row of `part`.  The next row's loads go out before the
+// current row is reduced.  Rows are read and written as buffers of their own
+// length: past their end reads give 0 and writes are dropped, and a row that
+// is none is an empty buffer.
+//
+// Bound by memory: 16384 x 2048 with d_sum, 268 MB, 49 us with k_rmsnorm_dw's 4
+// (5.5 TB/s; a copy here moves 5.1).  70 us without the next row in flight and
+// with weights read again for every row; two workgroups a CU, whose sums are
+// twice the bytes, 51.  1021 x 7168: 18 us, half of it the start of two
+// kernels and their sums of dw.
 template <int TPR, int NC, bool WF32>
-__global__ __launch_bounds__(256) void k_rmsnorm_backward(
+__global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
     const uint16_t *__restrict__ dy, const uint16_t *__restrict__ sx, const void *__restrict__ w,
     const float *__restrict__ rstd, const uint16_t *dsum, int64_t rows, int64_t C, uint16_t *dx,
     float *__restrict__ part) {
-  constexpr int RPB = 256 / TPR;
+  constexpr int RPB = TPR == 64 ? 4 : 1, WAVES = TPR == 512 ? 8 : 4;
   extern __shared__ float lds[];  // [4][C] with one wave a row
-  __shared__ float red[4];
-  const int l = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  __shared__ float red[2][WAVES];
+  const int l = threadIdx.x % TPR;
+  const int sub = RPB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const int step = (int)gridDim.x * RPB;
+  struct Row {
+    nb_u4 g[NC], s[NC], d[NC];
+    float rs;
+  };
+  const auto buffer = [&](const uint16_t *p, int row) {
+    const bool in = p && row < rows;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p) + (in ? row * C : 0), (short)0,
+                                             in ? (int)(2 * C) : 0, 0x00020000);
+  };
+  const auto load = [&](Row &r, int row) {
+    const __amdgpu_buffer_rsrc_t g = buffer(dy, row), s = buffer(sx, row), d = buffer(dsum, row);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int o = (i * TPR + l) * 16;
+      r.g[i] = __builtin_amdgcn_raw_buffer_load_b128(g, o, 0, 0);
+      r.s[i] = __builtin_amdgcn_raw_buffer_load_b128(s, o, 0, 0);
+      r.d[i] = __builtin_amdgcn_raw_buffer_load_b128(d, o, 0, 0);
+    }
+    r.rs = row < rows ? rstd[row] : 0.0f;
+  };
+  // the weights of this thread's columns, kept as they are stored
+  const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void *>(w), (short)0, (int)(C * (WF32 ? 4 : 2)), 0x00020000);
+  nb_u4 wr[NC][WF32 ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int h = 0; h < (WF32 ? 2 : 1); ++h)
+      wr[i][h] = __builtin_amdgcn_raw_buffer_load_b128(wb, (i * TPR + l) * (WF32 ? 32 : 16) + 16 * h,
+                                                       0, 0);
+  const auto weight = [&](int i, int j) {
+    if constexpr (WF32) return __uint_as_float(wr[i][j / 4][j % 4]);
+    else return j & 1 ? bf16_hi_f32(wr[i][0][j / 2]) : bf16_lo_f32(wr[i][0][j / 2]);
+  };
   float acc[NC][8] = {};
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t row = r0 + sub;
-    const bool live = row < rows;
-    const float rs = live ? rstd[row] : 0.0f;
-    uint4 gv[NC], sv[NC];
+  const auto use = [&](const Row &r, int row, int turn) {
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = ((int64_t)i * TPR + l) * 8;
-      gv[i] = sv[i] = make_uint4(0, 0, 0, 0);
-      if (live && c < C) {
-        gv[i] = *reinterpret_cast<const uint4 *>(dy + row * C + c);
-        sv[i] = *reinterpret_cast<const uint4 *>(sx + row * C + c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int64_t c = ((int64_t)i * TPR + l) * 8;
-      if (c >= C) continue;
-      float wf[8];
-      load_w8<WF32>(w, c, wf);
-      const uint32_t gu[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
-      const uint32_t su[4] = {sv[i].x, sv[i].y, sv[i].z, sv[i].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = j & 1 ? bf16_hi_f32(gu[j / 2]) : bf16_lo_f32(gu[j / 2]);
-        const float h = (j & 1 ? bf16_hi_f32(su[j / 2]) : bf16_lo_f32(su[j / 2])) * rs;
+        const float d = j & 1 ? bf16_hi_f32(r.g[i][j / 2]) : bf16_lo_f32(r.g[i][j / 2]);
+        const float h = (j & 1 ? bf16_hi_f32(r.s[i][j / 2]) : bf16_lo_f32(r.s[i][j / 2])) * r.rs;
         const float t = d * h;
         acc[i][j] += t;
-        dot += t * wf[j];
+        dot += t * weight(i, j);
       }
     }
-    const float m = row_sum<TPR>(dot, red) / (float)C;
+    dot = wave_sum(dot);
+    if constexpr (TPR != 64) {  // two sets of slots: one barrier a row
+      if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = dot;
+      __syncthreads();
+      dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) dot += red[turn][i];
+    }
+    const float m = dot / (float)C;
+    const __amdgpu_buffer_rsrc_t out = buffer(dx, row);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t c = ((int64_t)i * TPR + l) * 8;
-      if (!live || c >= C) continue;
-      float wf[8];
-      load_w8<WF32>(w, c, wf);
-      const uint32_t gu[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
-      const uint32_t su[4] = {sv[i].x, sv[i].y, sv[i].z, sv[i].w};
-      uint4 dv = make_uint4(0, 0, 0, 0);
-      if (dsum) dv = *reinterpret_cast<const uint4 *>(dsum + row * C + c);
-      const uint32_t du[4] = {dv.x, dv.y, dv.z, dv.w};
-      uint32_t o[4];
+      nb_u4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float lo = rs * (bf16_lo_f32(gu[j]) * wf[2 * j] - bf16_lo_f32(su[j]) * rs * m);
-        const float hi = rs * (bf16_hi_f32(gu[j]) * wf[2 * j + 1] - bf16_hi_f32(su[j]) * rs * m);
-        o[j] = pk_bf16_rne(lo + bf16_lo_f32(du[j]), hi + bf16_hi_f32(du[j]));
+        const float lo = r.rs * (bf16_lo_f32(r.g[i][j]) * weight(i, 2 * j) - bf16_lo_f32(r.s[i][j]) * r.rs * m);
+        const float hi =
+            r.rs * (bf16_hi_f32(r.g[i][j]) * weight(i, 2 * j + 1) - bf16_hi_f32(r.s[i][j]) * r.rs * m);
+        o[j] = pk_bf16_rne(lo + bf16_lo_f32(r.d[i][j]), hi + bf16_hi_f32(r.d[i][j]));
       }
-      *reinterpret_cast<uint4 *>(dx + row * C + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      __builtin_amdgcn_raw_buffer_store_b128(o, out, (i * TPR + l) * 16, 0, 0);
     }
+  };
+  const int first = (int)blockIdx.x * RPB;  // every wave takes the same turns
+  Row a, b;
+  load(a, first + sub);
+  for (int r0 = first; r0 < rows; r0 += 2 * step) {
+    load(b, r0 + step + sub);
+    use(a, r0 + sub, 0);
+    if (r0 + step >= rows) break;
+    load(a, r0 + 2 * step + sub);
+    use(b, r0 + step + sub, 1);
   }
-  if constexpr (TPR == 256) {
+  if constexpr (TPR != 64) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int64_t c = ((int64_t)i * TPR + l) * 8;
@@ -241,24 +283,30 @@ __global__ __launch_bounds__(256) void k_rmsnorm_backward(
   }
 }
 
-// dw = sum of the P rows of part, always in the same order: 16 columns x 16
-// row groups a workgroup, the groups' sums joined through LDS.
-__global__ __launch_bounds__(256) void k_rmsnorm_dw(const float *__restrict__ part, int64_t P,
-                                                    int64_t C, float *__restrict__ dw) {
-  __shared__ float sh[16][17];
+// dw = sum of the P rows of part, always in the same order: 16 columns x 64
+// row groups a workgroup, eight rows of a group in flight, the groups' sums
+// joined through LDS.
+__global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float *__restrict__ part, int64_t P,
+                                                     int64_t C, float *__restrict__ dw) {
+  __shared__ float sh[64][17];
   const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + col;
-  float a = 0.0f;
+  float a[8] = {};
   if (c < C)
-    for (int64_t p = grp; p < P; p += 16) a += part[p * C + c];
-  sh[grp][col] = a;
-  __syncthreads();
-  if (grp == 0 && c < C) {
-    float t = 0.0f;
+    for (int64_t p0 = grp; p0 < P; p0 += 512) {
 #pragma unroll
-    for (int g = 0; g < 16; ++g) t += sh[g][col];
-    dw[c] = t;
+      for (int i = 0; i < 8; ++i) {
+        const int64_t p = p0 + 64 * i;
+        a[i] += p < P ? part[p * C + c] : 0.0f;
+      }
+    }
+  sh[grp][col] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+  __syncthreads();
+  for (int w = 32; w > 0; w >>= 1) {
+    if (grp < w) sh[grp][col] += sh[grp + w][col];
+    __syncthreads();
   }
+  if (grp == 0 && c < C) dw[c] = sh[0][col];
 }
 
 namespace {
@@ -269,7 +317,7 @@ constexpr int64_t NORM_MAX_COLS = 16384;  // 8 chunks of 8 values for each of 25
 int64_t norm_backward_groups(int64_t rows, int64_t C) {
   const int64_t per = C <= 2048 ? 4 : 1;
   const int64_t g = (rows + per - 1) / per;
-  return g < 512 ? g : 512;
+  return g < 256 ? g : 256;
 }
 
 template <int TPR, int NC>
@@ -292,18 +340,22 @@ hipError_t go_back(bool wf32, const uint16_t *dy, const uint16_t *x, const void 
                    float *part, hipStream_t st) {
   const dim3 grid((unsigned)norm_backward_groups(rows, C));
   const size_t lds = TPR == 64 ? 4 * C * sizeof(float) : 0;
+  const dim3 block(TPR == 512 ? 512 : 256);
   if (wf32)
-    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, true>), grid, dim3(256), lds, st, dy, x, w,
+    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, true>), grid, block, lds, st, dy, x, w,
                        rstd, dsum, rows, C, dx, part);
   else
-    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, false>), grid, dim3(256), lds, st, dy, x, w,
+    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, false>), grid, block, lds, st, dy, x, w,
                        rstd, dsum, rows, C, dx, part);
   return hipGetLastError();
 }
 
 // One wave a row up to 2048 columns (no barrier between a row's sum and its
 // use), the workgroup a row beyond (a wave would hold over 32 values a lane
-// of each tensor).
+// of each tensor).  The gradients hold two rows of three tensors, the weights
+// and dw's sums: at most four chunks a thread, hence 512 threads from 4097
+// columns on (1021 x 7168: 18.0 us, with 256 threads 17.9; 16384 columns
+// would spill 124 registers).
 #define PQM_NORM_PICK(FN, ...)                               \
   (C <= 512     ? FN<64, 1>(__VA_ARGS__)                     \
    : C <= 1024  ? FN<64, 2>(__VA_ARGS__)                     \
@@ -311,6 +363,13 @@ hipError_t go_back(bool wf32, const uint16_t *dy, const uint16_t *x, const void 
    : C <= 4096  ? FN<256, 2>(__VA_ARGS__)                    \
    : C <= 8192  ? FN<256, 4>(__VA_ARGS__)                    \
                 : FN<256, 8>(__VA_ARGS__))
+#define PQM_NORM_BACK_PICK(FN, ...)                          \
+  (C <= 512     ? FN<64, 1>(__VA_ARGS__)                     \
+   : C <= 1024  ? FN<64, 2>(__VA_ARGS__)                     \
+   : C <= 2048  ? FN<64, 4>(__VA_ARGS__)                     \
+   : C <= 4096  ? FN<256, 2>(__VA_ARGS__)                    \
+   : C <= 8192  ? FN<512, 2>(__VA_ARGS__)                    \
+                : FN<512, 4>(__VA_ARGS__))
 
 bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; }
@@ -366,12 +425,12 @@ pqm_status pqm_rmsnorm_backward(const uint16_t *dy, const uint16_t *x, const voi
   const int64_t C = cols;
   float *part = static_cast<float *>(workspace);
   if (rows > 0) {
-    const hipError_t e = PQM_NORM_PICK(go_back, weight_dtype == PQM_OUT_FP32, dy, x, weight, rstd,
+    const hipError_t e = PQM_NORM_BACK_PICK(go_back, weight_dtype == PQM_OUT_FP32, dy, x, weight, rstd,
                                        d_sum, rows, C, dx, part, stream);
     if (e != hipSuccess) return PQM_ERR_HIP;
   }
   // no rows: the sum over none of them is zero
-  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((C + 15) / 16)), dim3(256), 0, stream, part,
+  hipLaunchKernelGGL(k_rmsnorm_dw, dim3((unsigned)((C + 15) / 16)), dim3(1024), 0, stream, part,
                      rows > 0 ? norm_backward_groups(rows, C) : 0, C, dweight);
   return st_of(hipGetLastError());
 }
