@@ -16,6 +16,8 @@
 #include "pqm_internal.hpp"
 #include "pqmoe.h"
 
+#include <type_traits>
+
 namespace pqm {
 
 namespace {
@@ -24,24 +26,58 @@ constexpr int GATE_MAX_EXPERTS = 1024;
 constexpr int GATE_MAX_K = 16;
 constexpr int64_t GATE_GROUPS = 256;  // workgroups whose partial sums the last kernel joins
 
-// Reductions over the LPT lanes (16 or 64) that hold one token.
+template <int J>
+using lane_c = std::integral_constant<int, J>;
+
+template <typename F>
+__device__ __forceinline__ uint32_t dpp_step(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // lane ^ 1
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // lane ^ 2
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // 7 - lane
+  return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // 15 - lane
+}
+
+// Reductions over the LPT lanes (16, a DPP row, or 64) that hold one token, the
+// result in all of them.  Through the vector unit alone: with shuffles, which
+// pass through LDS, a choice of 8 among 256 took 8 us for 16 tokens, most of
+// it their latency.
+template <int LPT, typename F>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
+  v = dpp_step(v, f);
+  if constexpr (LPT == 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = f(b[0], b[1]);
+  }
+  return v;
+}
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return __uint_as_float(group_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int LPT>
+__device__ __forceinline__ float group_fmax(float v) {
+  return __uint_as_float(group_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
 }
 template <int LPT>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-  return v;
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int LPT>
-__device__ __forceinline__ int group_min(int v) {
-#pragma unroll
-  for (int o = LPT / 2; o >= 1; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
-  return v;
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
+// The value of the group's lane J in all its lanes.
+template <int LPT, int J>
+__device__ __forceinline__ uint32_t group_lane(uint32_t v) {
+  if constexpr (LPT == 64) return (uint32_t)__builtin_amdgcn_readlane((int)v, J);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xF, 0xF, false);
 }
 
 template <bool ZF32>
@@ -69,16 +105,18 @@ __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-
 // workgroup also leaves its counts and share sums in part_cnt / part_sum
 // [gridDim.x][E] (and its valid tokens in part_valid).
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
-__global__ __launch_bounds__(512) void k_moe_gate(
+__global__ __launch_bounds__(1024) void k_moe_gate(
     const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
     int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ prob,
-    int32_t *__restrict__ part_cnt, float *__restrict__ part_sum, int32_t *__restrict__ part_valid) {
+    int32_t *__restrict__ part_cnt, float *__restrict__ part_sum, int32_t *__restrict__ part_valid,
+    uint32_t *__restrict__ ticket) {
   extern __shared__ int32_t sh[];  // SUMS: counts [E], share sums [waves][E]
   const int l = threadIdx.x % LPT;
   const int groups = blockDim.x / LPT;
   float acc[VPL] = {};
   int nvalid = 0;
   if constexpr (SUMS) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;  // for k_moe_balance
     for (int e = threadIdx.x; e < E; e += blockDim.x) sh[e] = 0;
     __syncthreads();
   }
@@ -102,15 +140,15 @@ __global__ __launch_bounds__(512) void k_moe_gate(
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = max(m, key[i]);
       m = group_max<LPT>(m);
-      int at = INT32_MAX;
+      uint32_t at = UINT32_MAX;
 #pragma unroll
-      for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? i * LPT + l : at;
+      for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)(i * LPT + l) : at;
       at = group_min<LPT>(at);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = i * LPT + l == at ? 0u : key[i];
+      for (int i = 0; i < VPL; ++i) key[i] = (uint32_t)(i * LPT + l) == at ? 0u : key[i];
       if (j == 0) top = key_logit(m);
       if (l == j) {
-        my_id = at;
+        my_id = (int)at;
         my_z = key_logit(m);
       }
     }
@@ -176,57 +214,75 @@ __global__ __launch_bounds__(512) void k_moe_gate(
   }
 }
 
-// One workgroup joins the P workgroups' sums, in a fixed order, and forms the
-// loss.  256 threads a column group: 4 row groups of 256 columns.
+// Joins the P workgroups' sums, 32 columns a workgroup (32 row groups of them,
+// eight rows of a group in flight), and forms the loss: each workgroup leaves
+// its columns' part, and the one that draws the last ticket adds the parts.
+// Every sum has one order, whichever workgroup comes last.
 __global__ __launch_bounds__(1024) void k_moe_balance(
     const int32_t *__restrict__ part_cnt, const float *__restrict__ part_sum,
-    const int32_t *__restrict__ part_valid, int P, int E, int k, float coef,
-    int32_t *__restrict__ counts, float *__restrict__ prob_sum, float *__restrict__ loss) {
-  __shared__ float fs[1024];
-  __shared__ int32_t is[1024];
-  int nv = 0;
-  for (int p = threadIdx.x; p < P; p += 1024) nv += part_valid[p];
-  is[threadIdx.x] = nv;
-  __syncthreads();
-  for (int w = 512; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) is[threadIdx.x] += is[threadIdx.x + w];
-    __syncthreads();
+    const int32_t *__restrict__ part_valid, int P, int E, int k, float coef, float *part_dot,
+    uint32_t *ticket, int32_t *__restrict__ counts, float *__restrict__ prob_sum,
+    float *__restrict__ loss) {
+  __shared__ float fs[32][33];
+  __shared__ int32_t is[32][33], vs[16];
+  __shared__ bool last;
+  const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + col;
+  float s = 0.0f;
+  int c = 0, nv = 0;
+  for (int p0 = grp; p0 < P; p0 += 256) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + 32 * i;
+      const bool in = p < P && e < E;
+      s += in ? part_sum[(int64_t)p * E + e] : 0.0f;
+      c += in ? part_cnt[(int64_t)p * E + e] : 0;
+    }
   }
-  const int valid = is[0];
+  for (int p = threadIdx.x; p < P; p += 1024) nv += part_valid[p];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) nv += __shfl_xor(nv, o, 64);
+  if ((threadIdx.x & 63) == 0) vs[threadIdx.x >> 6] = nv;
+  fs[grp][col] = s;
+  is[grp][col] = c;
   __syncthreads();
-  const int col = threadIdx.x & 255, grp = threadIdx.x >> 8;
-  float dot = 0.0f;
-  for (int e0 = 0; e0 < E; e0 += 256) {
-    const int e = e0 + col;
-    float s = 0.0f;
-    int c = 0;
-    if (e < E)
-      for (int p = grp; p < P; p += 4) {
-        s += part_sum[(int64_t)p * E + e];
-        c += part_cnt[(int64_t)p * E + e];
-      }
-    fs[threadIdx.x] = s;
-    is[threadIdx.x] = c;
-    __syncthreads();
-    if (grp == 0 && e < E) {
-      s = (fs[col] + fs[col + 256]) + (fs[col + 512] + fs[col + 768]);
-      c = is[col] + is[col + 256] + is[col + 512] + is[col + 768];
-      prob_sum[e] = s;
-      counts[e] = c;
-      // the share of the assignments times the mean share of the probability
-      if (valid) dot += (float)c / ((float)k * (float)valid) * (s / (float)valid);
+  for (int w = 16; w > 0; w >>= 1) {
+    if (grp < w) {
+      fs[grp][col] += fs[grp + w][col];
+      is[grp][col] += is[grp + w][col];
     }
     __syncthreads();
   }
-  fs[threadIdx.x] = dot;
-  __syncthreads();
-  for (int w = 512; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) fs[threadIdx.x] += fs[threadIdx.x + w];
-    __syncthreads();
+  int valid = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) valid += vs[w];
+  if (threadIdx.x < 64) {
+    float dot = 0.0f;
+    if (threadIdx.x < 32 && e < E) {
+      s = fs[0][col];
+      c = is[0][col];
+      prob_sum[e] = s;
+      counts[e] = c;
+      // the share of the assignments times the mean share of the probability
+      if (valid) dot = (float)c / ((float)k * (float)valid) * (s / (float)valid);
+    }
+    dot = group_sum<64>(dot);
+    if (threadIdx.x == 0) {
+      __hip_atomic_store(&part_dot[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             gridDim.x - 1;
+    }
   }
+  __syncthreads();
+  if (!last || threadIdx.x >= 64) return;
+  float dot = threadIdx.x < gridDim.x  // at most 32 workgroups
+                  ? __hip_atomic_load(&part_dot[threadIdx.x], __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT)
+                  : 0.0f;
+  dot = group_sum<64>(dot);
   if (threadIdx.x == 0) {
     counts[E] = valid;
-    loss[0] = coef * (float)E * fs[0];
+    loss[0] = coef * (float)E * dot;
   }
 }
 
@@ -238,7 +294,6 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     const float *__restrict__ d_loss, void *__restrict__ d_z, int out_f32) {
   const int l = threadIdx.x % LPT;
   constexpr int groups = 256 / LPT;
-  const int base = (threadIdx.x & 63) / LPT * LPT;  // the token's first lane in its wave
   float h[VPL];
   float hc = 0.0f;
   if (counts && counts[E] > 0) {
@@ -273,8 +328,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       }
     }
     if constexpr (SOFTMAX) {
-#pragma unroll
-      for (int o = LPT / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      top = group_fmax<LPT>(top);
       if (!(top > -__builtin_inff())) top = 0.0f;
     }
     float sum = 0.0f;
@@ -299,11 +353,18 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       my_d = (my_d - dot * it) * it;
     }
     float u[VPL] = {};
-    for (int j = 0; j < k; ++j) {
-      const int id = __shfl(my_id, base + j, 64);
-      const float d = __shfl(my_d, base + j, 64);
+    const auto add = [&](auto j) {
+      if (decltype(j)::value >= k) return;  // the same for every lane
+      const int id = (int)group_lane<LPT, decltype(j)::value>((uint32_t)my_id);
+      const float d = __uint_as_float(group_lane<LPT, decltype(j)::value>(__float_as_uint(my_d)));
 #pragma unroll
       for (int i = 0; i < VPL; ++i) u[i] += i * LPT + l == id ? d : 0.0f;
+    };
+    add(lane_c<0>{}); add(lane_c<1>{}); add(lane_c<2>{}); add(lane_c<3>{});
+    add(lane_c<4>{}); add(lane_c<5>{}); add(lane_c<6>{}); add(lane_c<7>{});
+    if (k > 8) {
+      add(lane_c<8>{}); add(lane_c<9>{}); add(lane_c<10>{}); add(lane_c<11>{});
+      add(lane_c<12>{}); add(lane_c<13>{}); add(lane_c<14>{}); add(lane_c<15>{});
     }
     float dot = 0.0f;  // softmax: sum p (u + h); sigmoid: sum p h
 #pragma unroll
@@ -325,15 +386,19 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
 
 namespace {
 
+// Threads of a workgroup that leaves sums: their shares in LDS, one row of E a
+// wave, stay under 64 KB.
+int gate_block(int64_t E) { return E <= 512 ? 1024 : 512; }
+
 int64_t gate_groups(int64_t T, int64_t E) {
-  const int64_t per = 512 / (E <= 256 ? 16 : 64);
+  const int64_t per = gate_block(E) / (E <= 256 ? 16 : 64);
   const int64_t g = (T + per - 1) / per;
   return g < 1 ? 1 : g < GATE_GROUPS ? g : GATE_GROUPS;
 }
 
 size_t gate_workspace_bytes(int64_t T, int64_t E) {
   const int64_t P = gate_groups(T, E);
-  return (size_t)(P * E * 8 + P * 4);
+  return (size_t)(P * E * 8 + P * 4 + 33 * 4);  // and the loss's parts and ticket
 }
 
 struct GateArgs {
@@ -358,16 +423,21 @@ hipError_t go_gate(const GateArgs &a) {
     const int64_t per = 256 / LPT, g = (a.T + per - 1) / per;
     hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, false>), dim3((unsigned)g), dim3(256),
                        0, a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob,
-                       (int32_t *)nullptr, (float *)nullptr, (int32_t *)nullptr);
+                       (int32_t *)nullptr, (float *)nullptr, (int32_t *)nullptr,
+                       (uint32_t *)nullptr);
     return hipGetLastError();
   }
   float *ps = static_cast<float *>(a.ws);
   int32_t *pc = reinterpret_cast<int32_t *>(ps + P * a.E), *pv = pc + P * a.E;
-  const size_t lds = (size_t)(a.E * 9 + 8) * 4;
-  hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, true>), dim3((unsigned)P), dim3(512), lds,
-                     a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob, pc, ps, pv);
-  hipLaunchKernelGGL(k_moe_balance, dim3(1), dim3(1024), 0, a.st, pc, ps, pv, (int)P, a.E, a.k,
-                     a.coef, a.counts, a.prob_sum, a.loss);
+  float *pd = reinterpret_cast<float *>(pv + P);
+  uint32_t *ticket = reinterpret_cast<uint32_t *>(pd + 32);
+  const int block = gate_block(a.E), waves = block / 64;
+  const size_t lds = (size_t)(a.E * (1 + waves) + waves) * 4;
+  hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, true>), dim3((unsigned)P), dim3(block),
+                     lds, a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob, pc, ps,
+                     pv, ticket);
+  hipLaunchKernelGGL(k_moe_balance, dim3((a.E + 31) / 32), dim3(1024), 0, a.st, pc, ps, pv, (int)P,
+                     a.E, a.k, a.coef, pd, ticket, a.counts, a.prob_sum, a.loss);
   return hipGetLastError();
 }
 

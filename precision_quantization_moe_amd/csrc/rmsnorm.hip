@@ -177,17 +177,17 @@ __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
   __shared__ float red[2][WAVES];
   const int l = threadIdx.x % TPR;
   const int sub = RPB == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-  const int step = (int)gridDim.x * RPB;
+  const int64_t step = (int64_t)gridDim.x * RPB;
   struct Row {
     nb_u4 g[NC], s[NC], d[NC];
     float rs;
   };
-  const auto buffer = [&](const uint16_t *p, int row) {
+  const auto buffer = [&](const uint16_t *p, int64_t row) {
     const bool in = p && row < rows;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p) + (in ? row * C : 0), (short)0,
                                              in ? (int)(2 * C) : 0, 0x00020000);
   };
-  const auto load = [&](Row &r, int row) {
+  const auto load = [&](Row &r, int64_t row) {
     const __amdgpu_buffer_rsrc_t g = buffer(dy, row), s = buffer(sx, row), d = buffer(dsum, row);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
     else return j & 1 ? bf16_hi_f32(wr[i][0][j / 2]) : bf16_lo_f32(wr[i][0][j / 2]);
   };
   float acc[NC][8] = {};
-  const auto use = [&](const Row &r, int row, int turn) {
+  const auto use = [&](const Row &r, int64_t row, int turn) {
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -249,10 +249,10 @@ __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
       __builtin_amdgcn_raw_buffer_store_b128(o, out, (i * TPR + l) * 16, 0, 0);
     }
   };
-  const int first = (int)blockIdx.x * RPB;  // every wave takes the same turns
+  const int64_t first = (int64_t)blockIdx.x * RPB;  // every wave takes the same turns
   Row a, b;
   load(a, first + sub);
-  for (int r0 = first; r0 < rows; r0 += 2 * step) {
+  for (int64_t r0 = first; r0 < rows; r0 += 2 * step) {
     load(b, r0 + step + sub);
     use(a, r0 + sub, 0);
     if (r0 + step >= rows) break;
