@@ -80,10 +80,34 @@ __device__ __forceinline__ uint32_t group_lane(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xF, 0xF, false);
 }
 
+constexpr uint32_t GATE_NONE = 0x80000000u;  // an offset past every buffer
+
+// The logits of the tokens t0 .. t0 + groups - 1 as a buffer: what lies past the
+// last token reads as 0, and writes there are dropped.
+template <int B>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gate_rows(const void *z, int64_t t0, int64_t T,
+                                                            int groups, int E) {
+  const int64_t n = min(T - t0, (int64_t)groups);
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(static_cast<const uint8_t *>(z)) + t0 * E * B, (short)0,
+      (int)(n * E * B), 0x00020000);
+}
+
 template <bool ZF32>
-__device__ __forceinline__ float load_logit(const void *z, int64_t i) {
-  if constexpr (ZF32) return static_cast<const float *>(z)[i];
-  return __uint_as_float((uint32_t) static_cast<const uint16_t *>(z)[i] << 16);
+__device__ __forceinline__ float load_logit(const __amdgpu_buffer_rsrc_t &r, uint32_t i) {
+  if constexpr (ZF32)
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)(4 * i), 0, 0));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(2 * i), 0, 0) << 16);
+}
+
+// e^x to about 2 ulp: 2^t with t = x log2(e) in two parts, the second through
+// its first-order term.  Beyond +-200 the result is inf or 0 in any case.
+__device__ __forceinline__ float exp_f32(float x) {
+  x = fminf(fmaxf(x, -200.0f), 200.0f);
+  const float t = x * 0x1.715476p+0f;
+  const float r = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, r * 0x1.62e43p-1f, p);
 }
 
 // Order-preserving key of a logit, never 0 (0 marks "no expert here" and
@@ -97,7 +121,9 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
+}
 
 }  // namespace
 
@@ -124,13 +150,16 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
     const int64_t t = t0 + threadIdx.x / LPT;
     const bool live = t < T;
     const bool valid = live && (!mask || mask[t]);
+    const __amdgpu_buffer_rsrc_t zr = gate_rows<ZF32 ? 4 : 2>(z, t0, T, groups, E);
+    const uint32_t row = (threadIdx.x / LPT) * E;
     float v[VPL];
     uint32_t key[VPL];
 #pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = load_logit<ZF32>(zr, row + i * LPT + l);
+#pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * LPT + l;
-      const bool in = e < E;
-      v[i] = in && valid ? load_logit<ZF32>(z, t * E + e) : -__builtin_inff();
+      const bool in = i * LPT + l < E;
+      v[i] = in && valid ? v[i] : -__builtin_inff();
       key[i] = in ? logit_key(v[i]) : 0u;
     }
     int my_id = 0;
@@ -157,13 +186,13 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = SOFTMAX ? expf(v[i] - top) : sigmoid(v[i]);
+      v[i] = SOFTMAX ? exp_f32(v[i] - top) : sigmoid(v[i]);
       if (i * LPT + l >= E) v[i] = 0.0f;
       sum += v[i];
     }
     sum = group_sum<LPT>(sum);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    float w = l < k ? (SOFTMAX ? expf(my_z - top) : sigmoid(my_z)) : 0.0f;
+    float w = l < k ? (SOFTMAX ? exp_f32(my_z - top) : sigmoid(my_z)) : 0.0f;
     if (renorm) {
       const float total = group_sum<LPT>(w);
       w = total > 0.0f ? w / total : 0.0f;
@@ -309,12 +338,15 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     const int64_t t = t0 + threadIdx.x / LPT;
     const bool live = t < T;
     const bool valid = live && (!mask || mask[t]);
+    const __amdgpu_buffer_rsrc_t zr = gate_rows<ZF32 ? 4 : 2>(z, t0, T, groups, E);
+    const uint32_t row = (threadIdx.x / LPT) * E;
     float v[VPL];
     float top = -__builtin_inff();
 #pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = load_logit<ZF32>(zr, row + i * LPT + l);
+#pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * LPT + l;
-      v[i] = e < E && valid ? load_logit<ZF32>(z, t * E + e) : -__builtin_inff();
+      v[i] = i * LPT + l < E && valid ? v[i] : -__builtin_inff();
       top = fmaxf(top, v[i]);
     }
     int my_id = -1;
@@ -323,7 +355,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       const int id = ids[t * k + l];
       if (id >= 0 && id < E) {
         my_id = id;
-        my_v = load_logit<ZF32>(z, t * E + id);
+        my_v = load_logit<ZF32>(zr, row + id);
         my_d = d_prob ? d_prob[t * k + l] * scale : 0.0f;
       }
     }
@@ -334,7 +366,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = SOFTMAX ? expf(v[i] - top) : sigmoid(v[i]);
+      v[i] = SOFTMAX ? exp_f32(v[i] - top) : sigmoid(v[i]);
       if (i * LPT + l >= E) v[i] = 0.0f;
       sum += v[i];
     }
@@ -344,7 +376,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
 #pragma unroll
       for (int i = 0; i < VPL; ++i) v[i] *= inv;
     }
-    if (my_id >= 0) my_v = SOFTMAX ? expf(my_v - top) * inv : sigmoid(my_v);
+    if (my_id >= 0) my_v = SOFTMAX ? exp_f32(my_v - top) * inv : sigmoid(my_v);
     else my_v = 0.0f;
     if (renorm) {
       const float total = group_sum<LPT>(my_v);
@@ -370,16 +402,27 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dot += SOFTMAX ? v[i] * (u[i] + h[i]) : v[i] * inv * h[i];
     dot = group_sum<LPT>(dot);
-    if (!live) continue;
+    float gz[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * LPT + l;
-      if (e >= E) continue;
-      float g = SOFTMAX ? v[i] * (u[i] + h[i] - dot)
-                        : v[i] * (1.0f - v[i]) * (u[i] + (h[i] - dot) * inv);
-      if (!valid) g = 0.0f;
-      if (out_f32) static_cast<float *>(d_z)[t * E + e] = g;
-      else static_cast<uint16_t *>(d_z)[t * E + e] = (uint16_t)pk_bf16_rne(g, 0.0f);
+      gz[i] = SOFTMAX ? v[i] * (u[i] + h[i] - dot)
+                      : v[i] * (1.0f - v[i]) * (u[i] + (h[i] - dot) * inv);
+      if (!valid) gz[i] = 0.0f;
+    }
+    if (out_f32) {
+      const __amdgpu_buffer_rsrc_t o = gate_rows<4>(d_z, t0, T, groups, E);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __float_as_uint(gz[i]), o,
+            (int)(i * LPT + l < E ? 4 * (row + i * LPT + l) : GATE_NONE), 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t o = gate_rows<2>(d_z, t0, T, groups, E);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        __builtin_amdgcn_raw_buffer_store_b16(
+            (uint16_t)pk_bf16_rne(gz[i], 0.0f), o,
+            (int)(i * LPT + l < E ? 2 * (row + i * LPT + l) : GATE_NONE), 0, 0);
     }
   }
 }
