@@ -20,6 +20,14 @@ namespace pqm {
 namespace {
 
 typedef uint32_t nb_u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t nb_u2 __attribute__((ext_vector_type(2)));
+
+// A store that streams past the caches, or an ordinary one.
+template <bool STREAM, typename V>
+__device__ __forceinline__ void put(void *p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<V *>(p));
+  else *static_cast<V *>(p) = v;
+}
 
 // 8 weights from column c on, as binary32.
 template <bool WF32>
@@ -63,9 +71,9 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // One row per TPR threads, NC chunks of 8 values per thread, kept in registers
 // between the sum of squares and the scaling, so each input is read once.
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
-// Bound by memory: 16384 x 2048 with residual, 235 MB, 44 us (5.4 TB/s); 8 x
-// 2048 takes 4.7 us, the time of a launch.
-template <int TPR, int NC, bool WF32>
+// Bound by memory: 16384 x 2048 with residual, 235 MB, 47 us (5.0 TB/s; a copy
+// here moves 5.1); 8 x 2048 takes 4.7 us, the time of a launch.
+template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
     int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *__restrict__ y,
@@ -103,8 +111,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     for (int i = 0; i < NC; ++i) {
       const int64_t c = ((int64_t)i * TPR + l) * 8;
       if (live && c < C)
-        *reinterpret_cast<uint4 *>(sum + row * C + c) =
-            make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        put<STREAM>(sum + row * C + c, nb_u4{v[i][0], v[i][1], v[i][2], v[i][3]});
     }
   }
   const float total = row_sum<TPR>(sq, red);
@@ -138,7 +145,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     for (int j = 0; j < 4; ++j)
       o[j] = pk_bf16_rne(bf16_lo_f32(v[i][j]) * rstd * wf[2 * j],
                          bf16_hi_f32(v[i][j]) * rstd * wf[2 * j + 1]);
-    if (y) *reinterpret_cast<uint4 *>(y + row * C + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (y) put<STREAM>(y + row * C + c, nb_u4{o[0], o[1], o[2], o[3]});
     if (q) {
       uint32_t mm = pk_max_u16(pk_max_u16(o[0] & 0x7FFF7FFFu, o[1] & 0x7FFF7FFFu),
                                pk_max_u16(o[2] & 0x7FFF7FFFu, o[3] & 0x7FFF7FFFu));
@@ -147,8 +154,8 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
       mm = max(mm, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mm, 0x4E, 0xF, 0xF, false));
       const uint32_t b = mx_scale_byte(mm);
       const float scale = __uint_as_float(b << 23);
-      *reinterpret_cast<uint2 *>(q + row * C + c) =
-          make_uint2(cvt4_e4m3_bf16(o[0], o[1], scale), cvt4_e4m3_bf16(o[2], o[3], scale));
+      put<STREAM>(q + row * C + c,
+                  nb_u2{cvt4_e4m3_bf16(o[0], o[1], scale), cvt4_e4m3_bf16(o[2], o[3], scale)});
       if ((threadIdx.x & 3) == 0) s[row * (C / 32) + c / 32] = (uint8_t)b;
     }
   }
@@ -162,10 +169,10 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
 // length: past their end reads give 0 and writes are dropped, and a row that
 // is none is an empty buffer.
 //
-// Bound by memory: 16384 x 2048 with d_sum, 268 MB, 49 us with k_rmsnorm_dw's 4
-// (5.5 TB/s; a copy here moves 5.1).  70 us without the next row in flight and
+// Bound by memory: 16384 x 2048 with d_sum, 268 MB, 52 us with k_rmsnorm_dw's 4
+// (5.2 TB/s; a copy here moves 5.1).  70 us without the next row in flight and
 // with weights read again for every row; two workgroups a CU, whose sums are
-// twice the bytes, 51.  1021 x 7168: 18 us, half of it the start of two
+// twice the bytes, 2 us more.  1021 x 7168: 18 us, half of it the start of two
 // kernels and their sums of dw.
 template <int TPR, int NC, bool WF32>
 __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
@@ -246,7 +253,8 @@ __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
             r.rs * (bf16_hi_f32(r.g[i][j]) * weight(i, 2 * j + 1) - bf16_hi_f32(r.s[i][j]) * r.rs * m);
         o[j] = pk_bf16_rne(lo + bf16_lo_f32(r.d[i][j]), hi + bf16_hi_f32(r.d[i][j]));
       }
-      __builtin_amdgcn_raw_buffer_store_b128(o, out, (i * TPR + l) * 16, 0, 0);
+      // streaming (2): 16384 x 2048 53.5 -> 51.7 us, 1021 x 7168 19.2 -> 18.4
+      __builtin_amdgcn_raw_buffer_store_b128(o, out, (i * TPR + l) * 16, 0, 2);
     }
   };
   const int64_t first = (int64_t)blockIdx.x * RPB;  // every wave takes the same turns
@@ -325,12 +333,17 @@ hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r
                     const void *w, int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *y,
                     uint8_t *q, uint8_t *s, float *rstd, hipStream_t st) {
   const dim3 grid((unsigned)((rows + 256 / TPR - 1) / (256 / TPR)));
-  if (wf32)
-    hipLaunchKernelGGL((k_rmsnorm_quant<TPR, NC, true>), grid, dim3(256), 0, st, x, ldx, r, ldr, w,
-                       rows, C, eps, sum, y, q, s, rstd);
-  else
-    hipLaunchKernelGGL((k_rmsnorm_quant<TPR, NC, false>), grid, dim3(256), 0, st, x, ldx, r, ldr, w,
-                       rows, C, eps, sum, y, q, s, rstd);
+  // Streaming stores from 2^21 values on: 16384 x 2048 with residual 51 -> 45.5
+  // us, 4096 x 7168 47 -> 42.6, 2048 x 2048 9.3 -> 8.1, 1024 x 2048 7.5 -> 7.0,
+  // 256 x 2048 5.6 -> 5.9; with a gather that reads q and y afterwards the sum of
+  // the two stays within 4 % either way.
+  const bool stream = rows * C >= (1 << 21);
+  const auto kernel = wf32 ? stream ? k_rmsnorm_quant<TPR, NC, true, true>
+                                    : k_rmsnorm_quant<TPR, NC, true, false>
+                           : stream ? k_rmsnorm_quant<TPR, NC, false, true>
+                                    : k_rmsnorm_quant<TPR, NC, false, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, x, ldx, r, ldr, w, rows, C, eps, sum, y, q, s,
+                     rstd);
   return hipGetLastError();
 }
 
