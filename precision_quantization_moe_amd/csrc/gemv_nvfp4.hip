@@ -458,23 +458,24 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
     // loads of its own turns alone
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
+    const auto block = [&](int blk, int i) {
+      load_x(blk + 1);
+      rescale(i);
+      multiply(b0, i, 0, 2 * i);
+      load(b0, 2 * blk + 2);
+      if (2 * blk + 1 < chunks) multiply(b1, i, 1, 2 * i + 1);
+      load(b1, 2 * blk + 3);
+      stage(i ^ 1);
+      __syncthreads();
+    };
     // two blocks a turn: the scales of their four chunks come together
-    for (int blk = 0; blk < blocks; blk += 2) {
+    for (int blk = 0;;) {
       put_s();
       load_s(2 * blk + 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (blk + i < blocks) {
-          load_x(blk + i + 1);
-          rescale(i);
-          multiply(b0, i, 0, 2 * i);
-          load(b0, 2 * (blk + i) + 2);
-          multiply(b1, i, 1, 2 * i + 1);
-          load(b1, 2 * (blk + i) + 3);
-          stage(i ^ 1);
-          __syncthreads();
-        }
-      }
+      block(blk, 0);
+      if (++blk >= blocks) break;
+      block(blk, 1);
+      if (++blk >= blocks) break;
     }
     if (ln < mr) {
       const int row = list[m0 + ln];
