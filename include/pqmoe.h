@@ -560,8 +560,8 @@ pqm_status pqm_moe_combine(const uint16_t *y_rows, const int32_t *slot,
  *   sum, y [rows, cols] bf16; q [rows, cols] E4M3; s [rows, cols/32] E8M0;
  *   rstd [rows] binary32, for the backward pass                     (device)
  * sum, y and rstd may be NULL, and so may the pair q, s; one of y and q is
- * required (PQM_ERR_NULL).  sum may be the memory of x or of residual (with
- * a row stride of cols) and is then updated in place; no other output may
+ * required (PQM_ERR_NULL).  sum may be the memory of x or of residual, whose
+ * row stride must then be cols (PQM_ERR_SHAPE), and is updated in place; no other output may
  * overlap an input.  Sums are binary32; rows whose squares leave binary32
  * (values from about 2^63 on) are handled.  x + residual and y must stay
  * within the bf16 range.
@@ -617,7 +617,8 @@ size_t pqm_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  * mask 0 are not read; its prob is 0, it takes no part in counts, prob_sum or
  * loss, and its ids are (t k + j) mod E, so that padding loads every expert
  * alike in pqm_moe_route.  A logit of -inf closes an expert to a token
- * (chosen last, prob 0; a row of -inf alone gives prob 0).  NaN and +inf are
+ * (chosen last, prob 0; a row of -inf alone gives prob 0, as do chosen sigmoid
+ * scores that all vanish in binary32, z below about -87).  NaN and +inf are
  * outside the contract (the ids stay in [0, E)).  The arithmetic is binary32.
  * counts, prob_sum and loss go together: all NULL skips the loss, and
  * workspace is then not needed.  workspace (device, 4-byte aligned, contents

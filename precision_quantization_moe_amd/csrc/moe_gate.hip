@@ -202,7 +202,7 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
     if (live && l < k) {
       // a token that the mask leaves out is not read: experts in turn, so that
       // padding loads all of them alike, and no weight
-      ids[t * k + l] = valid ? my_id : (int32_t)((t * k + l) % E);
+      ids[t * k + l] = valid ? my_id : (int32_t)((uint32_t)(t * k + l) % (uint32_t)E);
       prob[t * k + l] = valid ? w * scale : 0.0f;
     }
     if constexpr (SUMS) {

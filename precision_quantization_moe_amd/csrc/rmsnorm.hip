@@ -403,6 +403,8 @@ pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint
     return PQM_ERR_SHAPE;
   if (ldx < cols || (residual && ldr < cols)) return PQM_ERR_SHAPE;
   if ((q || s) && cols % 32) return PQM_ERR_SHAPE;
+  // in place only where the rows of sum lie where they were read
+  if (sum && ((sum == x && ldx != cols) || (sum == residual && ldr != cols))) return PQM_ERR_SHAPE;
   if (!(eps >= 0x1p-100f) || !(eps < __builtin_inff())) return PQM_ERR_SHAPE;
   if (rows == 0 || cols == 0) return PQM_OK;
   if (!x || !weight || (!q && !y) || (q == nullptr) != (s == nullptr)) return PQM_ERR_NULL;

@@ -243,3 +243,27 @@ def test_deterministic_on_streams_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(want, out)), i
         both()
         torch.cuda.synchronize()
+
+
+def test_more_than_2_31_logits():
+    """The last tokens' offsets pass 32 bits; the counts and sums are whole."""
+    T, E, k = 2_200_000, 1024, 2
+    z = torch.full((T, E), -4.0, device="cuda", dtype=torch.bfloat16)
+    assert z.numel() > 2 ** 31
+    z[:, 5], z[:, 9] = 2.0, 1.0
+    tail = logits(7, E, True, 11)
+    z[-7:] = tail.cuda()
+    ids, prob, counts, prob_sum, loss = pqm.moe_gate(z, k, loss_coef=0.01)
+    want = ref.gate(ref.f64(tail), k, True, True, 1.0)
+    assert torch.equal(ids[-7:].cpu().long(), want["ids"])
+    assert (ids[:-7] == torch.tensor([5, 9], device="cuda")).all()
+    tol = (spread(tail.double()) + 32) * ref.U
+    assert ((ref.f64(prob[-7:]) - want["prob"]).abs() <= tol * want["prob"]).all()
+    assert int(counts[E]) == T and int(counts[:E].sum()) == T * k
+    assert int(counts[5]) >= T - 7 and int(counts[9]) >= T - 7
+    assert abs(float(prob_sum.double().sum()) / T - 1) <= (T // 4096 + 64) * ref.U
+    d = torch.zeros(T, k, device="cuda")
+    d[-7:] = torch.randn(7, k, generator=torch.Generator().manual_seed(1)).cuda()
+    dz = pqm.moe_gate_backward(z, ids, d)
+    one = pqm.moe_gate_backward(tail.cuda(), ids[-7:].contiguous(), d[-7:].contiguous())
+    assert torch.equal(dz[-7:], one) and not dz[:-7].any()

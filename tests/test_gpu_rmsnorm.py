@@ -193,3 +193,25 @@ def test_other_stream_and_graph_replay():
         assert all(torch.equal(a, b) for a, b in zip(want + want_b, out + out_b)), i
         pqm.rmsnorm_backward(dy, want[3], wg, want[4])
         torch.cuda.synchronize()
+
+
+def test_more_than_2_31_values():
+    """Rows beyond the reach of 32-bit offsets, and streaming stores."""
+    rows, cols = 140000, 16384
+    few = 6
+    x, r, w = inputs(few, cols, False, True, 77)
+    dy = torch.randn(few, cols, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    xg = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    rg, gg = torch.zeros_like(xg), torch.zeros_like(xg)
+    assert xg.numel() > 2 ** 31
+    xg[-few:], rg[-few:], gg[-few:] = cu(x), cu(r), cu(dy)
+    out = pqm.rmsnorm_quantize_mxfp8(xg, cu(w), 1e-6, residual=rg, keep_y=True)
+    check(x, r, w, 1e-6, tuple(t[-few:] for t in out))
+    # 0 times a negative weight is -0, the code 0x80
+    assert not (out[0][:-few] & 0x7F).any()
+    dx, dw = pqm.rmsnorm_backward(gg, out[3], cu(w), out[4], d_sum=rg)
+    alone = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 1e-6, residual=cu(r), keep_y=True)
+    want, _ = pqm.rmsnorm_backward(cu(dy), alone[3], cu(w), alone[4], d_sum=cu(r))
+    assert torch.equal(dx[-few:], want) and not dx[:-few].any()
+    want64 = ref.norm_backward(ref.f64(dy), ref.f64(alone[3]), ref.f64(w), ref.f64(alone[4]))
+    assert ((ref.f64(dw) - want64[1]).abs() <= (few + 3) * ref.U * want64[3]).all()

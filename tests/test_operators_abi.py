@@ -12,6 +12,7 @@ import operators_ref as ref
 import precision_quantization_moe_amd as pqm
 
 A = ctypes.c_void_p(0x10000)
+D = ctypes.c_void_p(0x20000)
 B8 = ctypes.c_void_p(0x10008)
 B2 = ctypes.c_void_p(0x10002)
 B1 = ctypes.c_void_p(0x10001)
@@ -31,7 +32,7 @@ def caller(name, ok):
 def test_rmsnorm_quantize_arguments():
     # x ldx residual ldr weight wdtype rows cols eps sum y q s rstd stream
     c = caller("pqm_rmsnorm_quantize_mxfp8",
-               [A, 64, A, 64, A, 0, 4, 64, 1e-6, A, A, A, A, A, None])
+               [A, 64, A, 64, A, 0, 4, 64, 1e-6, D, A, A, A, A, None])
     assert c(a5=2) == 4
     assert c(a6=-1) == 2 and c(a7=-32) == 2
     assert c(a7=48) == 2                              # quantized: cols % 32
@@ -48,6 +49,8 @@ def test_rmsnorm_quantize_arguments():
         assert c(**{f"a{i}": B8}) == 3, i             # 16-byte
     assert c(a11=B2) == 3 and c(a13=B2) == 3
     assert c(a1=68) == 3 and c(a3=68) == 3            # stride not 16 bytes
+    assert c(a1=72, a9=A, a2=D) == 2                  # sum is x, with another stride
+    assert c(a0=D, a3=72, a9=A) == 2                  # sum is residual, the same
     assert c(a6=0, a0=None) == 0 and c(a7=0) == 0     # nothing to do
 
 
