@@ -82,15 +82,17 @@ __device__ __forceinline__ uint32_t group_lane(uint32_t v) {
 
 constexpr uint32_t GATE_NONE = 0x80000000u;  // an offset past every buffer
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gate_buffer(const void *p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, bytes, 0x00020000);
+}
+
 // The logits of the tokens t0 .. t0 + groups - 1 as a buffer: what lies past the
 // last token reads as 0, and writes there are dropped.
 template <int B>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t gate_rows(const void *z, int64_t t0, int64_t T,
                                                             int groups, int E) {
   const int64_t n = min(T - t0, (int64_t)groups);
-  return __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(static_cast<const uint8_t *>(z)) + t0 * E * B, (short)0,
-      (int)(n * E * B), 0x00020000);
+  return gate_buffer(static_cast<const uint8_t *>(z) + t0 * E * B, (int)(n * E * B));
 }
 
 template <bool ZF32>
@@ -127,7 +129,12 @@ __device__ __forceinline__ float sigmoid(float z) {
 
 }  // namespace
 
-// LPT lanes hold one token, VPL logits each (expert i LPT + lane).  SUMS: each
+// LPT lanes hold one token, VPL logits each (expert i LPT + lane); the choice
+// takes k turns of a maximum over the keys, the lowest index that has it, and
+// its removal.  Bound by those turns' vector instructions (about 50 a turn for
+// 128 experts, shared by four tokens) and, for few tokens, by the start of a
+// kernel: 16384 x 128, top-8, with the loss 14.5 us (k_moe_balance 4 of them,
+// floor 1.9), 16 x 256 without 5.0.  SUMS: each
 // workgroup also leaves its counts and share sums in part_cnt / part_sum
 // [gridDim.x][E] (and its valid tokens in part_valid).
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
@@ -147,15 +154,18 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
     __syncthreads();
   }
   for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < T; t0 += (int64_t)gridDim.x * groups) {
-    const int64_t t = t0 + threadIdx.x / LPT;
-    const bool live = t < T;
-    const bool valid = live && (!mask || mask[t]);
+    const int n = (int)min(T - t0, (int64_t)groups), mine = threadIdx.x / LPT;
+    const int64_t t = t0 + mine;
+    const bool live = mine < n;
     const __amdgpu_buffer_rsrc_t zr = gate_rows<ZF32 ? 4 : 2>(z, t0, T, groups, E);
-    const uint32_t row = (threadIdx.x / LPT) * E;
+    const uint32_t row = mine * E;
     float v[VPL];
     uint32_t key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = load_logit<ZF32>(zr, row + i * LPT + l);
+    const uint32_t mk = __builtin_amdgcn_raw_buffer_load_b8(
+        gate_buffer(mask + (mask ? t0 : 0), mask ? n : 0), mine, 0, 0);
+    const bool valid = live && (!mask || mk);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const bool in = i * LPT + l < E;
@@ -315,6 +325,11 @@ __global__ __launch_bounds__(1024) void k_moe_balance(
   }
 }
 
+// The gradient, laid out as the forward kernel.  16384 x 128 7.9 us, 4093 x 256
+// in bf16 5.6 (floors 3.5 and 0.8; a launch takes about 4.5).  Every load goes
+// out before the first is used (10.1 and 8.5 us with the counts, the ids and
+// the chosen logits waited for in turn); comparing each expert with each of the
+// k ids instead of the row in LDS took 0.8 us more.
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
 __global__ __launch_bounds__(256) void k_moe_gate_backward(
     const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
@@ -323,41 +338,38 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     const float *__restrict__ d_loss, void *__restrict__ d_z, int out_f32) {
   const int l = threadIdx.x % LPT;
   constexpr int groups = 256 / LPT;
-  float h[VPL];
-  float hc = 0.0f;
-  if (counts && counts[E] > 0) {
-    const float tv = (float)counts[E];
-    hc = d_loss[0] * coef * (float)E / (float)k / tv / tv;
-  }
+  // A token's row of E values, for what one lane has and another needs: its
+  // scores, then d prob / d v, 0 but at the chosen experts.  (16 more: tokens
+  // in other banks.)  One wave's LDS accesses keep their order, so the fences
+  // hold only the compiler.
+  __shared__ float rows[groups][VPL * LPT + 16];
+  float *mine = rows[threadIdx.x / LPT];
+  // counts, empty without a loss: every load below goes out before one is used
+  const __amdgpu_buffer_rsrc_t cr = gate_buffer(counts, counts ? 4 * (E + 1) : 0);
+  int cnt[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * LPT + l;
-    h[i] = counts && e < E ? hc * (float)counts[e] : 0.0f;
-  }
+  for (int i = 0; i < VPL; ++i)
+    cnt[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(cr, 4 * (i * LPT + l), 0, 0);
+  const float valid_tokens = counts ? (float)counts[E] : 0.0f, dl = counts ? d_loss[0] : 0.0f;
   for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < T; t0 += (int64_t)gridDim.x * groups) {
-    const int64_t t = t0 + threadIdx.x / LPT;
-    const bool live = t < T;
-    const bool valid = live && (!mask || mask[t]);
+    const int n = (int)min(T - t0, (int64_t)groups), in = threadIdx.x / LPT;
     const __amdgpu_buffer_rsrc_t zr = gate_rows<ZF32 ? 4 : 2>(z, t0, T, groups, E);
-    const uint32_t row = (threadIdx.x / LPT) * E;
+    const uint32_t row = in * E, at = l < k ? 4 * (in * k + l) : GATE_NONE;
     float v[VPL];
-    float top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = load_logit<ZF32>(zr, row + i * LPT + l);
+    const int id =
+        (int)__builtin_amdgcn_raw_buffer_load_b32(gate_buffer(ids + t0 * k, 4 * n * k), (int)at, 0, 0);
+    const float dp = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        gate_buffer(d_prob + (d_prob ? t0 * k : 0), d_prob ? 4 * n * k : 0), (int)at, 0, 0));
+    const uint32_t mk = __builtin_amdgcn_raw_buffer_load_b8(
+        gate_buffer(mask + (mask ? t0 : 0), mask ? n : 0), in, 0, 0);
+    const bool valid = in < n && (!mask || mk);
+    float top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       v[i] = i * LPT + l < E && valid ? v[i] : -__builtin_inff();
       top = fmaxf(top, v[i]);
-    }
-    int my_id = -1;
-    float my_v = 0.0f, my_d = 0.0f;
-    if (valid && l < k) {
-      const int id = ids[t * k + l];
-      if (id >= 0 && id < E) {
-        my_id = id;
-        my_v = load_logit<ZF32>(zr, row + id);
-        my_d = d_prob ? d_prob[t * k + l] * scale : 0.0f;
-      }
     }
     if constexpr (SOFTMAX) {
       top = group_fmax<LPT>(top);
@@ -376,21 +388,31 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
 #pragma unroll
       for (int i = 0; i < VPL; ++i) v[i] *= inv;
     }
-    if (my_id >= 0) my_v = SOFTMAX ? exp_f32(my_v - top) * inv : sigmoid(my_v);
-    else my_v = 0.0f;
+    // the chosen experts' scores, from the lanes that hold them
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine[i * LPT + l] = v[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int my_id = valid && l < k && id >= 0 && id < E ? id : -1;
+    const float my_v = my_id >= 0 ? mine[my_id] : 0.0f;
+    float my_d = my_id >= 0 ? dp * scale : 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine[i * LPT + l] = 0.0f;
     if (renorm) {
       const float total = group_sum<LPT>(my_v);
       const float dot = group_sum<LPT>(my_d * my_v);
       const float it = total > 0.0f ? 1.0f / total : 0.0f;
       my_d = (my_d - dot * it) * it;
     }
-    float u[VPL] = {};
+    // An expert chosen twice gets the sum, in both its places; then each place
+    // lays its value where the expert's lane finds it.
+    float total = 0.0f;
     const auto add = [&](auto j) {
       if (decltype(j)::value >= k) return;  // the same for every lane
       const int id = (int)group_lane<LPT, decltype(j)::value>((uint32_t)my_id);
       const float d = __uint_as_float(group_lane<LPT, decltype(j)::value>(__float_as_uint(my_d)));
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) u[i] += i * LPT + l == id ? d : 0.0f;
+      total += id == my_id ? d : 0.0f;
     };
     add(lane_c<0>{}); add(lane_c<1>{}); add(lane_c<2>{}); add(lane_c<3>{});
     add(lane_c<4>{}); add(lane_c<5>{}); add(lane_c<6>{}); add(lane_c<7>{});
@@ -398,6 +420,17 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       add(lane_c<8>{}); add(lane_c<9>{}); add(lane_c<10>{}); add(lane_c<11>{});
       add(lane_c<12>{}); add(lane_c<13>{}); add(lane_c<14>{}); add(lane_c<15>{});
     }
+    float u[VPL];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (my_id >= 0) mine[my_id] = total;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) u[i] = mine[i * LPT + l];
+    const float hc =
+        valid_tokens > 0.0f ? dl * coef * (float)E / (float)k / valid_tokens / valid_tokens : 0.0f;
+    float h[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) h[i] = i * LPT + l < E ? hc * (float)cnt[i] : 0.0f;
     float dot = 0.0f;  // softmax: sum p (u + h); sigmoid: sum p h
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dot += SOFTMAX ? v[i] * (u[i] + h[i]) : v[i] * inv * h[i];
