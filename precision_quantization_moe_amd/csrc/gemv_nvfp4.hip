@@ -144,10 +144,10 @@ struct GvTurn {
 };
 
 // A lane's part of a 256-wide chunk of a tile: eight rows a load, eight lanes
-// each; of the scales a row's 16 bytes in four lanes, two and two.
+// each; of the scales a row's 16 bytes in four lanes.
 struct GdChunk {
   gv_u4 q[2];
-  uint32_t s[2];
+  uint32_t s;
 };
 
 }  // namespace
@@ -157,10 +157,15 @@ struct GdChunk {
 // and its up tile) and a quarter of the contraction in 256-wide chunks, so a
 // chain is short: what bounds this kernel is latency (ids, weights, x, then
 // the joining).  One decode step of top-8 of 128 experts, 2048 x 768: gate_up
-// 9.6 us, down 6.2 us of about 4.5 that a kernel of nothing takes here.  Two
+// 8.9 us, down 6.0 us of about 4.5 that a kernel of nothing takes here.  Two
 // tiles a wave took 10.4 and 6.7; waiting for the rows before the first
-// weights were asked for, 12.  Any K % 32 == 0.
-template <bool ACT, bool OUTF32>
+// weights were asked for, 12; the next chunk's loads ahead of this one's
+// products, 9.0 and 7.1 (the registers halve what a CU holds).
+//
+// WORDS: K % 64 == 0, so that a row of scales starts at a word; otherwise (any
+// K % 32 == 0) it starts at any even byte and its words come in halves, which
+// the compiler joins, and waits for, before the rows are known: 9.6 and 6.2.
+template <bool ACT, bool OUTF32, bool WORDS>
 __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
                                                         const int32_t *__restrict__ ids) {
   constexpr int KS = 4;
@@ -188,9 +193,11 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
     const int vs = (int)((lane >> 2) * (uint32_t)(K / 16) + 4 * (lane & 3) + os);
     b.q[0] = __builtin_amdgcn_raw_buffer_load_b128(wq, vq, 0, 0);
     b.q[1] = __builtin_amdgcn_raw_buffer_load_b128(wq, vq + 8 * (K / 2), 0, 0);
-    // a row of scales starts at any even byte
-    b.s[0] = __builtin_amdgcn_raw_buffer_load_b16(ws, vs, 0, 0);
-    b.s[1] = __builtin_amdgcn_raw_buffer_load_b16(ws, vs + 2, 0, 0);
+    if constexpr (WORDS)
+      b.s = __builtin_amdgcn_raw_buffer_load_b32(ws, vs, 0, 0);
+    else
+      b.s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ws, vs, 0, 0) |
+            (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ws, vs + 2, 0, 0) << 16;
   };
   // the first chunk's loads go out before the rows are known
   GdChunk b;
@@ -217,8 +224,7 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
     const auto multiply = [&](const GdChunk &b, const uint4 (&x)[8]) {
       gv_u4 q[2];
       turn(b.q, q);
-      const int sw =
-          __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)(b.s[0] | b.s[1] << 16));
+      const int sw = __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)b.s);
       const float f[4] = {__builtin_amdgcn_cvt_f32_fp8(sw, 0), __builtin_amdgcn_cvt_f32_fp8(sw, 1),
                           __builtin_amdgcn_cvt_f32_fp8(sw, 2), __builtin_amdgcn_cvt_f32_fp8(sw, 3)};
 #pragma unroll
@@ -289,7 +295,7 @@ struct GvChunk {
 // 2^14 times less than what the binary32 sum may round.
 //
 // Measured, 37 tokens x top-8 of 64 experts, 5120 x 1280: gate_up 472 MB in
-// 100 us (4.7 TB/s; loads alone in this pattern 6.1), 29 tokens: down 61 us.
+// 101 us (4.7 TB/s; loads alone in this pattern 6.1), 29 tokens: down 59 us.
 // What made it so, gate_up: 174 us with a row of weights in each lane (see
 // GvTurn); 150 -> 136 by waits that count loads (no load in a branch); 125
 // after the scales' loads became whole lines; 111 without a pass that found
@@ -525,9 +531,12 @@ hipError_t launch_gemv(GemvArgs a, const int32_t *ids, bool act, bool f32, hipSt
     return gv_launch(a, gs_cols(false), 256, lds, k_gemv_staged<false, false>, ids, st);
   }
   const int lds = 2 * a.rows;
-  if (act) return gv_launch(a, 16, 512, lds, k_gemv_direct<true, false>, ids, st);
-  if (f32) return gv_launch(a, 32, 512, lds, k_gemv_direct<false, true>, ids, st);
-  return gv_launch(a, 32, 512, lds, k_gemv_direct<false, false>, ids, st);
+  const bool w = a.K % 64 == 0;
+  const auto kernel = act   ? w ? k_gemv_direct<true, false, true> : k_gemv_direct<true, false, false>
+                      : f32 ? w ? k_gemv_direct<false, true, true> : k_gemv_direct<false, true, false>
+                      : w   ? k_gemv_direct<false, false, true>
+                            : k_gemv_direct<false, false, false>;
+  return gv_launch(a, act ? 16 : 32, 512, lds, kernel, ids, st);
 }
 
 bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
