@@ -181,8 +181,7 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
   const int64_t n0 = (int64_t)blockIdx.x * COLS, NW = ACT ? 2 * a.N : a.N;
   const int cols = (int)min((int64_t)COLS, a.N - n0);
   const int K = (int)a.K, chunks = (K + 255) / 256;
-  // The tile's weight rows as buffers: what lies past their end reads as 0,
-  // and x is 0 past the end of its rows.
+  // The tile's weight rows as buffers: what lies past their end reads as 0.
   const int64_t r0 = (int64_t)(e < 0 ? 0 : e) * NW + n0 + (t ? (ACT ? a.N : 16) : 0);
   const int rows = ACT ? cols : max(0, min(16, cols - 16 * t));
   const __amdgpu_buffer_rsrc_t wq = gv_buffer(a.w + r0 * (K / 2), (int64_t)rows * (K / 2));
@@ -221,10 +220,14 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
       }
     };
     gv_f4 acc = {0, 0, 0, 0};
-    const auto multiply = [&](const GdChunk &b, const uint4 (&x)[8]) {
+    const auto multiply = [&](const GdChunk &b, const uint4 (&x)[8], int ch) {
       gv_u4 q[2];
       turn(b.q, q);
-      const int sw = __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)b.s);
+      int sw = __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)b.s);
+      // past the row's end stand the next row's scales, maybe NaN: x is 0 there,
+      // the scale has to be so too
+      const int left = K - 256 * ch - 64 * g;
+      if (left < 64) sw = left == 32 ? sw & 0xFFFF : 0;
       const float f[4] = {__builtin_amdgcn_cvt_f32_fp8(sw, 0), __builtin_amdgcn_cvt_f32_fp8(sw, 1),
                           __builtin_amdgcn_cvt_f32_fp8(sw, 2), __builtin_amdgcn_cvt_f32_fp8(sw, 3)};
 #pragma unroll
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
       if (!early || m0 > 0 || ch > kw) load(b, ch);
       uint4 x[8];
       load_x(x, ch);
-      multiply(b, x);
+      multiply(b, x, ch);
     }
     red[kw][t][lane] = acc;
     __syncthreads();
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
   const int64_t NW = ACT ? 2 * a.N : a.N;
   const int K = (int)a.K, chunks = (K + 255) / 256, blocks = (K + GS_KB - 1) / GS_KB;
   // The workgroup's weight rows as buffers: what lies past their end reads as
-  // 0, and x is 0 past the end of its rows, so neither needs a bound here.
+  // 0; past the end of one row, x and the scales are made 0 at their use.
   const int64_t r0 = (int64_t)e * NW + n0;
   const __amdgpu_buffer_rsrc_t wq = gv_buffer(a.w + r0 * (K / 2), (int64_t)cols * (K / 2));
   const __amdgpu_buffer_rsrc_t ws = gv_buffer(a.ws + r0 * (K / 16), (int64_t)cols * (K / 16));
@@ -429,15 +432,16 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     // ch: the chunk's place in its block; sc: its place among the four whose
-    // scales are in LDS
-    const auto multiply = [&](const GvChunk &b, int buf, int ch, int sc) {
+    // scales are in LDS; left: what the rows hold from it on
+    const auto multiply = [&](const GvChunk &b, int buf, int ch, int sc, int left) {
       const uint8_t *xp = smem + (buf * 16 + min(ln, mr - 1)) * GS_STR + ch * 512 + g * 128;
       gv_h2 f[2][2];
       gv_u4 q[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         turn(b.q[t], q[t]);
-        const int sw = *reinterpret_cast<const int *>(mys + (16 * t + ln) * 80 + sc * 16 + 4 * g);
+        int sw = *reinterpret_cast<const int *>(mys + (16 * t + ln) * 80 + sc * 16 + 4 * g);
+        if (64 * g >= left) sw = 0;  // the next row's, maybe NaN; x is 0 there
         f[t][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, false);
         f[t][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, true);
       }
@@ -467,9 +471,9 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
     const auto block = [&](int blk, int i) {
       load_x(blk + 1);
       rescale(i);
-      multiply(b0, i, 0, 2 * i);
+      multiply(b0, i, 0, 2 * i, K - 512 * blk);
       load(b0, 2 * blk + 2);
-      if (2 * blk + 1 < chunks) multiply(b1, i, 1, 2 * i + 1);
+      if (2 * blk + 1 < chunks) multiply(b1, i, 1, 2 * i + 1, K - 512 * blk - 256);
       load(b1, 2 * blk + 3);
       stage(i ^ 1);
       __syncthreads();

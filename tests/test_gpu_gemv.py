@@ -194,6 +194,27 @@ def test_a_row_depends_on_its_own_values_alone(N):
     assert not torch.isfinite(got[1]).any()
 
 
+@pytest.mark.parametrize("N,K", [(40, 96), (40, 64), (40, 320), (40, 800), (640, 64), (640, 320), (640, 832),
+                                 (640, 1088)])
+def test_a_weight_row_of_nan_scales_stays_alone(N, K):
+    """Rows end inside a chunk of 256: what is read past the end belongs to the
+    next row, whose NaN must not meet the zeros that x has there."""
+    rows = G = 41
+    ids = torch.arange(rows, dtype=torch.int32)
+    x = acts(rows, K, K)
+    q, sb, sg, rps = weights(G, N, K, K)
+    clean = run_plain(x, ids, (q, sb, sg, rps), N)
+    bad = sb.clone()
+    bad.view(G, N, -1)[:, 1::2] = 0x7F
+    got = run_plain(x, ids, (q, bad, sg, rps), N)
+    assert torch.equal(got[:, 0::2], clean[:, 0::2])
+    assert got[:, 1::2].isnan().all()
+    prob = torch.ones(rows, 1)
+    act = [pqm.moe_gemv_swiglu_nvfp4(x.cuda(), ids.view(-1, 1).cuda(), prob.cuda(), q.cuda(), s.cuda(), sg.cuda(),
+                                     N // 2, rps, 1) for s in (sb, bad)]
+    assert torch.equal(act[0][:, 0::2], act[1][:, 0::2])
+
+
 @pytest.mark.parametrize("N", [96, 2050])
 def test_same_result_whatever_else_is_in_the_batch(N):
     """The same number of rows, the others' experts and values changed."""
