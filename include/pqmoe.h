@@ -561,12 +561,12 @@ pqm_status pqm_moe_combine(const uint16_t *y_rows, const int32_t *slot,
  *   rstd [rows] binary32, for the backward pass                     (device)
  * sum, y and rstd may be NULL, and so may the pair q, s; one of y and q is
  * required (PQM_ERR_NULL).  sum may be the memory of x or of residual, whose
- * row stride must then be cols (PQM_ERR_SHAPE), and is updated in place; no other output may
- * overlap an input.  Sums are binary32; rows whose squares leave binary32
+ * row stride must then be cols (PQM_ERR_SHAPE), and is updated in place; no
+ * other output may overlap an input.  Sums are binary32; rows whose squares leave binary32
  * (values from about 2^63 on) are handled.  x + residual and y must stay
  * within the bf16 range.
  * Requires cols % 8 == 0 (% 32 with q, s), cols <= 16384, rows < 2^31,
- * ldx, ldr >= cols, 2^-100 <= eps < infinity (PQM_ERR_SHAPE); x, residual,
+ * ldx, ldr >= cols, 2^-100 <= eps <= 1 (PQM_ERR_SHAPE); x, residual,
  * weight, sum, y and the strides 16-byte aligned, q 8-byte, rstd 4-byte
  * (PQM_ERR_ALIGN).
  */
@@ -646,8 +646,8 @@ size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts);
  * are held fixed; counts is the forward call's [E + 1], and counts and d_loss
  * go together (both NULL: no loss).  The other arguments are the forward
  * call's.  d_logits [tokens, E] in d_logits_dtype (rounded once), zero for
- * masked tokens; it may not overlap logits.  topk_ids may hold any experts (an id twice adds
- * up); ids outside [0, E) add nothing.  Same limits and errors.
+ * masked tokens; it may not overlap logits.  topk_ids may hold any experts (an
+ * id twice adds up); ids outside [0, E) add nothing.  Same limits and errors.
  */
 pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
                                  int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,

@@ -495,12 +495,13 @@ template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
 hipError_t go_gate(const GateArgs &a) {
   const int64_t P = gate_groups(a.T, a.E);
   if (!a.loss) {
-    // no sums to join: as many workgroups as there are tokens for
-    const int64_t per = 256 / LPT, g = (a.T + per - 1) / per;
-    hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, false>), dim3((unsigned)g), dim3(256),
-                       0, a.st, a.z, a.mask, a.T, a.E, a.k, a.renorm, a.scale, a.ids, a.prob,
-                       (int32_t *)nullptr, (float *)nullptr, (int32_t *)nullptr,
-                       (uint32_t *)nullptr);
+    // no sums to join: as many workgroups as there are tokens for (a grid has
+    // fewer than 2^32 threads, so at most 2^20; their loop takes the rest)
+    const int64_t per = 256 / LPT, g = (a.T + per - 1) / per, most = 1 << 20;
+    hipLaunchKernelGGL((k_moe_gate<LPT, VPL, ZF32, SOFTMAX, false>),
+                       dim3((unsigned)(g < most ? g : most)), dim3(256), 0, a.st, a.z, a.mask, a.T, a.E,
+                       a.k, a.renorm, a.scale, a.ids, a.prob, (int32_t *)nullptr, (float *)nullptr,
+                       (int32_t *)nullptr, (uint32_t *)nullptr);
     return hipGetLastError();
   }
   float *ps = static_cast<float *>(a.ws);

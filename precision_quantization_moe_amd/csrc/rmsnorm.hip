@@ -117,7 +117,8 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
   const float total = row_sum<TPR>(sq, red);
   float rstd = 1.0f / sqrtf(total / (float)C + eps);
   // Values from about 2^63 on square beyond binary32: sum (s 2^-80)^2 then,
-  // at most 2^15 (2^48)^2; eps is far below the last bit of such a mean.
+  // at most 2^15 (2^48)^2; eps, at most 1, is far below the last bit of such a
+  // mean.
   if (!(total < __builtin_inff())) {
     float t = 0.0f;
 #pragma unroll
@@ -332,7 +333,6 @@ template <int TPR, int NC>
 hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr,
                     const void *w, int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *y,
                     uint8_t *q, uint8_t *s, float *rstd, hipStream_t st) {
-  const dim3 grid((unsigned)((rows + 256 / TPR - 1) / (256 / TPR)));
   // Streaming stores from 2^21 values on: 16384 x 2048 with residual 51 -> 45.5
   // us, 4096 x 7168 47 -> 42.6, 2048 x 2048 9.3 -> 8.1, 1024 x 2048 7.5 -> 7.0,
   // 256 x 2048 5.6 -> 5.9; with a gather that reads q and y afterwards the sum of
@@ -342,8 +342,15 @@ hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r
                                     : k_rmsnorm_quant<TPR, NC, true, false>
                            : stream ? k_rmsnorm_quant<TPR, NC, false, true>
                                     : k_rmsnorm_quant<TPR, NC, false, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, x, ldx, r, ldr, w, rows, C, eps, sum, y, q, s,
-                     rstd);
+  // a grid has fewer than 2^32 threads: at most 2^23 workgroups a launch
+  constexpr int64_t RPB = 256 / TPR, most = RPB << 23;
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most, o = r0 * C;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((n + RPB - 1) / RPB)), dim3(256), 0, st,
+                       x + r0 * ldx, ldx, r ? r + r0 * ldr : r, ldr, w, n, C, eps,
+                       sum ? sum + o : sum, y ? y + o : y, q ? q + o : q, s ? s + o / 32 : s,
+                       rstd ? rstd + r0 : rstd);
+  }
   return hipGetLastError();
 }
 
@@ -405,7 +412,7 @@ pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint
   if ((q || s) && cols % 32) return PQM_ERR_SHAPE;
   // in place only where the rows of sum lie where they were read
   if (sum && ((sum == x && ldx != cols) || (sum == residual && ldr != cols))) return PQM_ERR_SHAPE;
-  if (!(eps >= 0x1p-100f) || !(eps < __builtin_inff())) return PQM_ERR_SHAPE;
+  if (!(eps >= 0x1p-100f) || !(eps <= 1.0f)) return PQM_ERR_SHAPE;
   if (rows == 0 || cols == 0) return PQM_OK;
   if (!x || !weight || (!q && !y) || (q == nullptr) != (s == nullptr)) return PQM_ERR_NULL;
   if (!al(x, 16) || ldx % 8 || !al(weight, 16) || !al(sum, 16) || !al(y, 16) || !al(q, 8) ||

@@ -192,7 +192,9 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
     """An expert layer's training forward pass from the residual stream on:
     residual addition, RMS norm and MXFP8 encoding in one pass, router gate
     with its balance loss, then the experts of mxfp8_moe_forward.  mask [T]
-    marks padding with 0.  Returns the experts' dict and h, y, rstd, logits,
+    marks padding with 0: no part in the loss, no weight, no gradient to the
+    gate; its x must be finite, since its rows still pass through the products.
+    Returns the experts' dict and h, y, rstd, logits,
     ids, prob, counts, prob_sum, loss."""
     T = x.shape[0]
     plan = plan or block_plan(T, k, x.device)

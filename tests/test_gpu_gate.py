@@ -267,3 +267,14 @@ def test_more_than_2_31_logits():
     dz = pqm.moe_gate_backward(z, ids, d)
     one = pqm.moe_gate_backward(tail.cuda(), ids[-7:].contiguous(), d[-7:].contiguous())
     assert torch.equal(dz[-7:], one) and not dz[:-7].any()
+
+
+def test_more_tokens_than_one_grid_holds():
+    T = 2 ** 28 + 5
+    z = torch.zeros(T, 2, dtype=torch.bfloat16, device="cuda")
+    z[::3, 1] = 1
+    ids, prob, _, _, _ = pqm.moe_gate(z, 1, pqm.SCORE_SOFTMAX, False)
+    assert torch.equal(ids[:, 0], z[:, 1].to(torch.int32))
+    want = torch.full((T,), 0.5, device="cuda")
+    want[::3] = 1 / (1 + 2.718281828459045 ** -1)
+    assert ((prob[:, 0] - want).abs() <= 64 * ref.U).all()

@@ -66,6 +66,13 @@ def test_decode_step(T):
     assert ((ref.f64(o["out"]) - y).abs() <= bound + ref.HALF_BF16 * (y.abs() + bound)).all()
 
 
+def test_no_tokens():
+    q, norm_w, gate_w = layer(True)
+    x, r = tokens(1, 15)
+    o = ml.nvfp4_moe_decode(x[:0], r[:0], norm_w, gate_w, *q, K, I)
+    assert o["out"].shape == (0, H) and o["h"].shape == (0, H) and o["ids"].shape == (0, K)
+
+
 def test_decode_step_captured():
     q, norm_w, gate_w = layer(True)
     x, r = tokens(2, 20)

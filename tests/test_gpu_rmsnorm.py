@@ -215,3 +215,16 @@ def test_more_than_2_31_values():
     assert torch.equal(dx[-few:], want) and not dx[:-few].any()
     want64 = ref.norm_backward(ref.f64(dy), ref.f64(alone[3]), ref.f64(w), ref.f64(alone[4]))
     assert ((ref.f64(dw) - want64[1]).abs() <= (few + 3) * ref.U * want64[3]).all()
+
+
+def test_more_rows_than_one_grid_holds():
+    rows, cols, few = 2 ** 26 + 5, 8, 7
+    x, r, w = inputs(few, cols, False, True, 78)
+    xg = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    rg = torch.zeros_like(xg)
+    at = torch.tensor([0, 1, 2 ** 25 - 1, 2 ** 25, 2 ** 26 - 1, 2 ** 26, rows - 1], device="cuda")
+    xg[at], rg[at] = cu(x), cu(r)
+    out = pqm.rmsnorm_quantize_mxfp8(xg, cu(w), 1e-6, residual=rg, quantize=False)
+    check(x, r, w, 1e-6, tuple(None if t is None else t[at] for t in out))
+    assert int((out[2] != 0).any(1).sum()) == few
+    assert int((out[4] == out[4][2]).sum()) + few == rows     # the zero rows, all alike
