@@ -71,6 +71,12 @@ def test_no_tokens():
     x, r = tokens(1, 15)
     o = ml.nvfp4_moe_decode(x[:0], r[:0], norm_w, gate_w, *q, K, I)
     assert o["out"].shape == (0, H) and o["h"].shape == (0, H) and o["ids"].shape == (0, K)
+    q, norm_w, gate_w = layer(False)
+    f = ml.mxfp8_moe_block_forward(x[:0], r[:0], norm_w, gate_w, *q, K, I)
+    assert f["out"].shape == (0, H) and float(f["loss"]) == 0 and not f["counts"].any()
+    one = torch.ones(1, device="cuda")
+    b = ml.moe_block_backward(f, norm_w, gate_w, x[:0], f["prob"], one, r[:0])
+    assert b["dx"].shape == (0, H) and not b["d_norm_w"].any() and not b["d_gate_w"].any()
 
 
 def test_decode_step_captured():
@@ -138,3 +144,40 @@ def test_training_step():
     assert ((ref.f64(b["dx"]) - dx).abs() <= ref.HALF_BF16 * (dx.abs() + bound) + bound).all()
     assert ((ref.f64(b["d_norm_w"]) - dw).abs()
             <= (slack * h.abs()).sum(0) + 1.01 * (T + 3) * ref.U * dw_size).all()
+
+
+def test_training_step_captured():
+    """Forward pass and gradients in one graph, the choice of experts, the
+    counts and the mask different at every replay."""
+    q, norm_w, gate_w = layer(False)
+    T = 33
+    x, r = tokens(T, 60)
+    mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+    dy, dh = tokens(T, 61)
+    d_prob = torch.randn(T, K, generator=torch.Generator().manual_seed(6)).cuda()
+    one = torch.ones(1, device="cuda")
+    plan = ml.block_plan(T, K, x.device)
+
+    def step():
+        f = ml.mxfp8_moe_block_forward(x, r, norm_w, gate_w, *q, K, I, 0.05, mask, plan)
+        b = ml.moe_block_backward(f, norm_w, gate_w, dy, d_prob, one, dh, 0.05, mask, plan)
+        return dict({n: f[n] for n in ("out", "h", "ids", "prob", "counts", "prob_sum", "loss")}, **b)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        a, b = tokens(T, 70 + i)
+        x.copy_(a)
+        r.copy_(b)
+        mask.fill_(1)
+        mask[T - 5 * i:] = 0
+        for t in out.values():
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(want[n], out[n]), (i, n)
