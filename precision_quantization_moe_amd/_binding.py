@@ -103,7 +103,8 @@ def _call(name: str, dev: torch.device, *args):
     """The entry point `name` on dev's current stream, with dev current: a
     kernel is launched on the current device.  (The raw stream getter takes a
     tenth of a microsecond; building a Stream object takes two, half the time
-    of a launch.)"""
+    of a launch.  The new tensors' sizes go to torch.empty as separate arguments
+    for the same reason: 1.3 us instead of 1.7.)"""
     i = dev.index
     fn = getattr(_lib or lib(), name)
     if i == torch.cuda.current_device():
@@ -248,14 +249,14 @@ def rmsnorm_quantize_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
             raise ValueError("residual: expected x's shape and device")
         if inplace and not residual.is_contiguous():
             raise ValueError("residual: must be contiguous to be updated in place")
-        total = residual if inplace else x.new_empty((R, C))
+        total = residual if inplace else x.new_empty(R, C)
     q = s = y = None
     if quantize:
-        q = torch.empty((R, C), dtype=torch.uint8, device=dev)
-        s = torch.empty((R, C // 32), dtype=torch.uint8, device=dev)
+        q = torch.empty(R, C, dtype=torch.uint8, device=dev)
+        s = torch.empty(R, C // 32, dtype=torch.uint8, device=dev)
     if keep_y or not quantize:
-        y = x.new_empty((R, C))
-    rstd = torch.empty((R,), dtype=torch.float32, device=dev)
+        y = x.new_empty(R, C)
+    rstd = torch.empty(R, dtype=torch.float32, device=dev)
     _call("pqm_rmsnorm_quantize_mxfp8", dev, _ptr(x), x.stride(0) if R > 1 else C, _ptr(residual),
           residual.stride(0) if residual is not None and R > 1 else C, _ptr(weight), wdt, R, C,
           eps, None if residual is None else _ptr(total), _ptr(y), _ptr(q), _ptr(s), _ptr(rstd))
@@ -278,10 +279,10 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
     _want(rstd, "rstd", torch.float32, (R,), dev)
     if d_sum is not None:
         _want(d_sum, "d_sum", torch.bfloat16, (R, C), dev)
-    dx = x.new_empty((R, C))
-    dw = torch.empty((C,), dtype=torch.float32, device=dev)
+    dx = x.new_empty(R, C)
+    dw = torch.empty(C, dtype=torch.float32, device=dev)
     ws_bytes = lib().pqm_rmsnorm_backward_workspace(R, C)
-    ws = torch.empty((max(ws_bytes, 16),), dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
     _call("pqm_rmsnorm_backward", dev, _ptr(dy), _ptr(x), _ptr(weight), wdt, _ptr(rstd),
           _ptr(d_sum), R, C, _ptr(dx), _ptr(dw), _ptr(ws), ws_bytes)
     return dx, dw
@@ -394,7 +395,7 @@ def moe_gemv_nvfp4(x: torch.Tensor, ids: torch.Tensor, w_q, w_scale, w_outer, N:
     rows, K, G, rps = _gemv_args(x, ids, N, w_q, w_scale, w_outer, w_rows_per_scale, divisor)
     dev = x.device
     odt = torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16
-    out = torch.empty((rows, N), dtype=odt, device=dev)
+    out = torch.empty(rows, N, dtype=odt, device=dev)
     _call("pqm_moe_gemv_nvfp4", dev, _ptr(x), _ptr(ids), rows, divisor, _ptr(w_q), _ptr(w_scale),
           _ptr(w_outer), rps, G, N, K, _ptr(out), out_dtype)
     return out
@@ -411,7 +412,7 @@ def moe_gemv_swiglu_nvfp4(x: torch.Tensor, ids: torch.Tensor, prob: torch.Tensor
     _want(prob, "prob", torch.float32, prob.shape, dev)
     if prob.numel() != rows:
         raise ValueError("prob: expected one value per row")
-    d = x.new_empty((rows, inter))
+    d = x.new_empty(rows, inter)
     _call("pqm_moe_gemv_swiglu_nvfp4", dev, _ptr(x), _ptr(ids), _ptr(prob), rows, divisor,
           _ptr(w_q), _ptr(w_scale), _ptr(w_outer), rps, G, inter, K, _ptr(d))
     return d
@@ -435,16 +436,16 @@ def moe_gate(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renormali
     _want(logits, "logits", logits.dtype, (T, E), dev)
     if mask is not None:
         _want(mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, (T,), dev)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-    prob = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    ids = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
+    prob = torch.empty(T, max(k, 0), dtype=torch.float32, device=dev)
     counts = prob_sum = loss = ws = None
     ws_bytes = 0
     if loss_coef is not None:
-        counts = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-        prob_sum = torch.empty((E,), dtype=torch.float32, device=dev)
-        loss = torch.empty((1,), dtype=torch.float32, device=dev)
+        counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
         ws_bytes = lib().pqm_moe_gate_workspace(T, E)
-        ws = torch.empty((max(ws_bytes, 4),), dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(ws_bytes, 4), dtype=torch.uint8, device=dev)
     _call("pqm_moe_gate", dev, _ptr(logits), zdt, _ptr(mask), T, E, k, score, int(renormalize),
           scale, _ptr(ids), _ptr(prob), loss_coef or 0.0, _ptr(counts), _ptr(prob_sum), _ptr(loss),
           _ptr(ws), ws_bytes)
@@ -481,7 +482,7 @@ def moe_gate_backward(logits: torch.Tensor, ids: torch.Tensor, d_prob: torch.Ten
         if d_loss.numel() != 1:
             raise ValueError("d_loss: expected one value")
     odt = zdt if out_dtype is None else out_dtype
-    dz = torch.empty((T, E), dtype=torch.float32 if odt == OUT_FP32 else torch.bfloat16,
+    dz = torch.empty(T, E, dtype=torch.float32 if odt == OUT_FP32 else torch.bfloat16,
                      device=dev)
     _call("pqm_moe_gate_backward", dev, _ptr(logits), zdt, _ptr(mask), T, E, k, score,
           int(renormalize), scale, _ptr(ids), _ptr(d_prob), loss_coef or 0.0, _ptr(counts),
