@@ -107,11 +107,12 @@ def _call(name: str, dev: torch.device, *args):
     for the same reason: 1.3 us instead of 1.7.)"""
     i = dev.index
     fn = getattr(_lib or lib(), name)
-    if i == torch.cuda.current_device():
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    stream = torch._C._cuda_getCurrentRawStream(i)
+    if i == torch._C._cuda_getDevice():
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(i):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+            code = fn(*args, stream)
     if code != 0:
         raise PqmError(code, name)
 
@@ -365,6 +366,9 @@ def moe_fc2_online_nvfp4_split(p: torch.Tensor, w_q, w_scale, w_outer, offsets: 
     return (y, gs, q, sb, ratio) if encodings else (y, gs)
 
 
+_GEMV_TYPES = (torch.int32, torch.uint8, torch.uint8, torch.float32)
+
+
 def _gemv_args(x, ids, rows_n, w_q, w_scale, w_outer, w_rows_per_scale, divisor):
     """Checked sizes of a few-row product: (rows, K, G, rows per scale) for
     weights of rows_n rows per expert."""
@@ -372,12 +376,12 @@ def _gemv_args(x, ids, rows_n, w_q, w_scale, w_outer, w_rows_per_scale, divisor)
     if divisor < 1 or rows_n < 1 or K < 32 or K % 32:
         raise PqmError(2, "pqm_moe_gemv_nvfp4")
     _want(x, "x", torch.bfloat16, (-(-rows // divisor), K), dev)
-    for t, what, dtype in ((ids, "ids", torch.int32), (w_q, "w_q", torch.uint8),
-                           (w_scale, "w_scale", torch.uint8), (w_outer, "w_outer", torch.float32)):
-        if t.dtype is not dtype or t.device != dev:
-            raise TypeError(f"{what}: expected {dtype} on {dev}, got {t.dtype} on {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: must be contiguous")
+    if (ids.dtype, w_q.dtype, w_scale.dtype, w_outer.dtype) != _GEMV_TYPES or not (
+            ids.device == w_q.device == w_scale.device == w_outer.device == dev):
+        raise TypeError(f"expected ids int32, w_q and w_scale uint8, w_outer float32 on {dev}")
+    if not (ids.is_contiguous() and w_q.is_contiguous() and w_scale.is_contiguous()
+            and w_outer.is_contiguous()):
+        raise ValueError("ids, w_q, w_scale, w_outer: must be contiguous")
     values = rows_n * (K // 2)
     G = w_q.numel() // values
     rps = w_rows_per_scale or rows_n
