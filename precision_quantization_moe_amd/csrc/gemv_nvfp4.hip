@@ -297,14 +297,19 @@ struct GvChunk {
 // largest stay exact; what smaller ones lose is below 2^-38 of the largest,
 // 2^14 times less than what the binary32 sum may round.
 //
+// STREAM: the weights (not their scales) pass by the L2, which then keeps x for
+// the workgroups of an expert: its fetches fall from 524 to 483 MB in the case
+// below.  It loses where a workgroup reads its weights again for every 16 rows.
+//
 // Measured, 37 tokens x top-8 of 64 experts, 5120 x 1280: gate_up 472 MB in
-// 101 us (4.7 TB/s; loads alone in this pattern 6.1), 29 tokens: down 59 us.
+// 90 us (5.2 TB/s; a copy here moves 5.1), 29 tokens: down 55 us.
 // What made it so, gate_up: 174 us with a row of weights in each lane (see
 // GvTurn); 150 -> 136 by waits that count loads (no load in a branch); 125
 // after the scales' loads became whole lines; 111 without a pass that found
-// each row's maximum first; 100 with four chunks' scales in one load.  The
-// rest is a short grid's last round and the start of each workgroup (ids, x).
-template <bool ACT, bool OUTF32>
+// each row's maximum first; 100 with four chunks' scales in one load; 90 with
+// STREAM.  The rest is a short grid's last round and the start of each
+// workgroup (ids, x).
+template <bool ACT, bool OUTF32, bool STREAM>
 __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
                                                         const int32_t *__restrict__ ids) {
   constexpr int COLS = gs_cols(ACT), OT = ACT ? 1 : 2;  // output columns; output tiles a wave
@@ -339,8 +344,9 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
     for (int t = 0; t < 2; ++t) {
       const uint32_t row = row0 + 16 * (t % OT);
       const int vq = (int)((row + (lane >> 3)) * (uint32_t)(K / 2) + 16 * (lane & 7) + oq);
-      b.q[t][0] = __builtin_amdgcn_raw_buffer_load_b128(t < OT ? wq : uq, vq, 0, 0);
-      b.q[t][1] = __builtin_amdgcn_raw_buffer_load_b128(t < OT ? wq : uq, vq + 8 * (K / 2), 0, 0);
+      b.q[t][0] = __builtin_amdgcn_raw_buffer_load_b128(t < OT ? wq : uq, vq, 0, STREAM ? 2 : 0);
+      b.q[t][1] = __builtin_amdgcn_raw_buffer_load_b128(t < OT ? wq : uq, vq + 8 * (K / 2), 0,
+                                                        STREAM ? 2 : 0);
     }
   };
   // The scales of four chunks, 64 bytes of a row in four lanes.
@@ -529,10 +535,18 @@ hipError_t launch_gemv(GemvArgs a, const int32_t *ids, bool act, bool f32, hipSt
   // 1280: 133 / 85.
   const int64_t tiles = (a.N + gs_cols(act) - 1) / gs_cols(act);
   if (a.K % 64 == 0 && tiles * (a.byrow ? a.rows : a.G) >= 160) {
-    const int lds = gs_lds(a.rows);
-    if (act) return gv_launch(a, gs_cols(true), 256, lds, k_gemv_staged<true, false>, ids, st);
-    if (f32) return gv_launch(a, gs_cols(false), 256, lds, k_gemv_staged<false, true>, ids, st);
-    return gv_launch(a, gs_cols(false), 256, lds, k_gemv_staged<false, false>, ids, st);
+    // Streamed weights while an expert's rows are one pass of 16 on average.
+    // Streamed against not, 2560 x 5120 gate_up (us), rows per expert 4.6:
+    // 87.5 / 96.3, 8: 37.0 / 38.2, 12: 49.5 / 51.0, 16: 62.1 / 62.6, 24: 75.5 /
+    // 75.2, 64: 115 / 113; 5120 x 1280 down, 16: 31.5 / 30.4, 64: 59.2 / 54.5.
+    const bool stream = a.rows < 16 * (int64_t)a.G;
+    const auto kernel = act   ? stream ? k_gemv_staged<true, false, true>
+                                       : k_gemv_staged<true, false, false>
+                        : f32 ? stream ? k_gemv_staged<false, true, true>
+                                       : k_gemv_staged<false, true, false>
+                        : stream ? k_gemv_staged<false, false, true>
+                                 : k_gemv_staged<false, false, false>;
+    return gv_launch(a, gs_cols(act), 256, gs_lds(a.rows), kernel, ids, st);
   }
   const int lds = 2 * a.rows;
   const bool w = a.K % 64 == 0;
