@@ -170,12 +170,12 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
 // length: past their end reads give 0 and writes are dropped, and a row that
 // is none is an empty buffer.
 //
-// Bound by memory: 16384 x 2048 with d_sum, 268 MB, 52 us with k_rmsnorm_dw's 4
-// (5.2 TB/s; a copy here moves 5.1).  70 us without the next row in flight and
+// Bound by memory: 16384 x 2048 with d_sum, 268 MB, 48.5 us with k_rmsnorm_dw's
+// 4 (5.5 TB/s; a copy here moves 5.1).  70 us without the next row in flight and
 // with weights read again for every row; two workgroups a CU, whose sums are
 // twice the bytes, 2 us more.  1021 x 7168: 18 us, half of it the start of two
 // kernels and their sums of dw.
-template <int TPR, int NC, bool WF32>
+template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
     const uint16_t *__restrict__ dy, const uint16_t *__restrict__ sx, const void *__restrict__ w,
     const float *__restrict__ rstd, const uint16_t *dsum, int64_t rows, int64_t C, uint16_t *dx,
@@ -200,9 +200,9 @@ __global__ __launch_bounds__(TPR == 512 ? 512 : 256, 2) void k_rmsnorm_backward(
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int o = (i * TPR + l) * 16;
-      r.g[i] = __builtin_amdgcn_raw_buffer_load_b128(g, o, 0, 0);
-      r.s[i] = __builtin_amdgcn_raw_buffer_load_b128(s, o, 0, 0);
-      r.d[i] = __builtin_amdgcn_raw_buffer_load_b128(d, o, 0, 0);
+      r.g[i] = __builtin_amdgcn_raw_buffer_load_b128(g, o, 0, STREAM ? 2 : 0);
+      r.s[i] = __builtin_amdgcn_raw_buffer_load_b128(s, o, 0, STREAM ? 2 : 0);
+      r.d[i] = __builtin_amdgcn_raw_buffer_load_b128(d, o, 0, STREAM ? 2 : 0);
     }
     r.rs = row < rows ? rstd[row] : 0.0f;
   };
@@ -361,12 +361,17 @@ hipError_t go_back(bool wf32, const uint16_t *dy, const uint16_t *x, const void 
   const dim3 grid((unsigned)norm_backward_groups(rows, C));
   const size_t lds = TPR == 64 ? 4 * C * sizeof(float) : 0;
   const dim3 block(TPR == 512 ? 512 : 256);
-  if (wf32)
-    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, true>), grid, block, lds, st, dy, x, w,
-                       rstd, dsum, rows, C, dx, part);
-  else
-    hipLaunchKernelGGL((k_rmsnorm_backward<TPR, NC, false>), grid, block, lds, st, dy, x, w,
-                       rstd, dsum, rows, C, dx, part);
+  // Streaming loads once the four tensors (2^25 values: 268 MB) outgrow the 256
+  // MB of the last cache.  Streaming against not, after a kernel that wrote dy,
+  // its time included (us): 16384 x 2048 63.5 / 66.3, 8192 x 7168 114 / 123, 32768
+  // x 2048 120 / 150; with nothing in the caches 16384 x 2048 48.5 / 51.8; below,
+  // 4096 x 2048 15.9 / 15.7, 1024 x 7168 21.2 / 18.2.
+  const bool stream = rows * C >= (1 << 25);
+  const auto kernel = wf32 ? stream ? k_rmsnorm_backward<TPR, NC, true, true>
+                                    : k_rmsnorm_backward<TPR, NC, true, false>
+                           : stream ? k_rmsnorm_backward<TPR, NC, false, true>
+                                    : k_rmsnorm_backward<TPR, NC, false, false>;
+  hipLaunchKernelGGL(kernel, grid, block, lds, st, dy, x, w, rstd, dsum, rows, C, dx, part);
   return hipGetLastError();
 }
 
