@@ -22,11 +22,17 @@ namespace {
 typedef uint32_t nb_u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t nb_u2 __attribute__((ext_vector_type(2)));
 
-// A store that streams past the caches, or an ordinary one.
+// A store or load that streams past the caches, or an ordinary one.
 template <bool STREAM, typename V>
 __device__ __forceinline__ void put(void *p, V v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<V *>(p));
   else *static_cast<V *>(p) = v;
+}
+
+template <bool STREAM>
+__device__ __forceinline__ nb_u4 get(const uint16_t *p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const nb_u4 *>(p));
+  else return *reinterpret_cast<const nb_u4 *>(p);
 }
 
 // 8 weights from column c on, as binary32.
@@ -71,7 +77,7 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // One row per TPR threads, NC chunks of 8 values per thread, kept in registers
 // between the sum of squares and the scaling, so each input is read once.
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
-// Bound by memory: 16384 x 2048 with residual, 235 MB, 47 us (5.0 TB/s; a copy
+// Bound by memory: 16384 x 2048 with residual, 235 MB, 42 us (5.6 TB/s; a copy
 // here moves 5.1); 8 x 2048 takes 4.7 us, the time of a launch.
 template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
@@ -91,11 +97,11 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     if (live && c < C) {
       a = *reinterpret_cast<const uint4 *>(x + row * ldx + c);
       if (r) {
-        const uint4 b = *reinterpret_cast<const uint4 *>(r + row * ldr + c);
-        a.x = pk_bf16_rne(bf16_lo_f32(a.x) + bf16_lo_f32(b.x), bf16_hi_f32(a.x) + bf16_hi_f32(b.x));
-        a.y = pk_bf16_rne(bf16_lo_f32(a.y) + bf16_lo_f32(b.y), bf16_hi_f32(a.y) + bf16_hi_f32(b.y));
-        a.z = pk_bf16_rne(bf16_lo_f32(a.z) + bf16_lo_f32(b.z), bf16_hi_f32(a.z) + bf16_hi_f32(b.z));
-        a.w = pk_bf16_rne(bf16_lo_f32(a.w) + bf16_lo_f32(b.w), bf16_hi_f32(a.w) + bf16_hi_f32(b.w));
+        const nb_u4 b = get<STREAM>(r + row * ldr + c);
+        a.x = pk_bf16_rne(bf16_lo_f32(a.x) + bf16_lo_f32(b[0]), bf16_hi_f32(a.x) + bf16_hi_f32(b[0]));
+        a.y = pk_bf16_rne(bf16_lo_f32(a.y) + bf16_lo_f32(b[1]), bf16_hi_f32(a.y) + bf16_hi_f32(b[1]));
+        a.z = pk_bf16_rne(bf16_lo_f32(a.z) + bf16_lo_f32(b[2]), bf16_hi_f32(a.z) + bf16_hi_f32(b[2]));
+        a.w = pk_bf16_rne(bf16_lo_f32(a.w) + bf16_lo_f32(b[3]), bf16_hi_f32(a.w) + bf16_hi_f32(b[3]));
       }
     }
     v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
@@ -333,10 +339,14 @@ template <int TPR, int NC>
 hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr,
                     const void *w, int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *y,
                     uint8_t *q, uint8_t *s, float *rstd, hipStream_t st) {
-  // Streaming stores from 2^21 values on: 16384 x 2048 with residual 51 -> 45.5
-  // us, 4096 x 7168 47 -> 42.6, 2048 x 2048 9.3 -> 8.1, 1024 x 2048 7.5 -> 7.0,
+  // Streaming from 2^21 values on.  The stores: 16384 x 2048 with residual 51 ->
+  // 47 us, 4096 x 7168 47 -> 42.6, 2048 x 2048 9.3 -> 8.1, 1024 x 2048 7.5 -> 7.0,
   // 256 x 2048 5.6 -> 5.9; with a gather that reads q and y afterwards the sum of
-  // the two stays within 4 % either way.
+  // the two stays within 4 % either way.  The residual, which a layer before
+  // wrote: 16384 x 2048 47.7 -> 41.7 with nothing in the caches; after a kernel that
+  // wrote x, 1024 to 32768 rows, its time included, within 1 % either way (all of
+  // it still in a cache: 2048 x 2048 6.3 -> 8.3).  x itself streamed as well took
+  // 44.2.
   const bool stream = rows * C >= (1 << 21);
   const auto kernel = wf32 ? stream ? k_rmsnorm_quant<TPR, NC, true, true>
                                     : k_rmsnorm_quant<TPR, NC, true, false>
