@@ -326,7 +326,7 @@ __global__ __launch_bounds__(1024) void k_moe_balance(
 }
 
 // The gradient, laid out as the forward kernel.  16384 x 128 7.9 us, 4093 x 256
-// in bf16 5.6 (floors 3.5 and 0.8; a launch takes about 4.5).  Every load goes
+// in bf16 5.7 (floors 3.5 and 0.9; a launch takes about 4.5).  Every load goes
 // out before the first is used (10.1 and 8.5 us with the counts, the ids and
 // the chosen logits waited for in turn); comparing each expert with each of the
 // k ids instead of the row in LDS took 0.8 us more.
@@ -375,10 +375,18 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       top = group_fmax<LPT>(top);
       if (!(top > -__builtin_inff())) top = 0.0f;
     }
-    float sum = 0.0f;
+    // slope: v (1 - v) of a sigmoid, the same for z and -z; 1 - v of a rounded v
+    // would have no digits left near 1
+    float sum = 0.0f, slope[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = SOFTMAX ? exp_f32(v[i] - top) : sigmoid(v[i]);
+      if constexpr (SOFTMAX) {
+        v[i] = exp_f32(v[i] - top);
+      } else {
+        const float t = exp_f32(-fabsf(v[i])), r = __builtin_amdgcn_rcpf(1.0f + t);
+        slope[i] = t * r * r;
+        v[i] = v[i] < 0.0f ? t * r : r;
+      }
       if (i * LPT + l >= E) v[i] = 0.0f;
       sum += v[i];
     }
@@ -403,7 +411,9 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       const float total = group_sum<LPT>(my_v);
       const float dot = group_sum<LPT>(my_d * my_v);
       const float it = total > 0.0f ? 1.0f / total : 0.0f;
-      my_d = (my_d - dot * it) * it;
+      // d (total - v) - (dot - d v) over total^2: 0 of itself where k is 1, while
+      // d - dot / total leaves a rounding of d
+      my_d = (my_d * (total - my_v) - (dot - my_d * my_v)) * it * it;
     }
     // An expert chosen twice gets the sum, in both its places; then each place
     // lays its value where the expert's lane finds it.
@@ -439,7 +449,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       gz[i] = SOFTMAX ? v[i] * (u[i] + h[i] - dot)
-                      : v[i] * (1.0f - v[i]) * (u[i] + (h[i] - dot) * inv);
+                      : slope[i] * (u[i] + (h[i] - dot) * inv);
       if (!valid) gz[i] = 0.0f;
     }
     if (out_f32) {

@@ -196,6 +196,31 @@ def test_backward_of_a_repeated_expert_adds_up(softmax):
     assert torch.allclose(a, b, rtol=0, atol=float(64 * ref.U * 4 * d.abs().max()))
 
 
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("E", [60, 300])
+def test_renormalized_single_choice_has_no_gradient(softmax, E):
+    """prob is 1 whatever the logits are: not a rounding may be left."""
+    z = logits(50, E, False, 8).cuda()
+    ids, _, _, _, _ = pqm.moe_gate(z, 1, score_of(softmax))
+    d = torch.randn(50, 1, generator=torch.Generator().manual_seed(3)).cuda()
+    assert not pqm.moe_gate_backward(z, ids, d, score_of(softmax)).any()
+
+
+@pytest.mark.parametrize("E", [60, 300])
+def test_gradient_of_sigmoids_near_one(E):
+    """d v (1 - v) keeps its relative accuracy where v rounds to 1.  The two
+    factors keep 4 U from the exponential and 5 U from the quotient each, three
+    products 3 U: 32 U holds all."""
+    z = torch.linspace(-20, 20, 40 * E).view(40, E)
+    ids, _, _, _, _ = pqm.moe_gate(z.cuda(), 4, pqm.SCORE_SIGMOID, False)
+    d = torch.randn(40, 4, generator=torch.Generator().manual_seed(4))
+    dz = pqm.moe_gate_backward(z.cuda(), ids, d.cuda(), pqm.SCORE_SIGMOID, False)
+    v = z.double()
+    want = torch.zeros(40, E, dtype=torch.float64).scatter_(1, ids.cpu().long(), d.double()) * \
+        torch.sigmoid(v) * torch.sigmoid(-v)
+    assert ((ref.f64(dz) - want).abs() <= 32 * ref.U * want.abs()).all()
+
+
 def test_python_form_refuses():
     z = torch.zeros(4, 8).cuda()
     with pytest.raises(pqm.PqmError):
