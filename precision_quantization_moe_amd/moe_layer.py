@@ -219,6 +219,9 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
       d_prob [T, k] f32  gradient of the routing probabilities
       d_loss [1] f32     gradient of the balance loss
       d_h [T, H] bf16    gradient of h past the norm (may be None)
+    d_logits enters its two products in bf16, their operand type, and what comes
+    back through the gate is rounded to bf16 before and after it joins dy, the
+    type that rmsnorm_backward takes; all sums are binary32.
     Returns dict(dx [T, H] bf16, the gradient of x and of residual; d_norm_w
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
