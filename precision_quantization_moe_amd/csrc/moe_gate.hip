@@ -116,8 +116,8 @@ __device__ __forceinline__ float exp_f32(float x) {
 // "already chosen").  -0 counts as +0; a NaN, outside the contract, ranks as
 // -inf, so that the ids stay experts whatever the logits hold.
 __device__ __forceinline__ uint32_t logit_key(float z) {
-  const uint32_t u = __float_as_uint(z == z ? z + 0.0f : -__builtin_inff());
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(fmaxf(z, -__builtin_inff()) + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
@@ -131,12 +131,13 @@ __device__ __forceinline__ float sigmoid(float z) {
 
 // LPT lanes hold one token, VPL logits each (expert i LPT + lane); the choice
 // takes k turns of a maximum over the keys, the lowest index that has it, and
-// its removal.  Bound by those turns' vector instructions (about 50 a turn for
+// its removal.  Bound by those turns' vector instructions (about 40 a turn for
 // 128 experts, shared by four tokens) and, for few tokens, by the start of a
-// kernel: 16384 x 128, top-8, with the loss 14.5 us (k_moe_balance 4 of them,
-// floor 1.9), 16 x 256 without 5.0.  SUMS: each
-// workgroup also leaves its counts and share sums in part_cnt / part_sum
-// [gridDim.x][E] (and its valid tokens in part_valid).
+// kernel: 16384 x 128, top-8, with the loss 14.0 us (k_moe_balance 4 of them,
+// floor 1.8), 16 x 256 without 4.6; 14.4 and 5.0 with the removal found by
+// comparing each index again.  SUMS: each workgroup also leaves its counts and
+// share sums in part_cnt / part_sum [gridDim.x][E] (and its valid tokens in
+// part_valid).
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
 __global__ __launch_bounds__(1024) void k_moe_gate(
     const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
@@ -173,24 +174,35 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
       key[i] = in ? logit_key(v[i]) : 0u;
     }
     int my_id = 0;
-    float my_z = -__builtin_inff(), top = 0.0f;
+    uint32_t my_key = 0, top_key = 0;
     for (int j = 0; j < k; ++j) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = max(m, key[i]);
       m = group_max<LPT>(m);
-      uint32_t at = UINT32_MAX;
+      // this lane's first expert that has the maximum, and the lowest lane's of
+      // them: the conditions stay in scalar registers
+      uint32_t mine_at = UINT32_MAX;
+      bool hit[VPL], seen = false;
 #pragma unroll
-      for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)(i * LPT + l) : at;
-      at = group_min<LPT>(at);
+      for (int i = 0; i < VPL; ++i) {
+        const bool eq = key[i] == m;
+        hit[i] = eq && !seen;
+        seen = seen || eq;
+        mine_at = hit[i] ? (uint32_t)(i * LPT + l) : mine_at;
+      }
+      const uint32_t at = group_min<LPT>(mine_at);
+      const bool won = at == mine_at;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = (uint32_t)(i * LPT + l) == at ? 0u : key[i];
-      if (j == 0) top = key_logit(m);
+      for (int i = 0; i < VPL; ++i) key[i] = hit[i] && won ? 0u : key[i];
+      if (j == 0) top_key = m;
       if (l == j) {
         my_id = (int)at;
-        my_z = key_logit(m);
+        my_key = m;
       }
     }
+    float top = key_logit(top_key);
+    const float my_z = l < k ? key_logit(my_key) : -__builtin_inff();
     // shares: exp(z - top) or sigmoid(z), and their sum; an all -inf row has none
     if (!(top > -__builtin_inff())) top = 0.0f;
     float sum = 0.0f;
