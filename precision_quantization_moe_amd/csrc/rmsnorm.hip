@@ -7,7 +7,10 @@
 // rounded first because that rounded sum is what the residual stream carries
 // on and what the backward pass reads again; y is rounded to bf16 before the
 // encoding, so that the bytes are those of pqm_quantize_mxfp8 of the y that a
-// caller may keep.  Squares and their sum are binary32.
+// caller may keep.  Eight values' squares are added in binary32, the rest and
+// the root are binary64, and a product of binary32 that lies within its own
+// error of the middle of two bf16 values is formed again in binary64: y is the
+// nearest bf16 value but for what the sums of eight round.
 //
 // Backward (straight through both roundings), g = dy w, h = s rstd:
 //   dx = rstd (g - h mean(g h)) + d_sum,   dw_c = sum over rows of dy h.
@@ -54,16 +57,54 @@ __device__ __forceinline__ void load_w8(const void *__restrict__ w, int64_t c, f
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+__device__ __forceinline__ double join(uint32_t lo, uint32_t hi) {
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// v of another lane of the same 16, of the other 16 of 32, of the other 32.
+template <int CTRL>
+__device__ __forceinline__ float other(float v) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double other(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xF, 0xF, false);
+  return join(lo, hi);
+}
+__device__ __forceinline__ float add_halves(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t w = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ double add_halves(double v) {
+  uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const auto al = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto ah = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  u = __builtin_bit_cast(uint64_t, join(al[0], ah[0]) + join(al[1], ah[1]));
+  const auto bl = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto bh = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  return join(bl[0], bh[0]) + join(bl[1], bh[1]);
+}
+
+// Sum over a wave, the same in every lane, through the vector unit alone: six
+// shuffles, which pass through LDS, take about four times as long.
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+  v += other<0xB1>(v);   // lane ^ 1
+  v += other<0x4E>(v);   // lane ^ 2
+  v += other<0x141>(v);  // 7 - lane
+  v += other<0x140>(v);  // 15 - lane
+  return add_halves(v);
 }
 
 // Sum over the TPR threads of a row (64: one wave; 256: the workgroup, through
 // `red`, 4 slots).  Every thread of the workgroup must call it.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *red) {
+__device__ __forceinline__ double row_sum(double v, double *red) {
   v = wave_sum(v);
   if constexpr (TPR == 64) return v;
   __syncthreads();  // the slots' last readers are done
@@ -72,24 +113,46 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// 1 / sqrt(m): the hardware's estimate (about 2^-27) and one Newton step.
+__device__ __forceinline__ double inverse_root(double m) {
+  const double r = __builtin_amdgcn_rsq(m);
+  return __builtin_fma(0.5 * r, __builtin_fma(-m * r, r, 1.0), r);
+}
+
+// At most 6 where v, nearest but for 3 units in the last place, is so close to
+// the middle of two bf16 values that those units may decide.
+__device__ __forceinline__ uint16_t to_middle(float v) {
+  return (uint16_t)((uint16_t)__float_as_uint(v) + (uint16_t)0x8003);
+}
+
+// The binary32 value from which d rounds to bf16 as it would at once: where the
+// nearest one is the middle of two, its neighbour on d's side.
+__device__ __forceinline__ float before_bf16(double d) {
+  const float f = (float)d;
+  const double a = __builtin_fabs((double)f), b = __builtin_fabs(d);
+  const uint32_t u = __float_as_uint(f);
+  return (u & 0xFFFFu) == 0x8000u && a != b ? __uint_as_float(a < b ? u + 1 : u - 1) : f;
+}
+
 }  // namespace
 
 // One row per TPR threads, NC chunks of 8 values per thread, kept in registers
 // between the sum of squares and the scaling, so each input is read once.
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
-// Bound by memory: 16384 x 2048 with residual, 235 MB, 42 us (5.6 TB/s; a copy
-// here moves 5.1); 8 x 2048 takes 4.7 us, the time of a launch.
+// Bound by memory: 16384 x 2048 with residual, 235 MB, 41.5 us (5.7 TB/s; a copy
+// here moves 5.1); 8 x 2048 takes 4.75 us, the time of a launch.  The binary64
+// sum, root and middles cost 0.1 us there and 0.4 for 256 to 2048 rows.
 template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
-    int64_t rows, int64_t C, float eps, uint16_t *sum, uint16_t *__restrict__ y,
+    int64_t rows, int64_t C, double inv_c, float eps, uint16_t *sum, uint16_t *__restrict__ y,
     uint8_t *__restrict__ q, uint8_t *__restrict__ s, float *__restrict__ rstd_out) {
-  __shared__ float red[4];
+  __shared__ double red[4];
   const int l = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   const bool live = row < rows;  // with 64 threads a row: the last workgroup's spare waves
   uint32_t v[NC][4];
-  float sq = 0.0f;
+  double sq = 0.0;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int64_t c = ((int64_t)i * TPR + l) * 8;
@@ -105,12 +168,13 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
       }
     }
     v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+    float pair[4];  // squares of bf16 values are exact
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float lo = bf16_lo_f32(v[i][j]), hi = bf16_hi_f32(v[i][j]);
-      sq += lo * lo;
-      sq += hi * hi;
+      pair[j] = __builtin_fmaf(hi, hi, lo * lo);
     }
+    sq += (pair[0] + pair[1]) + (pair[2] + pair[3]);
   }
   if (sum) {
 #pragma unroll
@@ -120,25 +184,24 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
         put<STREAM>(sum + row * C + c, nb_u4{v[i][0], v[i][1], v[i][2], v[i][3]});
     }
   }
-  const float total = row_sum<TPR>(sq, red);
-  float rstd = 1.0f / sqrtf(total / (float)C + eps);
+  const double total = row_sum<TPR>(sq, red);
+  double root = inverse_root(total * inv_c + eps);
   // Values from about 2^63 on square beyond binary32: sum (s 2^-80)^2 then,
   // at most 2^15 (2^48)^2; eps, at most 1, is far below the last bit of such a
   // mean.
-  if (!(total < __builtin_inff())) {
-    float t = 0.0f;
+  if (!(total < (double)__builtin_inff())) {
+    double t = 0.0;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float lo = bf16_lo_f32(v[i][j]) * 0x1p-80f, hi = bf16_hi_f32(v[i][j]) * 0x1p-80f;
-        t += lo * lo;
-        t += hi * hi;
+        t += __builtin_fmaf(hi, hi, lo * lo);
       }
     // with one wave a row the other waves' rows need not take this branch
-    t = row_sum<TPR>(t, red);
-    rstd = 0x1p-80f / sqrtf(t / (float)C);
+    root = 0x1p-80 * inverse_root(row_sum<TPR>(t, red) * inv_c);
   }
+  const float rstd = (float)root;
   if (!live) return;
   if (rstd_out && l == 0) rstd_out[row] = rstd;
 #pragma unroll
@@ -147,11 +210,22 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     if (c >= C) continue;  // whole quads: C is a multiple of 32 where q is written
     float wf[8];
     load_w8<WF32>(w, c, wf);
+    float f[8];
+    uint16_t close = 0xFFFF;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = (j & 1 ? bf16_hi_f32(v[i][j / 2]) : bf16_lo_f32(v[i][j / 2])) * rstd * wf[j];
+      close = min(close, to_middle(f[j]));
+    }
+    if (close <= 6) {  // one lane in a thousand; all eight, which keeps the code short
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = before_bf16((double)(j & 1 ? bf16_hi_f32(v[i][j / 2]) : bf16_lo_f32(v[i][j / 2])) *
+                           (double)wf[j] * root);
+    }
     uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pk_bf16_rne(bf16_lo_f32(v[i][j]) * rstd * wf[2 * j],
-                         bf16_hi_f32(v[i][j]) * rstd * wf[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) o[j] = pk_bf16_rne(f[2 * j], f[2 * j + 1]);
     if (y) put<STREAM>(y + row * C + c, nb_u4{o[0], o[1], o[2], o[3]});
     if (q) {
       uint32_t mm = pk_max_u16(pk_max_u16(o[0] & 0x7FFF7FFFu, o[1] & 0x7FFF7FFFu),
@@ -357,7 +431,7 @@ hipError_t go_quant(bool wf32, const uint16_t *x, int64_t ldx, const uint16_t *r
   for (int64_t r0 = 0; r0 < rows; r0 += most) {
     const int64_t n = rows - r0 < most ? rows - r0 : most, o = r0 * C;
     hipLaunchKernelGGL(kernel, dim3((unsigned)((n + RPB - 1) / RPB)), dim3(256), 0, st,
-                       x + r0 * ldx, ldx, r ? r + r0 * ldr : r, ldr, w, n, C, eps,
+                       x + r0 * ldx, ldx, r ? r + r0 * ldr : r, ldr, w, n, C, 1.0 / (double)C, eps,
                        sum ? sum + o : sum, y ? y + o : y, q ? q + o : q, s ? s + o / 32 : s,
                        rstd ? rstd + r0 : rstd);
   }

@@ -115,6 +115,26 @@ def test_zero_tiny_and_huge_rows(cols):
     assert not out[2][0].any() and not out[1][0].any()
 
 
+@pytest.mark.parametrize("cols", [96, 2048, 5000])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_y_is_the_nearest_value(cols, wf32):
+    """Whole numbers up to 255: every sum of squares is exact, so only y's own
+    rounding is left, and it has to be the binary64 product's."""
+    g = torch.Generator().manual_seed(cols)
+    rows = 2 ** 21 // cols
+    x = torch.randint(-255, 256, (rows, cols), generator=g).to(torch.bfloat16)
+    w = 1 + 0.3 * torch.randn(cols, generator=g)
+    w = w if wf32 else w.to(torch.bfloat16)
+    _, _, y, _, rstd = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), 2.0 ** -20, quantize=False)
+    mean = ref.f64(x).square().mean(1)
+    root = (mean + 2.0 ** -20).pow(-0.5)
+    assert torch.equal(rstd.cpu(), root.float())
+    bits = (ref.f64(x) * ref.f64(w) * root[:, None]).contiguous().view(torch.int64)
+    bits = bits + (2 ** 44 - 1) + ((bits >> 45) & 1)     # binary64 to 8 significant bits, nearest
+    want = (bits & ~(2 ** 45 - 1)).view(torch.float64)
+    assert torch.equal(ref.f64(y), want)
+
+
 def test_no_rows():
     x = torch.zeros(0, 64, dtype=torch.bfloat16).cuda()
     w = torch.ones(64).cuda()
