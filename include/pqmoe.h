@@ -562,13 +562,12 @@ pqm_status pqm_moe_combine(const uint16_t *y_rows, const int32_t *slot,
  * sum, y and rstd may be NULL, and so may the pair q, s; one of y and q is
  * required (PQM_ERR_NULL).  sum may be the memory of x or of residual, whose
  * row stride must then be cols (PQM_ERR_SHAPE), and is updated in place; no
- * other output may overlap an input.  Eight squares are added in binary32,
- * the rest and the root are binary64, and y is the nearest bf16 value of the
- * product but for what the sums of eight round.  Rows whose squares leave
- * binary32 (values from about 2^63 on) are handled.  x + residual and y must
- * stay within the bf16 range.
+ * other output may overlap an input.  The sum and the root are binary64, and y
+ * is the nearest bf16 value of the product; rows whose squares leave binary32
+ * (values from about 2^63 on) are handled.  x + residual and y must stay
+ * within the bf16 range.
  * Requires cols % 8 == 0 (% 32 with q, s), cols <= 16384, rows < 2^31,
- * ldx, ldr >= cols, 2^-100 <= eps <= 1 (PQM_ERR_SHAPE); x, residual,
+ * ldx, ldr >= cols, 2^-100 <= eps < infinity (PQM_ERR_SHAPE); x, residual,
  * weight, sum, y and the strides 16-byte aligned, q 8-byte, rstd 4-byte
  * (PQM_ERR_ALIGN).
  */

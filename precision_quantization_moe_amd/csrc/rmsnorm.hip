@@ -7,10 +7,10 @@
 // rounded first because that rounded sum is what the residual stream carries
 // on and what the backward pass reads again; y is rounded to bf16 before the
 // encoding, so that the bytes are those of pqm_quantize_mxfp8 of the y that a
-// caller may keep.  Eight values' squares are added in binary32, the rest and
-// the root are binary64, and a product of binary32 that lies within its own
-// error of the middle of two bf16 values is formed again in binary64: y is the
-// nearest bf16 value but for what the sums of eight round.
+// caller may keep.  The sum of squares and the root are binary64 (no square
+// overflows, and their cost hides behind the loads), and a binary32 product that
+// lies within its own error of the middle of two bf16 values is formed again in
+// binary64: y is the nearest bf16 value.
 //
 // Backward (straight through both roundings), g = dy w, h = s rstd:
 //   dx = rstd (g - h mean(g h)) + d_sum,   dw_c = sum over rows of dy h.
@@ -141,7 +141,7 @@ __device__ __forceinline__ float before_bf16(double d) {
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
 // Bound by memory: 16384 x 2048 with residual, 235 MB, 41.5 us (5.7 TB/s; a copy
 // here moves 5.1); 8 x 2048 takes 4.75 us, the time of a launch.  The binary64
-// sum, root and middles cost 0.1 us there and 0.4 for 256 to 2048 rows.
+// sum, root and middles cost 0.1 us there and 0.5 for 256 to 2048 rows.
 template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
@@ -168,13 +168,12 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
       }
     }
     v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
-    float pair[4];  // squares of bf16 values are exact
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float lo = bf16_lo_f32(v[i][j]), hi = bf16_hi_f32(v[i][j]);
-      pair[j] = __builtin_fmaf(hi, hi, lo * lo);
+      const double lo = bf16_lo_f32(v[i][j]), hi = bf16_hi_f32(v[i][j]);
+      sq = __builtin_fma(lo, lo, sq);
+      sq = __builtin_fma(hi, hi, sq);
     }
-    sq += (pair[0] + pair[1]) + (pair[2] + pair[3]);
   }
   if (sum) {
 #pragma unroll
@@ -185,22 +184,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     }
   }
   const double total = row_sum<TPR>(sq, red);
-  double root = inverse_root(total * inv_c + eps);
-  // Values from about 2^63 on square beyond binary32: sum (s 2^-80)^2 then,
-  // at most 2^15 (2^48)^2; eps, at most 1, is far below the last bit of such a
-  // mean.
-  if (!(total < (double)__builtin_inff())) {
-    double t = 0.0;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = bf16_lo_f32(v[i][j]) * 0x1p-80f, hi = bf16_hi_f32(v[i][j]) * 0x1p-80f;
-        t += __builtin_fmaf(hi, hi, lo * lo);
-      }
-    // with one wave a row the other waves' rows need not take this branch
-    root = 0x1p-80 * inverse_root(row_sum<TPR>(t, red) * inv_c);
-  }
+  const double root = inverse_root(total * inv_c + eps);  // no square of bf16 leaves binary64
   const float rstd = (float)root;
   if (!live) return;
   if (rstd_out && l == 0) rstd_out[row] = rstd;
@@ -219,9 +203,11 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     }
     if (close <= 6) {  // one lane in a thousand; all eight, which keeps the code short
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f[j] = before_bf16((double)(j & 1 ? bf16_hi_f32(v[i][j / 2]) : bf16_lo_f32(v[i][j / 2])) *
-                           (double)wf[j] * root);
+      for (int j = 0; j < 8; ++j) {
+        uint32_t u = v[i][j / 2];
+        asm("" : "+v"(u));  // or the sum's conversions would be kept for here, 16 registers a chunk
+        f[j] = before_bf16((double)(j & 1 ? bf16_hi_f32(u) : bf16_lo_f32(u)) * (double)wf[j] * root);
+      }
     }
     uint32_t o[4];
 #pragma unroll
@@ -501,7 +487,7 @@ pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint
   if ((q || s) && cols % 32) return PQM_ERR_SHAPE;
   // in place only where the rows of sum lie where they were read
   if (sum && ((sum == x && ldx != cols) || (sum == residual && ldr != cols))) return PQM_ERR_SHAPE;
-  if (!(eps >= 0x1p-100f) || !(eps <= 1.0f)) return PQM_ERR_SHAPE;
+  if (!(eps >= 0x1p-100f) || !(eps < __builtin_inff())) return PQM_ERR_SHAPE;
   if (rows == 0 || cols == 0) return PQM_OK;
   if (!x || !weight || (!q && !y) || (q == nullptr) != (s == nullptr)) return PQM_ERR_NULL;
   if (!al(x, 16) || ldx % 8 || !al(weight, 16) || !al(sum, 16) || !al(y, 16) || !al(q, 8) ||

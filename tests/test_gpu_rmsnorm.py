@@ -118,8 +118,8 @@ def test_zero_tiny_and_huge_rows(cols):
 @pytest.mark.parametrize("cols", [96, 2048, 5000])
 @pytest.mark.parametrize("wf32", [False, True])
 def test_y_is_the_nearest_value(cols, wf32):
-    """Whole numbers up to 255: every sum of squares is exact, so only y's own
-    rounding is left, and it has to be the binary64 product's."""
+    """Whole numbers up to 255: every sum of squares is exact in binary64, so
+    only y's own rounding is left, and it has to be the binary64 product's."""
     g = torch.Generator().manual_seed(cols)
     rows = 2 ** 21 // cols
     x = torch.randint(-255, 256, (rows, cols), generator=g).to(torch.bfloat16)
@@ -248,3 +248,12 @@ def test_more_rows_than_one_grid_holds():
     check(x, r, w, 1e-6, tuple(None if t is None else t[at] for t in out))
     assert int((out[2] != 0).any(1).sum()) == few
     assert int((out[4] == out[4][2]).sum()) + few == rows     # the zero rows, all alike
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -100, 2.0 ** 40])
+def test_eps_of_any_size(eps):
+    x, r, w = inputs(20, 1024, False, True, 79)
+    x[3], r[3] = x[3] * 2.0 ** 100, 0
+    x[4], r[4] = x[4] * 2.0 ** -60, 0
+    out = pqm.rmsnorm_quantize_mxfp8(cu(x), cu(w), eps, residual=cu(r), keep_y=True)
+    check(x, r, w, eps, out)
