@@ -102,10 +102,12 @@ __device__ __forceinline__ float load_logit(const __amdgpu_buffer_rsrc_t &r, uin
   return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(2 * i), 0, 0) << 16);
 }
 
-// e^x to about 2 ulp: 2^t with t = x log2(e) in two parts, the second through
-// its first-order term.  Beyond +-200 the result is inf or 0 in any case.
+// e^x of x <= 0 to about 2 ulp: 2^t with t = x log2(e) in two parts, the second
+// through its first-order term.  Results below 2^-126 are 0; below -200 they are
+// so in any case.  (Above 0 the first part may overflow, where the correction
+// would make a NaN of it.)
 __device__ __forceinline__ float exp_f32(float x) {
-  x = fminf(fmaxf(x, -200.0f), 200.0f);
+  x = fmaxf(x, -200.0f);
   const float t = x * 0x1.715476p+0f;
   const float r = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
   const float p = __builtin_amdgcn_exp2f(t);
@@ -123,8 +125,10 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// Through the exponential of -|z|, which cannot overflow.
 __device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
+  const float t = exp_f32(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + t);
+  return z < 0.0f ? t * r : r;
 }
 
 }  // namespace
