@@ -24,6 +24,7 @@ namespace {
 
 constexpr int GATE_MAX_EXPERTS = 1024;
 constexpr int GATE_MAX_K = 16;
+constexpr int64_t GATE_MAX_VALUES = 0x7FFFFFFF;  // tokens (k + 1)
 constexpr int64_t GATE_GROUPS = 256;  // workgroups whose partial sums the last kernel joins
 
 template <int J>
@@ -592,7 +593,7 @@ pqm_status gate_shape(pqm_dtype dtype, pqm_score score, int64_t T, int64_t E, in
   if (renorm != 0 && renorm != 1) return PQM_ERR_ENUM;
   if (T < 0 || E < 1 || E > GATE_MAX_EXPERTS || k < 1 || k > GATE_MAX_K || k > E)
     return PQM_ERR_SHAPE;
-  if (T * (k + 1) > (int64_t)0x7FFFFFFF) return PQM_ERR_SHAPE;
+  if (T > GATE_MAX_VALUES / (k + 1)) return PQM_ERR_SHAPE;  // the product may leave 64 bits
   return PQM_OK;
 }
 
@@ -602,7 +603,9 @@ pqm_status gate_shape(pqm_dtype dtype, pqm_score score, int64_t T, int64_t E, in
 extern "C" {
 
 size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts) {
-  if (tokens < 0 || num_experts < 1 || num_experts > pqm::GATE_MAX_EXPERTS) return 0;
+  if (tokens < 0 || tokens > pqm::GATE_MAX_VALUES || num_experts < 1 ||
+      num_experts > pqm::GATE_MAX_EXPERTS)
+    return 0;
   return pqm::gate_workspace_bytes(tokens, num_experts);
 }
 

@@ -500,7 +500,7 @@ pqm_status pqm_rmsnorm_quantize_mxfp8(const uint16_t *x, int64_t ldx, const uint
 }
 
 size_t pqm_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || cols > pqm::NORM_MAX_COLS) return 0;
+  if (rows <= 0 || rows >= ((int64_t)1 << 31) || cols <= 0 || cols > pqm::NORM_MAX_COLS) return 0;
   return (size_t)(pqm::norm_backward_groups(rows, cols) * cols) * sizeof(float);
 }
 
