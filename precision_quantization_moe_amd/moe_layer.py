@@ -156,6 +156,22 @@ def block_plan(tokens: int, k: int, device):
                 row=torch.arange(tokens, **i32).view(tokens, 1))
 
 
+def _plan(plan, tokens: int, k: int, device):
+    """plan, or a new one without it.  A plan for other sizes would send the
+    products past their rows or leave some unwritten, so its shapes are
+    compared on the host (what it holds is on the device and not read)."""
+    if not plan:
+        return block_plan(tokens, k, device)
+    want = dict(off=((2,), torch.int64), slot=((tokens, k), torch.int32),
+                row=((tokens, 1), torch.int32))
+    for name, (shape, dtype) in want.items():
+        t = plan.get(name)
+        if (t is None or t.shape != shape or t.dtype is not dtype or t.device != device
+                or not t.is_contiguous()):
+            raise ValueError(f"plan: {name} is not of block_plan({tokens}, {k}, {device})")
+    return plan
+
+
 def _router_logits(y, gate_w, off):
     """y [T, H] times the router's weight [E, H], both bf16, in binary32."""
     E, H = gate_w.shape
@@ -175,7 +191,7 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
     device).  Returns dict(out [T, H] bf16, h (the new residual stream), y,
     ids, prob, d)."""
     T, H = x.shape
-    plan = plan or block_plan(T, k, x.device)
+    plan = _plan(plan, T, k, x.device)
     _, _, y, h, _ = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, quantize=False)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, _, _, _ = b.moe_gate(logits, k, score, renormalize, scale)
@@ -197,7 +213,7 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
     Returns the experts' dict and h, y, rstd, logits,
     ids, prob, counts, prob_sum, loss."""
     T = x.shape[0]
-    plan = plan or block_plan(T, k, x.device)
+    plan = _plan(plan, T, k, x.device)
     qx, sx, y, h, rstd = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, keep_y=True)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, counts, prob_sum, loss = b.moe_gate(logits, k, score, renormalize, scale, mask,
@@ -226,7 +242,7 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
     E = gate_w.shape[0]
-    plan = plan or block_plan(T, saved["ids"].shape[1], dy.device)
+    plan = _plan(plan, T, saved["ids"].shape[1], dy.device)
     off = plan["off"]
     dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,
                              mask, loss_coef, saved["counts"], d_loss, out_dtype=b.OUT_BF16)

@@ -5,8 +5,10 @@ from __future__ import annotations
 import ctypes
 
 import pytest
+import torch
 
 import precision_quantization_moe_amd as pqm
+from precision_quantization_moe_amd import moe_layer as ml
 
 A = ctypes.c_void_p(0x10000)
 
@@ -31,3 +33,82 @@ def test_workspace_queries_of_sizes_that_no_call_takes():
     assert L.pqm_moe_gate_workspace((1 << 30) - 1, 64) == L.pqm_moe_gate_workspace(1 << 20, 64) > 0
     assert L.pqm_rmsnorm_backward_workspace((1 << 31) - 1, 64) == \
         L.pqm_rmsnorm_backward_workspace(1 << 20, 64) > 0
+
+
+# The block passes look over what they are given before any call, so that their
+# refusals show on the host too: T tokens of H values, E experts of I, top-K.
+T, H, E, I, K = 6, 64, 8, 32, 2
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+def nvfp4_weights(e=E):
+    return (u8(e * 2 * I, H // 2), u8(e * 2 * I, H // 16), torch.ones(e),
+            u8(e * H, I // 2), u8(e * H, I // 16), torch.ones(e))
+
+
+def mxfp8_weights(e=E):
+    return u8(e * 2 * I, H), u8(e * 2 * I, H // 32), u8(e * H, I), u8(e * H, I // 32)
+
+
+def decode(plan=None, gate_w=None, weights=None):
+    return ml.nvfp4_moe_decode(bf16(T, H), bf16(T, H), bf16(H), bf16(E, H) if gate_w is None else gate_w,
+                               *(weights or nvfp4_weights()), K, I, plan)
+
+
+def forward(plan=None, gate_w=None, weights=None):
+    return ml.mxfp8_moe_block_forward(bf16(T, H), bf16(T, H), bf16(H), bf16(E, H) if gate_w is None else gate_w,
+                                      *(weights or mxfp8_weights()), K, I, plan=plan)
+
+
+def saved_of(t=T, e=E, h=H):
+    return dict(h=bf16(t, h), y=bf16(t, h), rstd=torch.ones(t), logits=torch.zeros(t, e),
+                ids=torch.zeros(t, K, dtype=torch.int32), counts=torch.zeros(e + 1, dtype=torch.int32))
+
+
+def backward(plan=None, saved=None, gate_w=None, dy=None):
+    return ml.moe_block_backward(saved or saved_of(), bf16(H), bf16(E, H) if gate_w is None else gate_w,
+                                 bf16(T, H) if dy is None else dy, torch.zeros(T, K), torch.ones(1), plan=plan)
+
+
+PASSES = [decode, forward, backward]
+
+
+@pytest.mark.parametrize("call", PASSES)
+@pytest.mark.parametrize("t,k", [(T + 1, K), (T - 1, K), (4 * T, K), (0, K), (T, K + 1), (T, 1)])
+def test_a_plan_for_other_sizes_is_refused(call, t, k):
+    """A larger plan would send the products past their rows, a smaller one
+    leave rows unwritten."""
+    with pytest.raises(ValueError, match="plan"):
+        call(ml.block_plan(t, k, "cpu"))
+
+
+@pytest.mark.parametrize("call", PASSES)
+def test_a_plan_on_another_device_or_in_parts_is_refused(call):
+    with pytest.raises(ValueError, match="plan"):
+        call(ml.block_plan(T, K, "meta"))
+    good = ml.block_plan(T, K, "cpu")
+    for name in good:
+        with pytest.raises(ValueError, match="plan"):
+            call({n: v for n, v in good.items() if n != name})
+        with pytest.raises(ValueError, match="plan"):
+            call(dict(good, **{name: good[name][:-1]}))
+        with pytest.raises(ValueError, match="plan"):
+            call(dict(good, **{name: good[name].float()}))
+    wide = ml.block_plan(T, K + 1, "cpu")["slot"][:, :K]
+    with pytest.raises(ValueError, match="plan"):
+        call(dict(good, slot=wide))
+
+
+@pytest.mark.parametrize("call", PASSES)
+def test_the_plan_made_for_the_call_is_taken(call):
+    with pytest.raises(TypeError, match="device tensor"):  # on to the first operator, which wants a GPU
+        call(ml.block_plan(T, K, "cpu"))
+    with pytest.raises(TypeError, match="device tensor"):
+        call()
