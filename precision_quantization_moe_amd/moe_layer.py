@@ -172,6 +172,20 @@ def _plan(plan, tokens: int, k: int, device):
     return plan
 
 
+def _experts_of(gate_w, hidden: int, device, **weights) -> int:
+    """The router's experts, E, of gate_w [E, hidden] bf16.  weights: name ->
+    (tensor of bytes, their number per expert); they have to be of E experts,
+    since the products would read past the end of fewer and leave more out."""
+    E = gate_w.shape[0]
+    b._want(gate_w, "gate_w", torch.bfloat16, (E, hidden), device)
+    for name, (w, size) in weights.items():
+        if (w.element_size() != 1 or w.device != device or not w.is_contiguous()
+                or w.numel() != E * size):
+            raise ValueError(f"{name}: expected {size} contiguous bytes on {device} for each of the "
+                             f"router's {E} experts, got {w.numel()} (no shared expert here)")
+    return E
+
+
 def _router_logits(y, gate_w, off):
     """y [T, H] times the router's weight [E, H], both bf16, in binary32."""
     E, H = gate_w.shape
@@ -186,12 +200,14 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
     (T * k <= 4096): residual addition and RMS norm, router gate, gate_up with
     SwiGLU, down projection, combine.  Activations stay in bf16, and nothing
     is sorted or gathered.  x, residual [T, H] bf16 (residual may be None);
-    gate_w [E, H] bf16, E % 8 == 0; the weights as
-    quantize_expert_weights_nvfp4 returns them; plan from block_plan(T, k,
-    device).  Returns dict(out [T, H] bf16, h (the new residual stream), y,
-    ids, prob, d)."""
+    gate_w [E, H] bf16, E % 8 == 0; the weights of those E experts as
+    quantize_expert_weights_nvfp4 returns them (routed experts alone: weights
+    with a shared expert's group, as nvfp4_moe_forward takes them, are refused);
+    plan from block_plan(T, k, device).  Returns dict(out [T, H] bf16, h (the new
+    residual stream), y, ids, prob, d)."""
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
+    _experts_of(gate_w, H, x.device, w1q=(w1q, inter * H), w2q=(w2q, H * inter // 2))
     _, _, y, h, _ = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, quantize=False)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, _, _, _ = b.moe_gate(logits, k, score, renormalize, scale)
@@ -210,16 +226,18 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
     with its balance loss, then the experts of mxfp8_moe_forward.  mask [T]
     marks padding with 0: no part in the loss, no weight, no gradient to the
     gate; its x must be finite, since its rows still pass through the products.
-    Returns the experts' dict and h, y, rstd, logits,
-    ids, prob, counts, prob_sum, loss."""
-    T = x.shape[0]
+    The weights are those of gate_w's E experts, as quantize_expert_weights_mxfp8
+    returns them.  Returns the experts' dict and h, y, rstd, logits, ids, prob,
+    counts, prob_sum, loss."""
+    T, H = x.shape
     plan = _plan(plan, T, k, x.device)
+    E = _experts_of(gate_w, H, x.device, w1q=(w1q, 2 * inter * H), w1s=(w1s, inter * H // 16),
+                    w2q=(w2q, H * inter), w2s=(w2s, H * inter // 32))
     qx, sx, y, h, rstd = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, keep_y=True)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, counts, prob_sum, loss = b.moe_gate(logits, k, score, renormalize, scale, mask,
                                                    loss_coef)
-    r = _mxfp8_experts(qx, sx, ids, prob.view(-1), w1q, w1s, w2q, w2s, gate_w.shape[0], inter,
-                       True)
+    r = _mxfp8_experts(qx, sx, ids, prob.view(-1), w1q, w1s, w2q, w2s, E, inter, True)
     r.update(h=h, y=y, rstd=rstd, logits=logits, ids=ids, prob=prob, counts=counts,
              prob_sum=prob_sum, loss=loss)
     return r
@@ -241,7 +259,7 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
     Returns dict(dx [T, H] bf16, the gradient of x and of residual; d_norm_w
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
-    E = gate_w.shape[0]
+    E = _experts_of(gate_w, H, dy.device)
     plan = _plan(plan, T, saved["ids"].shape[1], dy.device)
     off = plan["off"]
     dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,

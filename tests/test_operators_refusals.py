@@ -112,3 +112,35 @@ def test_the_plan_made_for_the_call_is_taken(call):
         call(ml.block_plan(T, K, "cpu"))
     with pytest.raises(TypeError, match="device tensor"):
         call()
+
+
+@pytest.mark.parametrize("call,weights", [(decode, nvfp4_weights), (forward, mxfp8_weights)])
+@pytest.mark.parametrize("e", [E + 1, E - 1, 0, 2 * E])
+def test_weights_of_other_experts_than_the_routers_are_refused(call, weights, e):
+    """One group more is a shared expert, which these passes do not have: its
+    product would be left out in silence."""
+    with pytest.raises(ValueError, match="experts"):
+        call(weights=weights(e))
+    first = weights()[:len(weights()) // 2]
+    with pytest.raises(ValueError, match="experts"):
+        call(weights=first + weights(e)[len(first):])
+
+
+@pytest.mark.parametrize("call", PASSES)
+def test_a_router_weight_of_another_kind_is_refused(call):
+    with pytest.raises(TypeError, match="gate_w"):
+        call(gate_w=torch.zeros(E, H))
+    with pytest.raises(TypeError, match="gate_w"):
+        call(gate_w=bf16(E, H).to("meta"))
+    with pytest.raises(ValueError, match="gate_w"):
+        call(gate_w=bf16(E, H + 32))
+    with pytest.raises(ValueError, match="gate_w"):
+        call(gate_w=bf16(H, E).t())
+
+
+def test_expert_weights_of_another_kind_are_refused():
+    q1, s1, q2, s2 = mxfp8_weights()
+    for bad in ((q1, s1[:-1], q2, s2), (q1, s1, q2, s2[:, :-1]), (q1.float(), s1, q2, s2),
+                (u8(H, E * 2 * I).t(), s1, q2, s2), (q1, s1, q2.to("meta"), s2)):
+        with pytest.raises(ValueError, match="experts"):
+            forward(weights=bad)
