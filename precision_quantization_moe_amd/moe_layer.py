@@ -248,7 +248,8 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
                        score: int = b.SCORE_SOFTMAX, renormalize: bool = True,
                        scale: float = 1.0):
     """The gradients of a block's gate and norm, behind the experts' own
-    backward pass.  saved: what mxfp8_moe_block_forward returned.
+    backward pass.  saved: what mxfp8_moe_block_forward returned; a tensor of
+    other sizes or with strides is refused.
       dy [T, H] bf16     gradient of y through the experts
       d_prob [T, k] f32  gradient of the routing probabilities
       d_loss [1] f32     gradient of the balance loss
@@ -259,8 +260,17 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
     Returns dict(dx [T, H] bf16, the gradient of x and of residual; d_norm_w
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
-    E = _experts_of(gate_w, H, dy.device)
-    plan = _plan(plan, T, saved["ids"].shape[1], dy.device)
+    dev, bf16, k = dy.device, torch.bfloat16, saved["ids"].shape[1]
+    E = _experts_of(gate_w, H, dev)
+    plan = _plan(plan, T, k, dev)
+    # the products and the combine take their sizes from here
+    b._want(dy, "dy", bf16, (T, H), dev)
+    b._want(saved["y"], "y", bf16, (T, H), dev)
+    b._want(saved["h"], "h", bf16, (T, H), dev)
+    b._want(saved["rstd"], "rstd", torch.float32, (T,), dev)
+    b._want(saved["logits"], "logits", saved["logits"].dtype, (T, E), dev)
+    b._want(saved["ids"], "ids", torch.int32, (T, k), dev)
+    b._want(saved["counts"], "counts", torch.int32, (E + 1,), dev)
     off = plan["off"]
     dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,
                              mask, loss_coef, saved["counts"], d_loss, out_dtype=b.OUT_BF16)

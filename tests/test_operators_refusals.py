@@ -144,3 +144,24 @@ def test_expert_weights_of_another_kind_are_refused():
                 (u8(H, E * 2 * I).t(), s1, q2, s2), (q1, s1, q2.to("meta"), s2)):
         with pytest.raises(ValueError, match="experts"):
             forward(weights=bad)
+
+
+@pytest.mark.parametrize("bad", [saved_of(t=T - 1), saved_of(t=T + 3), saved_of(e=E - 1), saved_of(e=E + 8),
+                                 saved_of(h=H + 32),
+                                 dict(saved_of(), y=bf16(T - 1, H)), dict(saved_of(), h=bf16(T + 1, H)),
+                                 dict(saved_of(), y=torch.zeros(T, H)), dict(saved_of(), y=bf16(H, T).t()),
+                                 dict(saved_of(), logits=torch.zeros(E, T).t()),
+                                 dict(saved_of(), rstd=torch.ones(T - 1))],
+                         ids=range(11))
+def test_gradients_of_another_calls_values_are_refused(bad):
+    """The weight's gradient takes as many rows of y as dy has."""
+    with pytest.raises((ValueError, TypeError), match="y:|h:|rstd:|logits:|ids:|counts:"):
+        backward(saved=bad)
+
+
+def test_gradients_of_strided_rows_are_refused():
+    wide = bf16(T, 2 * H)[:, :H]
+    with pytest.raises(ValueError, match="dy:"):
+        backward(dy=wide)
+    with pytest.raises(TypeError, match="dy:"):
+        backward(dy=torch.zeros(T, H))
