@@ -10,7 +10,8 @@
 // caller may keep.  The sum of squares and the root are binary64 (no square
 // overflows, and their cost hides behind the loads), and a binary32 product that
 // lies within its own error of the middle of two bf16 values is formed again in
-// binary64: y is the nearest bf16 value.
+// binary64, and so is one whose factors may be subnormal: y is the nearest bf16
+// value.
 //
 // Backward (straight through both roundings), g = dy w, h = s rstd:
 //   dx = rstd (g - h mean(g h)) + d_sum,   dw_c = sum over rows of dy h.
@@ -119,6 +120,22 @@ __device__ __forceinline__ double inverse_root(double m) {
   return __builtin_fma(0.5 * r, __builtin_fma(-m * r, r, 1.0), r);
 }
 
+// Smaller halves of a and of b's bf16 magnitudes, each as twice its bits less
+// one (0 becomes the largest): three packed instructions for two values.
+__device__ __forceinline__ uint32_t low_magnitudes(uint32_t a, uint32_t b) {
+  const pqm_us2 v = __builtin_bit_cast(pqm_us2, b) * (uint16_t)2 + (uint16_t)0xFFFF;
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(pqm_us2, a), v));
+}
+
+// The same of the magnitude below which v rstd may be subnormal in binary32
+// (with a subnormal rstd: all but 0), where a product keeps fewer bits than
+// to_middle counts on.  From the exponents: v rstd >= 2^-126 where the two
+// fields add up to 128 and v is normal.
+__device__ __forceinline__ uint32_t short_products(float rstd) {
+  const int e = (int)(__float_as_uint(rstd) >> 23);
+  return e == 0 ? 0xFFFFu : (uint32_t)max(1, 128 - e) << 8;
+}
+
 // At most 6 where v, nearest but for 3 units in the last place, is so close to
 // the middle of two bf16 values that those units may decide.
 __device__ __forceinline__ uint16_t to_middle(float v) {
@@ -141,7 +158,8 @@ __device__ __forceinline__ float before_bf16(double d) {
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
 // Bound by memory: 16384 x 2048 with residual, 235 MB, 41.3 us (5.7 TB/s; a copy
 // here moves 5.1); 8 x 2048 takes 4.8 us, the time of a launch.  The binary64
-// sum, root and middles cost 0.1 us there and 0.5 for 256 to 2048 rows.
+// sum, root and middles cost 0.1 us there and 0.5 for 256 to 2048 rows; the look
+// for factors that may be subnormal 0.13 for 8 rows and nothing for 16384.
 template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,
@@ -152,6 +170,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
   const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   const bool live = row < rows;  // with 64 threads a row: the last workgroup's spare waves
   uint32_t v[NC][4];
+  uint32_t low = 0xFFFFFFFFu;  // of this thread's smallest magnitudes but 0
   double sq = 0.0;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -170,6 +189,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      low = low_magnitudes(low, v[i][j]);
       const double lo = bf16_lo_f32(v[i][j]), hi = bf16_hi_f32(v[i][j]);
       sq = __builtin_fma(lo, lo, sq);
       sq = __builtin_fma(hi, hi, sq);
@@ -186,6 +206,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
   const double total = row_sum<TPR>(sq, red);
   const double root = inverse_root(total * inv_c + eps);  // no square of bf16 leaves binary64
   const float rstd = (float)root;
+  const bool all_close = min(low & 0xFFFFu, low >> 16) < short_products(rstd);
   if (!live) return;
   if (rstd_out && l == 0) rstd_out[row] = rstd;
 #pragma unroll
@@ -201,7 +222,7 @@ __global__ __launch_bounds__(256) void k_rmsnorm_quant(
       f[j] = (j & 1 ? bf16_hi_f32(v[i][j / 2]) : bf16_lo_f32(v[i][j / 2])) * rstd * wf[j];
       close = min(close, to_middle(f[j]));
     }
-    if (close <= 6) {  // one lane in a thousand; all eight, which keeps the code short
+    if (close <= 6 || all_close) {  // one lane in a thousand; all eight, which keeps the code short
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t u = v[i][j / 2];

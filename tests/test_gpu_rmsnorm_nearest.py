@@ -1,0 +1,82 @@
+"""The norm's exactness on the GPU: rstd is the binary32 value next to the
+binary64 one, and y the bf16 value next to the binary64 product.
+
+Bounds.  The kernel's binary64 sum adds at most 64 squares a thread and joins
+the threads in 8 steps, the reference's no worse; with mean, root and products
+both keep 2^-45 of the value.  So rstd is within half a step of binary32 and
+that (subnormal: half of 2^-149), and only a product within 2^-40 of itself
+from the middle of two bf16 values may go to either of them."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import precision_quantization_moe_amd as pqm
+from gpu_util import requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+U = 2.0 ** -24
+
+
+def nearest(v):
+    """bf16 values next to binary64 v, ties to even, subnormal ones too, and
+    where v lies in the middle of two."""
+    step = torch.exp2((torch.frexp(v).exponent - 1).clamp(min=-126).double() - 7)
+    part = v / step
+    middle = ((part - part.floor() - 0.5).abs() <= 2.0 ** -40 * part.abs())
+    return torch.round(part) * step, step, middle
+
+
+def check(x, r, w, eps, out):
+    q, s, y, total, rstd = out
+    want = x if r is None else (x.float() + r.float()).to(torch.bfloat16)
+    assert torch.equal(total, want)
+    v = want.double()
+    root = (v.square().mean(1) + eps).pow(-0.5)
+    assert ((rstd.double() - root).abs() <= (1 + 2.0 ** -20) * U * root + 2.0 ** -150).all()
+    n, step, middle = nearest(v * w.double() * root[:, None])
+    off = (y.double() - n).abs()
+    assert (off <= torch.where(middle, step, 0.0)).all(), \
+        f"{int((off > 0).sum())} of {off.numel()} values are not the nearest"
+    if q is not None:
+        oq, os_, _, _ = pqm.quantize_mxfp8(y, colwise=False)
+        assert torch.equal(q, oq) and torch.equal(s, os_)
+
+
+def rows_of(kind, rows, cols, seed):
+    """(x, w, eps) whose x rstd, rstd or y leave the normal numbers of binary32."""
+    g = torch.Generator().manual_seed(seed)
+    u = torch.randn(rows, cols, generator=g)
+    w = 1 + 0.3 * torch.randn(cols, generator=g)
+    if kind == "small values of a large row":      # x rstd about 2^-140, lifted by w
+        x, w, eps = u * 2.0 ** -80, w * 2.0 ** 20, 1e-6
+        x[:, ::cols // 8] = 2.0 ** 60
+    elif kind == "values that vanish before w":    # x rstd about 2^-160
+        x, w, eps = u * 2.0 ** -100, w * 2.0 ** 100, 1e-6
+        x[:, 5] = 2.0 ** 60
+        w[5] = 1
+    elif kind == "rows of the largest values":     # rstd below 2^-126
+        x, eps = torch.sign(u) * (1 + torch.rand(rows, cols, generator=g)) * 2.0 ** 127, 1e-6
+        x = x.clamp(-3.3e38, 3.3e38)
+    elif kind == "subnormal output":
+        x, w, eps = u, w * 2.0 ** -131, 1e-6
+    elif kind == "subnormal input":                # x rstd about 2^-126
+        x, w, eps = u * 2.0 ** -131, w * 2.0 ** 20, 2.0 ** -10
+    else:                                          # every size in one row
+        x = torch.sign(u) * torch.exp2(torch.rand(rows, cols, generator=g) * 250 - 130)
+        w, eps = torch.exp2(torch.rand(cols, generator=g) * 100), 2.0 ** -100
+    return x.to(torch.bfloat16).cuda(), w.cuda(), eps
+
+
+KINDS = ["small values of a large row", "values that vanish before w", "rows of the largest values",
+         "subnormal output", "subnormal input", "every size"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(64, 512), (40, 2048), (1100, 2048), (33, 4096), (9, 7168)])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_y_is_the_nearest_value_beyond_the_normal_numbers(kind, rows, cols, wf32):
+    x, w, eps = rows_of(kind, rows, cols, rows + cols)
+    w = w if wf32 else w.to(torch.bfloat16)
+    check(x, None, w, eps, pqm.rmsnorm_quantize_mxfp8(x, w, eps, keep_y=True))
