@@ -564,8 +564,9 @@ pqm_status pqm_moe_combine(const uint16_t *y_rows, const int32_t *slot,
  * row stride must then be cols (PQM_ERR_SHAPE), and is updated in place; no
  * other output may overlap an input.  The sum and the root are binary64, and y
  * is the nearest bf16 value of the product; rows whose squares leave binary32
- * (values from about 2^63 on) are handled.  x + residual and y must stay
- * within the bf16 range.
+ * (values from about 2^63 on) are handled, and so are subnormal values.  A sum
+ * or a y beyond bf16 is an infinity; an infinity in sum makes the row's rstd 0
+ * and y 0, NaN in its own place; a NaN in sum makes the row's rstd and y NaN.
  * Requires cols % 8 == 0 (% 32 with q, s), cols <= 16384, rows < 2^31,
  * ldx, ldr >= cols, 2^-100 <= eps < infinity (PQM_ERR_SHAPE); x, residual,
  * weight, sum, y and the strides 16-byte aligned, q 8-byte, rstd 4-byte

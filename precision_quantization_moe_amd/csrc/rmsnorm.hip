@@ -114,10 +114,12 @@ __device__ __forceinline__ double row_sum(double v, double *red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// 1 / sqrt(m): the hardware's estimate (about 2^-27) and one Newton step.
+// 1 / sqrt(m): the hardware's estimate (about 2^-27) and one Newton step, which
+// would make a NaN of the 0 that an infinite m gives.
 __device__ __forceinline__ double inverse_root(double m) {
   const double r = __builtin_amdgcn_rsq(m);
-  return __builtin_fma(0.5 * r, __builtin_fma(-m * r, r, 1.0), r);
+  const double s = __builtin_fma(0.5 * r, __builtin_fma(-m * r, r, 1.0), r);
+  return r == 0.0 ? r : s;
 }
 
 // Smaller halves of a and of b's bf16 magnitudes, each as twice its bits less

@@ -80,3 +80,35 @@ def test_y_is_the_nearest_value_beyond_the_normal_numbers(kind, rows, cols, wf32
     x, w, eps = rows_of(kind, rows, cols, rows + cols)
     w = w if wf32 else w.to(torch.bfloat16)
     check(x, None, w, eps, pqm.rmsnorm_quantize_mxfp8(x, w, eps, keep_y=True))
+
+
+@pytest.mark.parametrize("cols", [96, 2048, 5024])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_infinities_and_nan_in_a_row(cols, wf32):
+    """An infinity makes rstd 0: zeros beside it, no value in its own place.  A
+    NaN takes its whole row; the other rows are as without them."""
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(12, cols, generator=g).to(torch.bfloat16).cuda()
+    w = (1 + 0.3 * torch.randn(cols, generator=g)).cuda()
+    w = w if wf32 else w.to(torch.bfloat16)
+    clean = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, keep_y=True)
+    x[1, 7] = float("inf")
+    x[3, cols - 1] = -float("inf")
+    x[5, ::3] = float("inf")
+    x[7, 9] = float("nan")
+    x[9, 2], x[9, 70] = float("nan"), float("inf")
+    q, s, y, total, rstd = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, keep_y=True)
+    keep = [0, 2, 4, 6, 8, 10, 11]
+    for a, b in zip(clean, (q, s, y, total, rstd)):
+        assert torch.equal(a[keep], b[keep])
+    assert not rstd[[1, 3, 5]].any() and rstd[[7, 9]].isnan().all()
+    for row in (1, 3, 5):
+        there = torch.isinf(x[row])
+        assert y[row][there].isnan().all() and not y[row][~there].any()
+    assert y[[7, 9]].isnan().all()
+    oq, os_, _, _ = pqm.quantize_mxfp8(y, colwise=False)
+    assert torch.equal(q, oq) and torch.equal(s, os_)
+    # finite values whose sum leaves bf16: the sum is an infinity
+    a = torch.full((1, cols), 3e38).to(torch.bfloat16).cuda()
+    _, _, y, total, rstd = pqm.rmsnorm_quantize_mxfp8(a, w, 1e-6, residual=a, keep_y=True)
+    assert torch.isinf(total).all() and not rstd.any() and y.isnan().all()
