@@ -620,8 +620,9 @@ size_t pqm_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  * loss, and its ids are (t k + j) mod E, so that padding loads every expert
  * alike in pqm_moe_route.  A logit of -inf closes an expert to a token
  * (chosen last, prob 0; a row of -inf alone gives prob 0, as do chosen sigmoid
- * scores that all vanish in binary32, z below about -87).  NaN and +inf are
- * outside the contract (the ids stay in [0, E)).  The arithmetic is binary32.
+ * scores that all vanish in binary32, z below about -87).  A NaN logit ranks
+ * first; it (with softmax also +inf) makes its token's prob, and with it prob_sum
+ * and loss, NaN; the ids stay in [0, E).  The arithmetic is binary32.
  * counts, prob_sum and loss go together: all NULL skips the loss, and
  * workspace is then not needed.  workspace (device, 4-byte aligned, contents
  * irrelevant): pqm_moe_gate_workspace bytes; calls that may run at the same
@@ -648,7 +649,7 @@ size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts);
  * are held fixed; counts is the forward call's [E + 1], and counts and d_loss
  * go together (both NULL: no loss).  The other arguments are the forward
  * call's.  d_logits [tokens, E] in d_logits_dtype (rounded once), zero for
- * masked tokens; it may not overlap logits.  topk_ids may hold any experts (an
+ * masked tokens, NaN for a token whose prob is; it may not overlap logits.  topk_ids may hold any experts (an
  * id twice adds up); ids outside [0, E) add nothing.  Same limits and errors.
  */
 pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,

@@ -105,10 +105,10 @@ __device__ __forceinline__ float load_logit(const __amdgpu_buffer_rsrc_t &r, uin
 
 // e^x of x <= 0 to about 2 ulp: 2^t with t = x log2(e) in two parts, the second
 // through its first-order term.  Results below 2^-126 are 0; below -200 they are
-// so in any case.  (Above 0 the first part may overflow, where the correction
-// would make a NaN of it.)
+// so in any case; a NaN stays one.  (Above 0 the first part may overflow, where
+// the correction would make a NaN of it.)
 __device__ __forceinline__ float exp_f32(float x) {
-  x = fmaxf(x, -200.0f);
+  x = __builtin_elementwise_maximum(x, -200.0f);
   const float t = x * 0x1.715476p+0f;
   const float r = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
   const float p = __builtin_amdgcn_exp2f(t);
@@ -116,13 +116,16 @@ __device__ __forceinline__ float exp_f32(float x) {
 }
 
 // Order-preserving key of a logit, never 0 (0 marks "no expert here" and
-// "already chosen").  -0 counts as +0; a NaN, outside the contract, ranks as
-// -inf, so that the ids stay experts whatever the logits hold.
+// "already chosen").  -0 counts as +0.  The offset makes -inf 1, and of the NaN,
+// which lie above inf or, with a sign, below -inf, the largest: a row's largest
+// key shows whether it holds one.
+constexpr uint32_t GATE_KEY_LOW = 0x007FFFFEu;
 __device__ __forceinline__ uint32_t logit_key(float z) {
-  const uint32_t u = __float_as_uint(fmaxf(z, -__builtin_inff()) + 0.0f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  const uint32_t u = __float_as_uint(z + 0.0f);  // and no signalling NaN
+  return (u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) - GATE_KEY_LOW;
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
+  k += GATE_KEY_LOW;
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
       key[i] = in ? logit_key(v[i]) : 0u;
     }
     int my_id = 0;
-    uint32_t my_key = 0, top_key = 0;
+    uint32_t my_key = 0;
     for (int j = 0; j < k; ++j) {
       uint32_t m = 0;
 #pragma unroll
@@ -200,16 +203,16 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
       const bool won = at == mine_at;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = hit[i] && won ? 0u : key[i];
-      if (j == 0) top_key = m;
       if (l == j) {
         my_id = (int)at;
         my_key = m;
       }
     }
-    float top = key_logit(top_key);
+    float top = key_logit(group_lane<LPT, 0>(my_key));
     const float my_z = l < k ? key_logit(my_key) : -__builtin_inff();
-    // shares: exp(z - top) or sigmoid(z), and their sum; an all -inf row has none
-    if (!(top > -__builtin_inff())) top = 0.0f;
+    // shares: exp(z - top) or sigmoid(z), and their sum; an all -inf row has none,
+    // and one with a NaN, which is its top then, NaN
+    if (top == -__builtin_inff()) top = 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -218,14 +221,15 @@ __global__ __launch_bounds__(1024) void k_moe_gate(
       sum += v[i];
     }
     sum = group_sum<LPT>(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays one
     float w = l < k ? (SOFTMAX ? exp_f32(my_z - top) : sigmoid(my_z)) : 0.0f;
     if (renorm) {
       const float total = group_sum<LPT>(w);
-      w = total > 0.0f ? w / total : 0.0f;
+      w = total == 0.0f ? 0.0f : w / total;
     } else if (SOFTMAX) {
       w *= inv;
     }
+    if (!SOFTMAX && top != top) w = top;
     if (live && l < k) {
       // a token that the mask leaves out is not read: experts in turn, so that
       // padding loads all of them alike, and no weight
@@ -408,7 +412,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
       sum += v[i];
     }
     sum = group_sum<LPT>(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays one, in every term below
     if (SOFTMAX) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) v[i] *= inv;
