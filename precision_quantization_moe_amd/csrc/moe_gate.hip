@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
   const int l = threadIdx.x % LPT;
   constexpr int groups = 256 / LPT;
   // A token's row of E values, for what one lane has and another needs: its
-  // scores, then d prob / d v, 0 but at the chosen experts.  (16 more: tokens
+  // shares, then u, 0 but at the chosen experts.  (16 more: tokens
   // in other banks.)  One wave's LDS accesses keep their order, so the fences
   // hold only the compiler.
   __shared__ float rows[groups][VPL * LPT + 16];
@@ -413,11 +413,12 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     }
     sum = group_sum<LPT>(sum);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN stays one, in every term below
-    if (SOFTMAX) {
+    // From here on v is the share, and u of a renormalised sigmoid the gradient
+    // by the share.  By the score it would be 1 / sum v times as large, which
+    // leaves binary32 where all scores are near 2^-120.
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] *= inv;
-    }
-    // the chosen experts' scores, from the lanes that hold them
+    for (int i = 0; i < VPL; ++i) v[i] *= inv;
+    // the chosen experts' shares, from the lanes that hold them
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mine[i * LPT + l] = v[i];
@@ -464,13 +465,17 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
     for (int i = 0; i < VPL; ++i) h[i] = i * LPT + l < E ? hc * (float)cnt[i] : 0.0f;
     float dot = 0.0f;  // softmax: sum p (u + h); sigmoid: sum p h
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dot += SOFTMAX ? v[i] * (u[i] + h[i]) : v[i] * inv * h[i];
+    for (int i = 0; i < VPL; ++i) dot += SOFTMAX ? v[i] * (u[i] + h[i]) : v[i] * h[i];
     dot = group_sum<LPT>(dot);
     float gz[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      gz[i] = SOFTMAX ? v[i] * (u[i] + h[i] - dot)
-                      : slope[i] * (u[i] + (h[i] - dot) * inv);
+      if constexpr (SOFTMAX) {
+        gz[i] = v[i] * (u[i] + h[i] - dot);
+      } else {
+        const float si = slope[i] * inv;
+        gz[i] = (renorm ? si : slope[i]) * u[i] + si * (h[i] - dot);
+      }
       if (!valid) gz[i] = 0.0f;
     }
     if (out_f32) {

@@ -101,3 +101,25 @@ def test_rows_whose_scores_all_vanish(E, k, renorm):
     dz = pqm.moe_gate_backward(z.cuda(), ids, torch.ones(64, k).cuda(), pqm.SCORE_SIGMOID, renorm, 1.0,
                                None, 0.1, counts, torch.ones(1).cuda())
     assert not dz.any()
+
+
+@pytest.mark.parametrize("E,k", SIZES + [(20, 1)])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("size", [1e-5, 1.0, 1e4])
+def test_gradients_of_rows_that_almost_vanish(E, k, renorm, size):
+    """Scores of 2^-125 to 2^-115 alone in a row: their quotients are ordinary
+    numbers, and so are the gradients, whatever the products on the way."""
+    z = torch.linspace(-86.5, -80, 48 * E)[torch.randperm(48 * E, generator=torch.Generator().manual_seed(E))]
+    z = z.view(48, E)
+    want = ref.gate(ref.f64(z), k, False, renorm, 2.5, None, 0.1)
+    counts = torch.cat([want["counts"], torch.tensor([48]).double()]).to(torch.int32)
+    d = size * torch.randn(48, k, generator=torch.Generator().manual_seed(k))
+    args = (want["ids"], want["counts"], 48, False, renorm, 2.5, want["live"], 0.1)
+    for d_loss in (None, 1.0):
+        dz = pqm.moe_gate_backward(z.cuda(), want["ids"].to(torch.int32).cuda(), d.cuda(), pqm.SCORE_SIGMOID,
+                                   renorm, 2.5, None, 0.1, None if d_loss is None else counts.cuda(),
+                                   None if d_loss is None else torch.ones(1).cuda())
+        g, terms = ref.gate_backward(ref.f64(z), *args, ref.f64(d), d_loss or 0.0)
+        # without renormalization the gradient is of the scores' own size, where
+        # binary32 keeps 2^-149 and a product may vanish below 2^-126
+        assert ((ref.f64(dz) - g).abs() <= 3 * (2 * 87 + 48) * ref.U * terms + 4 * GONE).all()
