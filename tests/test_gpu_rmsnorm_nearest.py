@@ -11,6 +11,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+import operators_ref as ref
 import precision_quantization_moe_amd as pqm
 from gpu_util import requires_gpu
 
@@ -112,3 +113,49 @@ def test_infinities_and_nan_in_a_row(cols, wf32):
     a = torch.full((1, cols), 3e38).to(torch.bfloat16).cuda()
     _, _, y, total, rstd = pqm.rmsnorm_quantize_mxfp8(a, w, 1e-6, residual=a, keep_y=True)
     assert torch.isinf(total).all() and not rstd.any() and y.isnan().all()
+
+
+def usual(rows, cols, wf32, residual, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn(rows, cols, generator=g, device="cuda")
+         * torch.exp(torch.randn(rows, 1, generator=g, device="cuda"))).to(torch.bfloat16)
+    r = torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16) if residual else None
+    w = 1 + 0.3 * torch.randn(cols, generator=g, device="cuda")
+    return x, r, w if wf32 else w.to(torch.bfloat16)
+
+
+# every width's kernel, with and without streaming (from 2^21 values on)
+@pytest.mark.parametrize("rows,cols", [(1, 32), (5, 96), (9, 1024), (33, 1056), (300, 2048), (3, 4128),
+                                       (131, 7168), (2, 8224), (3, 16384),
+                                       (4200, 512), (2100, 1024), (1030, 2048), (515, 4096), (300, 7168),
+                                       (260, 8192), (130, 16384)])
+@pytest.mark.parametrize("wf32", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_y_and_rstd_are_the_nearest_values(rows, cols, wf32, residual):
+    x, r, w = usual(rows, cols, wf32, residual, rows + cols)
+    out = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, residual=r, keep_y=True)
+    check(x, r, w, 1e-6, out)
+    again = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, residual=r)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(out[i], again[i]), i
+    if residual:
+        mine = r.clone()
+        again = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, residual=mine, keep_y=True, inplace=True)
+        assert again[3] is mine and all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+# every width's gradients with streaming loads (from 2^25 values on)
+@pytest.mark.parametrize("rows,cols", [(65540, 512), (32771, 1024), (16385, 2048), (8193, 4096), (4700, 7168),
+                                       (2050, 16384)])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_gradients_of_large_calls(rows, cols, wf32):
+    x, ds, w = usual(rows, cols, wf32, True, rows + cols)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16)
+    rstd = (x.double().square().mean(1) + 1e-6).pow(-0.5).float()
+    for d_sum in (ds, None):
+        dx, dw = pqm.rmsnorm_backward(dy, x, w, rstd, d_sum=d_sum)
+        want, want_dw, bound, size = ref.norm_backward(
+            dy.double(), x.double(), w.double(), rstd.double(), None if d_sum is None else d_sum.double())
+        assert ((dx.double() - want).abs() <= ref.HALF_BF16 * want.abs() + bound).all()
+        assert ((dw.double() - want_dw).abs() <= (rows + 3) * ref.U * size).all()
