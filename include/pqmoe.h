@@ -676,7 +676,9 @@ pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, con
  * weights are exact; so are x's values down to 2^-31 of the largest of their
  * row, and smaller ones are off by less than 2^-38 of that largest value (large
  * calls hold x in scaled binary16).  A row's result depends on its own x and
- * on the call's sizes alone.  Nothing may overlap out.
+ * on the call's sizes alone.  Nothing may overlap out.  The weights are read
+ * again for each 16 rows of an expert: from about 32 rows an expert on,
+ * pqm_moe_route and pqm_moe_grouped_gemm are faster.
  * Requires rows <= 4096 (more: pqm_moe_route and pqm_moe_grouped_gemm),
  * 1 <= divisor <= 4096, 1 <= G <= 4096, N <= 2^20, K % 32 == 0, 32 <= K <=
  * 2^20, w_rows_per_scale >= 1 dividing G N (PQM_ERR_SHAPE); x, w_q and out

@@ -156,11 +156,12 @@ struct GdChunk {
 // workgroup's eight waves each takes one of two 16-row tiles (ACT: a gate tile
 // and its up tile) and a quarter of the contraction in 256-wide chunks, so a
 // chain is short: what bounds this kernel is latency (ids, weights, x, then
-// the joining).  One decode step of top-8 of 128 experts, 2048 x 768: gate_up
-// 8.9 us, down 6.0 us of about 4.5 that a kernel of nothing takes here.  Two
-// tiles a wave took 10.4 and 6.7; waiting for the rows before the first
-// weights were asked for, 12; the next chunk's loads ahead of this one's
-// products, 9.0 and 7.1 (the registers halve what a CU holds).
+// the joining).  One decode step of top-8 of 128 experts, 2048 x 768, in a
+// captured graph: gate_up 7.4 us, down 5.7, of which an empty launch is 1.6.
+// Measured against 8.9 and 6.0 of this form (kernel durations): two tiles a wave
+// 10.4 and 6.7; waiting for the rows before the first weights were asked for,
+// 12; the next chunk's loads ahead of this one's products, 9.0 and 7.1 (the
+// registers halve what a CU holds).
 //
 // WORDS: K % 64 == 0, so that a row of scales starts at a word; otherwise (any
 // K % 32 == 0) it starts at any even byte and its words come in halves, which
@@ -529,7 +530,9 @@ hipError_t launch_gemv(GemvArgs a, const int32_t *ids, bool act, bool f32, hipSt
   // Fewer rows than experts: a workgroup row per row of ids.  Otherwise one
   // per expert, and one for the rows without an expert.
   a.byrow = a.rows < a.G;
-  // The staged kernel from 160 workgroups on (its loads of scales need K % 64).
+  // The staged kernel from 160 workgroups on.  Its loads of scales need K % 64;
+  // without it the direct kernel runs at any size (gate_up of 37 tokens, K =
+  // 5088: 160 us, 5120: 92).
   // Measured, direct against staged: 96 workgroups 8.9 / 10.9 us, 128: 6.1 /
   // 7.6 and 12.8 / 16.3, 160: 22.5 / 21.3, 192: 12.4 / 11.6, 384: 21.9 / 15.4,
   // 1280: 133 / 85.

@@ -140,10 +140,10 @@ __device__ __forceinline__ float sigmoid(float z) {
 // LPT lanes hold one token, VPL logits each (expert i LPT + lane); the choice
 // takes k turns of a maximum over the keys, the lowest index that has it, and
 // its removal.  Bound by those turns' vector instructions (about 40 a turn for
-// 128 experts, shared by four tokens) and, for few tokens, by the start of a
-// kernel: 16384 x 128, top-8, with the loss 14.0 us (k_moe_balance 4 of them,
-// floor 1.8), 16 x 256 without 4.6; 14.4 and 5.0 with the removal found by
-// comparing each index again.  SUMS: each workgroup also leaves its counts and
+// 128 experts, shared by four tokens) and, for few tokens, by their latency:
+// 16384 x 128, top-8, with the loss 13.2 us (k_moe_balance 4 of them, floor
+// 1.8), 16 x 256 without 4.2 (an empty launch: 1.6); 0.4 us more with the removal
+// found by comparing each index again.  SUMS: each workgroup also leaves its counts and
 // share sums in part_cnt / part_sum [gridDim.x][E] (and its valid tokens in
 // part_valid).
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
@@ -346,11 +346,11 @@ __global__ __launch_bounds__(1024) void k_moe_balance(
   }
 }
 
-// The gradient, laid out as the forward kernel.  16384 x 128 7.9 us, 4093 x 256
-// in bf16 5.7 (floors 3.5 and 0.9; a launch takes about 4.5).  Every load goes
-// out before the first is used (10.1 and 8.5 us with the counts, the ids and
-// the chosen logits waited for in turn); comparing each expert with each of the
-// k ids instead of the row in LDS took 0.8 us more.
+// The gradient, laid out as the forward kernel.  16384 x 128 6.6 us, 4093 x 256
+// in bf16 4.6 (floors 3.5 and 0.9; an empty launch takes 1.6).  Every load goes
+// out before the first is used (2.2 and 2.8 us more with the counts, the ids
+// and the chosen logits waited for in turn); comparing each expert with each of
+// the k ids instead of the row in LDS took 0.8 us more.
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX>
 __global__ __launch_bounds__(256) void k_moe_gate_backward(
     const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
