@@ -162,9 +162,9 @@ def _plan(plan, tokens: int, k: int, device):
     compared on the host (what it holds is on the device and not read)."""
     if not plan:
         return block_plan(tokens, k, device)
-    want = dict(off=((2,), torch.int64), slot=((tokens, k), torch.int32),
-                row=((tokens, 1), torch.int32))
-    for name, (shape, dtype) in want.items():
+    i32 = torch.int32
+    for name, shape, dtype in (("off", (2,), torch.int64), ("slot", (tokens, k), i32),
+                               ("row", (tokens, 1), i32)):
         t = plan.get(name)
         if (t is None or t.shape != shape or t.dtype is not dtype or t.device != device
                 or not t.is_contiguous()):
@@ -172,18 +172,19 @@ def _plan(plan, tokens: int, k: int, device):
     return plan
 
 
-def _experts_of(gate_w, hidden: int, device, **weights) -> int:
-    """The router's experts, E, of gate_w [E, hidden] bf16.  weights: name ->
-    (tensor of bytes, their number per expert); they have to be of E experts,
-    since the products would read past the end of fewer and leave more out."""
+def _router(gate_w, hidden: int, device) -> int:
+    """The experts, E, of the router's weight gate_w [E, hidden] bf16."""
     E = gate_w.shape[0]
     b._want(gate_w, "gate_w", torch.bfloat16, (E, hidden), device)
-    for name, (w, size) in weights.items():
-        if (w.element_size() != 1 or w.device != device or not w.is_contiguous()
-                or w.numel() != E * size):
-            raise ValueError(f"{name}: expected {size} contiguous bytes on {device} for each of the "
-                             f"router's {E} experts, got {w.numel()} (no shared expert here)")
     return E
+
+
+def _of_experts(E: int, name: str, w, size: int):
+    """Refuses weights that are not of E experts with `size` bytes each: the
+    products would read past the end of fewer and leave more out."""
+    if w.numel() != E * size:
+        raise ValueError(f"{name}: expected {size} bytes for each of the router's {E} experts, got "
+                         f"{w.numel()} (no shared expert here)")
 
 
 def _router_logits(y, gate_w, off):
@@ -208,7 +209,9 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
     residual stream), y, ids, prob, d)."""
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
-    _experts_of(gate_w, H, x.device, w1q=(w1q, inter * H), w2q=(w2q, H * inter // 2))
+    E = _router(gate_w, H, x.device)
+    _of_experts(E, "w1q", w1q, inter * H)  # the few-row products check the rest
+    _of_experts(E, "w2q", w2q, H * inter // 2)
     _, _, y, h, _ = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, quantize=False)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, _, _, _ = b.moe_gate(logits, k, score, renormalize, scale)
@@ -232,8 +235,12 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
     counts, prob_sum, loss."""
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
-    E = _experts_of(gate_w, H, x.device, w1q=(w1q, 2 * inter * H), w1s=(w1s, inter * H // 16),
-                    w2q=(w2q, H * inter), w2s=(w2s, H * inter // 32))
+    E = _router(gate_w, H, x.device)
+    for name, w, size in (("w1q", w1q, 2 * inter * H), ("w1s", w1s, inter * H // 16),
+                          ("w2q", w2q, H * inter), ("w2s", w2s, H * inter // 32)):
+        _of_experts(E, name, w, size)
+        if w.element_size() != 1 or w.device != x.device or not w.is_contiguous():
+            raise ValueError(f"{name}: expected the experts' contiguous bytes on {x.device}")
     qx, sx, y, h, rstd = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, keep_y=True)
     logits = _router_logits(y, gate_w, plan["off"])
     ids, prob, counts, prob_sum, loss = b.moe_gate(logits, k, score, renormalize, scale, mask,
@@ -262,16 +269,15 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
     dev, bf16, k = dy.device, torch.bfloat16, saved["ids"].shape[1]
-    E = _experts_of(gate_w, H, dev)
+    E = _router(gate_w, H, dev)
     plan = _plan(plan, T, k, dev)
-    # the products and the combine take their sizes from here
+    # the products and the combine take their sizes from here (ids and counts are
+    # the gate's to check)
     b._want(dy, "dy", bf16, (T, H), dev)
     b._want(saved["y"], "y", bf16, (T, H), dev)
     b._want(saved["h"], "h", bf16, (T, H), dev)
     b._want(saved["rstd"], "rstd", torch.float32, (T,), dev)
     b._want(saved["logits"], "logits", saved["logits"].dtype, (T, E), dev)
-    b._want(saved["ids"], "ids", torch.int32, (T, k), dev)
-    b._want(saved["counts"], "counts", torch.int32, (E + 1,), dev)
     off = plan["off"]
     dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,
                              mask, loss_coef, saved["counts"], d_loss, out_dtype=b.OUT_BF16)
