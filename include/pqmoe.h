@@ -649,8 +649,9 @@ size_t pqm_moe_gate_workspace(int64_t tokens, int64_t num_experts);
  * are held fixed; counts is the forward call's [E + 1], and counts and d_loss
  * go together (both NULL: no loss).  The other arguments are the forward
  * call's.  d_logits [tokens, E] in d_logits_dtype (rounded once), zero for
- * masked tokens, NaN for a token whose prob is; it may not overlap logits.  topk_ids may hold any experts (an
- * id twice adds up); ids outside [0, E) add nothing.  Same limits and errors.
+ * masked tokens, NaN for a token whose prob is; it may not overlap logits.
+ * topk_ids may hold any experts (an id twice adds up); ids outside [0, E) add
+ * nothing.  Same limits and errors.
  */
 pqm_status pqm_moe_gate_backward(const void *logits, pqm_dtype logits_dtype, const uint8_t *mask,
                                  int64_t tokens, int64_t num_experts, int64_t k, pqm_score score,

@@ -143,9 +143,9 @@ __device__ __forceinline__ float sigmoid(float z) {
 // 128 experts, shared by four tokens) and, for few tokens, by their latency:
 // 16384 x 128, top-8, with the loss 13.2 us (k_moe_balance 4 of them, floor
 // 1.8), 16 x 256 without 4.2 (an empty launch: 1.6); 0.4 us more with the removal
-// found by comparing each index again.  SUMS: each workgroup also leaves its counts and
-// share sums in part_cnt / part_sum [gridDim.x][E] (and its valid tokens in
-// part_valid).
+// found by comparing each index again.  SUMS: each workgroup also leaves its
+// counts and share sums in part_cnt / part_sum [gridDim.x][E] (and its valid
+// tokens in part_valid).
 template <int LPT, int VPL, bool ZF32, bool SOFTMAX, bool SUMS>
 __global__ __launch_bounds__(1024) void k_moe_gate(
     const void *__restrict__ z, const uint8_t *__restrict__ mask, int64_t T, int E, int k,
@@ -360,9 +360,9 @@ __global__ __launch_bounds__(256) void k_moe_gate_backward(
   const int l = threadIdx.x % LPT;
   constexpr int groups = 256 / LPT;
   // A token's row of E values, for what one lane has and another needs: its
-  // shares, then u, 0 but at the chosen experts.  (16 more: tokens
-  // in other banks.)  One wave's LDS accesses keep their order, so the fences
-  // hold only the compiler.
+  // shares, then u, 0 but at the chosen experts.  (16 more: tokens in other
+  // banks.)  One wave's LDS accesses keep their order, so the fences hold only
+  // the compiler.
   __shared__ float rows[groups][VPL * LPT + 16];
   float *mine = rows[threadIdx.x / LPT];
   // counts, empty without a loss: every load below goes out before one is used

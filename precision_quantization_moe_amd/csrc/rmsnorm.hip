@@ -159,9 +159,10 @@ __device__ __forceinline__ float before_bf16(double d) {
 // between the sum of squares and the scaling, so each input is read once.
 // `sum` may be x or r itself: a thread reads what it overwrites before it does.
 // Bound by memory: 16384 x 2048 with residual, 235 MB, 41.3 us (5.7 TB/s; a copy
-// here moves 5.1); 8 x 2048 by latency, 4.6 us (an empty launch: 1.6).  The binary64
-// sum, root and middles cost 0.1 us there and 0.5 for 256 to 2048 rows; the look
-// for factors that may be subnormal 0.13 for 8 rows and nothing for 16384.
+// here moves 5.1); 8 x 2048 by latency, 4.6 us (an empty launch: 1.6).  The
+// binary64 sum, root and middles cost 0.1 us there and 0.5 for 256 to 2048 rows;
+// the look for factors that may be subnormal 0.13 for 8 rows and nothing for
+// 16384.
 template <int TPR, int NC, bool WF32, bool STREAM>
 __global__ __launch_bounds__(256) void k_rmsnorm_quant(
     const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const void *__restrict__ w,

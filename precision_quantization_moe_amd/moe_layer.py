@@ -199,9 +199,10 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
                      renormalize: bool = True, scale: float = 1.0, eps: float = 1e-6):
     """One decode step of an expert layer with NVFP4 weights for a few tokens
     (T * k <= 4096; up to about 16 assignments an expert, beyond which the
-    grouped GEMM of nvfp4_moe_forward is faster): residual addition and RMS norm, router gate, gate_up with
-    SwiGLU, down projection, combine.  Activations stay in bf16, and nothing
-    is sorted or gathered.  x, residual [T, H] bf16 (residual may be None);
+    grouped GEMM of nvfp4_moe_forward is faster): residual addition and RMS
+    norm, router gate, gate_up with SwiGLU, down projection, combine.
+    Activations stay in bf16, and nothing is sorted or gathered.  x, residual
+    [T, H] bf16 (residual may be None);
     gate_w [E, H] bf16, E % 8 == 0; the weights of those E experts as
     quantize_expert_weights_nvfp4 returns them (routed experts alone: weights
     with a shared expert's group, as nvfp4_moe_forward takes them, are refused);

@@ -159,3 +159,20 @@ def test_gradients_of_large_calls(rows, cols, wf32):
             dy.double(), x.double(), w.double(), rstd.double(), None if d_sum is None else d_sum.double())
         assert ((dx.double() - want).abs() <= ref.HALF_BF16 * want.abs() + bound).all()
         assert ((dw.double() - want_dw).abs() <= (rows + 3) * ref.U * size).all()
+
+
+@pytest.mark.parametrize("wf32", [False, True])
+def test_y_beyond_bf16_is_an_infinity(wf32):
+    """From the middle between the largest value, 2^128 - 2^120, and 2^128 on."""
+    x, _, _ = usual(64, 1024, True, False, 3)
+    w = torch.full((1024,), 1.5 * 2.0 ** 127, device="cuda")
+    w = w if wf32 else w.to(torch.bfloat16)
+    q, s, y, _, _ = pqm.rmsnorm_quantize_mxfp8(x, w, 1e-6, keep_y=True)
+    v = x.double()
+    v = v * w.double() * (v.square().mean(1, keepdim=True) + 1e-6).pow(-0.5)
+    beyond = v.abs() >= 2.0 ** 128 - 2.0 ** 119
+    assert 0.1 < beyond.float().mean() < 0.9
+    assert torch.equal(torch.isinf(y), beyond) and not y.isnan().any()
+    assert torch.equal(torch.sign(y.float()), torch.sign(v).float())
+    oq, os_, _, _ = pqm.quantize_mxfp8(y, colwise=False)
+    assert torch.equal(q, oq) and torch.equal(s, os_)
