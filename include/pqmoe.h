@@ -702,6 +702,65 @@ pqm_status pqm_moe_gemv_swiglu_nvfp4(const uint16_t *x, const int32_t *ids, cons
                                      int64_t w_rows_per_scale, int64_t G, int64_t inter, int64_t K,
                                      uint16_t *d, hipStream_t stream);
 
+/*
+ * Dense products of bf16 operands (a router, an output head, any projection
+ * that is not an expert's), with what follows them in the same pass:
+ *   z = x W^T + bias,   y = act(z) + residual
+ *   x [M, K] bf16, row stride ldx; w [N, K] bf16 contiguous          (device)
+ *   bias [N] binary32, may be NULL; residual [M, N] bf16, row stride ldr,
+ *       may be NULL                                                  (device)
+ *   y [M, N] bf16 (rounded once) or binary32 per y_dtype; z [M, N] bf16, for
+ *       the backward pass, may be NULL                               (device)
+ * act: PQM_ACT_NONE, PQM_ACT_SILU z / (1 + e^-z), or PQM_ACT_GELU
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.  Sums are binary32 and the
+ * activation takes z before its rounding.  A NaN or an infinity of x or of
+ * residual reaches its own row of y, one of w or bias its own column.  bf16 y
+ * may be the memory of residual, with ldr == N (PQM_ERR_SHAPE); nothing else
+ * may overlap an output.  workspace (device, 16-byte aligned, contents
+ * irrelevant): pqm_linear_workspace bytes, 0 for many sizes; calls that may run
+ * at the same time need separate ones.  A row's sums depend on the sizes alone
+ * besides its own values.
+ * Requires K % 8 == 0, 8 <= K <= 2^22, 0 <= N <= 2^22, M < 2^31 with fewer than
+ * 2^24 tiles of 128 x 128 and M (N + K) <= 2^40, K <= ldx <= 2^22,
+ * N <= ldr <= 2^22 (PQM_ERR_SHAPE); x, w, y, z and ldx aligned to 16 bytes,
+ * bias 4, residual 2 (PQM_ERR_ALIGN).  N and ldr of whole 8 and residual
+ * aligned to 16 bytes are stored faster.
+ */
+typedef enum pqm_act {
+    PQM_ACT_NONE = 0,
+    PQM_ACT_SILU = 1,
+    PQM_ACT_GELU = 2
+} pqm_act;
+pqm_status pqm_linear(const uint16_t *x, int64_t ldx, const uint16_t *w, const float *bias,
+                      pqm_act act, const uint16_t *residual, int64_t ldr, int64_t M, int64_t N,
+                      int64_t K, void *y, pqm_dtype y_dtype, uint16_t *z, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+size_t pqm_linear_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Gradients of that product (the residual's is dy itself):
+ *   dz = bf16(dy act'(z)), the operand type of the products; without an
+ *        activation it is dy, and z and dz are not used
+ *   dx = bf16(dz W + d_x), d_x (bf16 [M, K], row stride ldd, may be NULL): a
+ *        gradient that reaches x past this product
+ *   dw [N, K] = dz^T x and dbias [N] = sum of dz's rows, binary32, each sum in a
+ *        fixed order
+ * dy [M, N] bf16, row stride lddy; z and dz bf16 [M, N], dx bf16 [M, K],
+ * contiguous.  dx, dw, dbias may be NULL, but not all three; x is read for dw
+ * only, w for dx only.  dx may be the memory of d_x, with ldd == K, and dz that
+ * of z; nothing else may overlap an output.  M == 0 writes dw = 0, dbias = 0.
+ * workspace as above, of pqm_linear_backward_workspace bytes.
+ * Requires the sizes above, N >= 8, N % 8 == 0, N <= lddy <= 2^22,
+ * K <= ldx, ldd <= 2^22 (PQM_ERR_SHAPE); all tensors, lddy and ldx aligned to
+ * 16 bytes, d_x to 2 (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_linear_backward(const uint16_t *dy, int64_t lddy, const uint16_t *x, int64_t ldx,
+                               const uint16_t *w, pqm_act act, const uint16_t *z,
+                               const uint16_t *d_x, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                               uint16_t *dz, uint16_t *dx, float *dw, float *dbias,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+
 #ifdef __cplusplus
 }
 #endif

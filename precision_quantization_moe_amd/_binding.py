@@ -13,6 +13,7 @@ FMT_BF16, FMT_MXFP8, FMT_NVFP4, FMT_FP8_BLOCK = 0, 1, 2, 3
 GEMM_FPROP, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
 OUT_BF16, OUT_FP32 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 
 _STATUS = {0: "ok", 1: "PQM_ERR_NULL", 2: "PQM_ERR_SHAPE", 3: "PQM_ERR_ALIGN",
            4: "PQM_ERR_ENUM", 5: "PQM_ERR_WORKSPACE", 6: "PQM_ERR_HIP"}
@@ -66,6 +67,11 @@ SIGNATURES = {
                                P], I32),
     "pqm_moe_gemv_nvfp4": ([P, P, I64, I64, P, P, P, I64, I64, I64, I64, P, I32, P], I32),
     "pqm_moe_gemv_swiglu_nvfp4": ([P, P, P, I64, I64, P, P, P, I64, I64, I64, I64, P, P], I32),
+    "pqm_linear": ([P, I64, P, P, I32, P, I64, I64, I64, I64, P, I32, P, P, SZ, P], I32),
+    "pqm_linear_workspace": ([I64, I64, I64], SZ),
+    "pqm_linear_backward": ([P, I64, P, I64, P, I32, P, P, I64, I64, I64, I64, P, P, P, P, P, SZ,
+                             P], I32),
+    "pqm_linear_backward_workspace": ([I64, I64, I64], SZ),
 }
 
 
@@ -420,6 +426,87 @@ def moe_gemv_swiglu_nvfp4(x: torch.Tensor, ids: torch.Tensor, prob: torch.Tensor
     _call("pqm_moe_gemv_swiglu_nvfp4", dev, _ptr(x), _ptr(ids), _ptr(prob), rows, divisor,
           _ptr(w_q), _ptr(w_scale), _ptr(w_outer), rps, G, inter, K, _ptr(d))
     return d
+
+
+# ---------------------------------------------------------- dense products
+
+def _rows(t: torch.Tensor, what: str, shape, dev: torch.device) -> int:
+    """The row stride of t, a bf16 tensor of that shape on dev whose rows are
+    contiguous."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{what}: expected torch.bfloat16, got {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{what}: on {t.device}, expected {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]
+    if t.stride(1) != 1 or t.stride(0) < shape[1]:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.stride(0)
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+           act: int = ACT_NONE, residual: torch.Tensor | None = None, keep_z: bool = False,
+           out_dtype: int = OUT_BF16):
+    """act(x w^T + bias) + residual in one pass; see pqm_linear in pqmoe.h.  x
+    bf16 [M, K] and residual bf16 [M, N] with contiguous rows, w bf16 [N, K],
+    bias float32 [N].  Returns (y [M, N], z bf16 [M, N]), z, what the activation
+    took, None without keep_z."""
+    _bf16_2d(x)
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    ldx = _rows(x, "x", (M, K), dev)
+    _want(w, "w", torch.bfloat16, (N, K), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (N,), dev)
+    ldr = _rows(residual, "residual", (M, N), dev) if residual is not None else 0
+    y = torch.empty(M, N, dtype=torch.float32 if out_dtype == OUT_FP32 else torch.bfloat16,
+                    device=dev)
+    z = torch.empty(M, N, dtype=torch.bfloat16, device=dev) if keep_z else None
+    ws, size = None, 0
+    if M > 64:
+        size = lib().pqm_linear_workspace(M, N, K)
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _call("pqm_linear", dev, _ptr(x), ldx, _ptr(w), _ptr(bias), act, _ptr(residual), ldr, M, N, K,
+          _ptr(y), out_dtype, _ptr(z), _ptr(ws), size)
+    return y, z
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: int = ACT_NONE,
+                    z: torch.Tensor | None = None, d_x: torch.Tensor | None = None,
+                    need_dx: bool = True, need_dw: bool = True, need_dbias: bool = False):
+    """Gradients of linear; see pqm_linear_backward in pqmoe.h.  dy bf16 [M, N]
+    and x bf16 [M, K] with contiguous rows; z the forward call's, needed with an
+    activation; d_x (bf16 [M, K], may be None): a gradient that reaches x past
+    the product, added to dx.  Returns (dx bf16 [M, K], dw float32 [N, K],
+    dbias float32 [N], dz bf16 [M, N]), None for what was not asked for; dz is
+    None without an activation (it is dy)."""
+    _bf16_2d(dy)
+    M, N = dy.shape
+    K = w.shape[1]
+    dev = dy.device
+    lddy = _rows(dy, "dy", (M, N), dev)
+    ldx = _rows(x, "x", (M, K), dev)
+    _want(w, "w", torch.bfloat16, (N, K), dev)
+    dz = None
+    if act != ACT_NONE:
+        if z is None:
+            raise ValueError("z: needed with an activation")
+        _want(z, "z", torch.bfloat16, (M, N), dev)
+        dz = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    ldd = _rows(d_x, "d_x", (M, K), dev) if d_x is not None else 0
+    dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev) if need_dx else None
+    dw = torch.empty(N, K, dtype=torch.float32, device=dev) if need_dw else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
+    size = lib().pqm_linear_backward_workspace(M, N, K)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _call("pqm_linear_backward", dev, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), act,
+          _ptr(z) if act != ACT_NONE else None, _ptr(d_x), ldd, M, N, K, _ptr(dz), _ptr(dx),
+          _ptr(dw), _ptr(db), _ptr(ws), size)
+    return dx, dw, db, dz
 
 
 # ---------------------------------------------------------------- MoE glue

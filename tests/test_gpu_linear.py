@@ -1,0 +1,306 @@
+"""Dense products with their epilogue and their gradients against binary64 on
+the same values.
+
+Bounds, from the arithmetic: a binary32 sum of n exact products is off by at
+most n + 32 whole steps (2 U) of the sum of their magnitudes, also where the
+matrix core truncates; splits add at most 64 more.  z adds the bias (one
+rounding); the activation's relative error is that of its argument s in e^-s
+(|s| + 12 steps cover the argument, the hardware's exponential and reciprocal)
+and its slope is at most 1.2; a bf16 result adds half a step of bf16."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import precision_quantization_moe_amd as pqm
+from gpu_util import requires_gpu
+from operators_ref import HALF_BF16, U, f64
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+TINY = 2.0 ** -125  # results below binary32's normal range may be flushed
+
+
+def rand(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).to(torch.bfloat16)
+
+
+def squash(z, act):
+    return z if act == pqm.ACT_SILU else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+
+
+def activation(z, act):
+    """(act(z), act'(z), relative steps of the evaluation)."""
+    if act == pqm.ACT_NONE:
+        return z, torch.ones_like(z), torch.zeros_like(z)
+    s = squash(z, act)
+    v = torch.sigmoid(s)
+    ds = torch.ones_like(z) if act == pqm.ACT_SILU else \
+        2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    return z * v, v + z * v * torch.sigmoid(-s) * ds, 2 * s.abs() + 12
+
+
+def check(got, want, slack, what, half=0.0):
+    got = f64(got)
+    err = (got - want).abs()
+    bound = slack + half * (want.abs() + slack) + TINY
+    assert got.shape == want.shape, what
+    bad = ~(err <= bound)
+    assert not bad.any(), (what, int(bad.sum()), float((err / bound).max()))
+
+
+def forward(M, N, K, act, bias, residual, f32, keep_z, ldx=0, ldr=0, seed=0):
+    g = torch.Generator().manual_seed(1000 * M + 10 * N + K + seed)
+    x, w = rand(g, M, K + ldx), rand(g, N, K, scale=1 / math.sqrt(K))
+    b = torch.randn(N, generator=g) if bias else None
+    r = rand(g, M, N + ldr) if residual else None
+    y, z = pqm.linear(x.cuda()[:, :K], w.cuda(), b.cuda() if bias else None, act,
+                      r.cuda()[:, :N] if residual else None, keep_z,
+                      pqm.OUT_FP32 if f32 else pqm.OUT_BF16)
+    torch.cuda.synchronize()
+    xd, wd = f64(x)[:, :K], f64(w)
+    zd = xd @ wd.t()
+    slack = (K + 96) * 2 * U * (xd.abs() @ wd.abs().t())
+    if bias:
+        zd = zd + f64(b)
+        slack = slack + U * zd.abs()
+    slack = slack * 1.01
+    a, _, steps = activation(zd, act)
+    s = 1.2 * slack + steps * U * a.abs()
+    if residual:
+        a = a + f64(r)[:, :N]
+        s = s + 2 * U * a.abs()
+    if keep_z:
+        check(z, zd, slack, "z", HALF_BF16)
+    check(y, a, s, "y", 0.0 if f32 else HALF_BF16)
+
+
+# one row to a few tiles, ragged in every size, every way through the kernels
+SIZES = [(1, 1, 8), (1, 128, 2048), (3, 17, 40), (7, 4096, 72), (16, 100, 512), (17, 33, 264),
+         (40, 65, 1000), (64, 513, 136), (65, 8, 64), (65, 129, 8), (100, 300, 1048),
+         (128, 128, 32), (129, 127, 40), (255, 257, 104), (777, 96, 2056), (1030, 1001, 88),
+         (3584, 4100, 72), (4097, 3600, 40)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward_sizes(M, N, K):
+    forward(M, N, K, pqm.ACT_NONE, False, False, True, False)
+    forward(M, N, K, pqm.ACT_GELU, True, True, False, True)
+
+
+@pytest.mark.parametrize("act", [pqm.ACT_NONE, pqm.ACT_SILU, pqm.ACT_GELU])
+@pytest.mark.parametrize("bias,residual", [(False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M", [5, 200])
+def test_forward_epilogues(act, bias, residual, f32, M):
+    forward(M, 136, 160, act, bias, residual, f32, True)
+    forward(M, 75, 160, act, bias, residual, f32, True)
+
+
+@pytest.mark.parametrize("M,N", [(9, 64), (130, 64), (130, 61)])
+def test_forward_strides(M, N):
+    forward(M, N, 96, pqm.ACT_SILU, True, True, False, True, ldx=8, ldr=8)
+    forward(M, N, 96, pqm.ACT_SILU, True, True, False, True, ldx=40, ldr=3)
+
+
+def test_in_place_residual():
+    """y in the residual's memory, through the library itself (the Python form
+    makes a new y)."""
+    for M in (6, 300):
+        g = torch.Generator().manual_seed(M)
+        x, w, r = rand(g, M, 64).cuda(), rand(g, 128, 64).cuda(), rand(g, M, 128).cuda()
+        want, _ = pqm.linear(x, w, None, pqm.ACT_SILU, r)
+        size = pqm.lib().pqm_linear_workspace(M, 128, 64)
+        ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
+        code = pqm.lib().pqm_linear(x.data_ptr(), 64, w.data_ptr(), None, pqm.ACT_SILU, r.data_ptr(),
+                                    128, M, 128, 64, r.data_ptr(), pqm.OUT_BF16, None,
+                                    ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert code == 0 and torch.equal(r, want)
+
+
+def test_nothing_leaves_its_row_or_column():
+    """A NaN or an infinity of a row of x, or of w, stays in its row or column,
+    and the bytes around y and z are left alone."""
+    for M, N, K in ((33, 50, 40), (300, 261, 72)):
+        g = torch.Generator().manual_seed(M)
+        x, w = rand(g, M, K), rand(g, N, K)
+        clean, _ = pqm.linear(x.cuda(), w.cuda())
+        x[M // 2, K - 1] = float("nan")
+        x[M - 1, 0] = float("inf")
+        w[N - 3, 1] = float("nan")
+        y, _ = pqm.linear(x.cuda(), w.cuda())
+        torch.cuda.synchronize()
+        rows = [r for r in range(M) if r not in (M // 2, M - 1)]
+        cols = [c for c in range(N) if c != N - 3]
+        assert torch.equal(y[rows][:, cols], clean[rows][:, cols])
+        assert y[M // 2].isnan().all() and y[:, N - 3].isnan().all()
+        assert not y[M - 1, cols].isfinite().any()
+
+
+@pytest.mark.parametrize("act", [pqm.ACT_SILU, pqm.ACT_GELU])
+def test_activations_far_out(act):
+    """z from -3e38 to 3e38 through the bias: act and its slope stay finite and
+    reach their limits."""
+    far = torch.tensor([-3e38, -1e30, -1e13, -1e5, -200.0, -95.0, -89.0, -30.0, -8.0, -1.0, -0.0, 1e-30,
+                        1.0, 8.0, 30.0, 95.0, 200.0, 1e5, 1e13, 1e30, 3e38, 0.5, 2.0, -2.0])
+    N = far.numel()
+    x = torch.zeros(2, 8, dtype=torch.bfloat16).cuda()
+    w = torch.zeros(N, 8, dtype=torch.bfloat16).cuda()
+    y, z = pqm.linear(x, w, far.cuda(), act, keep_z=True, out_dtype=pqm.OUT_FP32)
+    a, _, steps = activation(f64(far), act)
+    a = torch.where(f64(far) < -1e12, torch.zeros_like(a), a)
+    slack = torch.where(a.abs() > 0, steps.clamp(max=2e3) * U * a.abs(), torch.zeros_like(a))
+    check(y, a.expand(2, N), slack + 100 * 2.0 ** -126, "act")
+    dy = torch.ones(2, N, dtype=torch.bfloat16).cuda()
+    dx, dw, db, dz = pqm.linear_backward(dy, x, w, act, z)
+    zb = f64(z)
+    v = torch.sigmoid(squash(zb, act))
+    _, slope, steps = activation(zb, act)
+    slope = torch.where(zb.abs() > 1e4, (zb > 0).double(), slope)
+    slack = torch.where(zb.abs() > 1e4, torch.zeros_like(zb),
+                        (steps + 8) * U * (v + (slope - v).abs()))
+    check(dz, slope, slack + 100 * 2.0 ** -126, "slope", HALF_BF16)
+
+
+def backward(M, N, K, act, add, bias, ldx=0, seed=0):
+    g = torch.Generator().manual_seed(1000 * M + 10 * N + K + seed)
+    x, w, dy = rand(g, M, K + ldx), rand(g, N, K, scale=1 / math.sqrt(K)), rand(g, M, N + ldx)
+    z = rand(g, M, N, scale=1.5) if act != pqm.ACT_NONE else None
+    a = rand(g, M, K + ldx) if add else None
+    dx, dw, db, dz = pqm.linear_backward(
+        dy.cuda()[:, :N], x.cuda()[:, :K], w.cuda(), act, z.cuda() if z is not None else None,
+        a.cuda()[:, :K] if add else None, need_dbias=bias)
+    torch.cuda.synchronize()
+    d, xd, wd = f64(dy)[:, :N], f64(x)[:, :K], f64(w)
+    if act != pqm.ACT_NONE:
+        zd = f64(z)
+        v = torch.sigmoid(squash(zd, act))
+        _, slope, steps = activation(zd, act)
+        check(dz, d * slope, (steps + 8) * U * d.abs() * (v + (slope - v).abs()), "dz", HALF_BF16)
+        d = f64(dz)
+    else:
+        assert dz is None
+    want = d @ wd
+    slack = (N + 96) * 2 * U * (d.abs() @ wd.abs())
+    if add:
+        want = want + f64(a)[:, :K]
+        slack = slack + 2 * U * want.abs()
+    check(dx, want, slack * 1.01, "dx", HALF_BF16)
+    check(dw, d.t() @ xd, 1.01 * (M + 96) * 2 * U * (d.abs().t() @ xd.abs()), "dw")
+    if bias:
+        # 16 rows a thread, 4 threads, then a 16th of the parts and 16 of them
+        check(db, d.sum(0), 1.01 * (40 + M / 1024 + 16) * U * d.abs().sum(0), "db")
+    else:
+        assert db is None
+
+
+BSIZES = [(1, 8, 8), (1, 128, 2048), (5, 16, 40), (33, 72, 264), (64, 256, 8), (65, 8, 264),
+          (100, 304, 1048), (129, 136, 40), (257, 264, 520), (1030, 96, 2056), (4000, 128, 256),
+          (3585, 3592, 72), (40, 3592, 3848)]
+
+
+@pytest.mark.parametrize("M,N,K", BSIZES)
+def test_backward_sizes(M, N, K):
+    backward(M, N, K, pqm.ACT_NONE, False, True)
+    backward(M, N, K, pqm.ACT_GELU, True, False)
+
+
+@pytest.mark.parametrize("act", [pqm.ACT_NONE, pqm.ACT_SILU, pqm.ACT_GELU])
+@pytest.mark.parametrize("add,bias", [(False, False), (True, True)])
+def test_backward_epilogues(act, add, bias):
+    backward(75, 40, 136, act, add, bias, ldx=8)
+    backward(300, 520, 136, act, add, bias, ldx=24)
+
+
+def test_backward_parts():
+    """Each gradient alone is the one of the whole call."""
+    g = torch.Generator().manual_seed(3)
+    dy, x, w = rand(g, 90, 64).cuda(), rand(g, 90, 72).cuda(), rand(g, 64, 72).cuda()
+    dx, dw, db, _ = pqm.linear_backward(dy, x, w, need_dbias=True)
+    only = pqm.linear_backward(dy, x, w, need_dw=False)
+    assert torch.equal(only[0], dx) and only[1] is None and only[2] is None
+    assert torch.equal(pqm.linear_backward(dy, x, w, need_dx=False)[1], dw)
+    assert torch.equal(pqm.linear_backward(dy, x, w, need_dx=False, need_dw=False, need_dbias=True)[2], db)
+
+
+def test_no_rows():
+    g = torch.Generator().manual_seed(4)
+    x, w = rand(g, 0, 64).cuda(), rand(g, 40, 64).cuda()
+    y, z = pqm.linear(x, w, keep_z=True)
+    assert y.shape == z.shape == (0, 40)
+    dx, dw, db, dz = pqm.linear_backward(y, x, w, pqm.ACT_SILU, z, need_dbias=True)
+    torch.cuda.synchronize()
+    assert dx.shape == (0, 64) and not dw.any() and not db.any() and dw.shape == (40, 64)
+
+
+def test_rows_do_not_depend_on_their_place():
+    """A row's values are the same wherever it stands in a call of the same
+    sizes, and every call gives the same bits."""
+    g = torch.Generator().manual_seed(5)
+    for M in (30, 700):
+        x, w = rand(g, M, 520).cuda(), rand(g, 96, 520).cuda()
+        y, _ = pqm.linear(x, w, act=pqm.ACT_SILU, out_dtype=pqm.OUT_FP32)
+        p = torch.randperm(M, generator=g).cuda()
+        a, _ = pqm.linear(x[p].contiguous(), w, act=pqm.ACT_SILU, out_dtype=pqm.OUT_FP32)
+        assert torch.equal(a, y[p])
+        assert torch.equal(pqm.linear(x, w, act=pqm.ACT_SILU, out_dtype=pqm.OUT_FP32)[0], y)
+
+
+def test_captured_forward_and_backward():
+    g = torch.Generator().manual_seed(6)
+    M, N, K = 600, 128, 1024  # split contractions: both passes use a workspace
+    x, w, b = rand(g, M, K).cuda(), rand(g, N, K).cuda(), torch.randn(N, generator=g).cuda()
+    add = rand(g, M, K).cuda()
+
+    def step():
+        y, z = pqm.linear(x, w, b, pqm.ACT_GELU, keep_z=True)
+        return (y, z) + pqm.linear_backward(y, x, w, pqm.ACT_GELU, z, add, need_dbias=True)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        x.copy_(rand(g, M, K))
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(out, want)), i
+
+
+def test_on_another_stream():
+    g = torch.Generator().manual_seed(7)
+    x, w = rand(g, 256, 512).cuda(), rand(g, 128, 512).cuda()
+    want, _ = pqm.linear(x, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got, _ = pqm.linear(x, w)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^31 elements of y and of dy: offsets leave 32 bits."""
+    M, N, K = 70000, 32768, 8
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16)
+    y, _ = pqm.linear(x, w)
+    rows = torch.tensor([0, 1, 65535, 65536, 69998, 69999], device="cuda")
+    want = f64(x[rows]) @ f64(w).t()
+    slack = 104 * 2 * U * (f64(x[rows]).abs() @ f64(w).abs().t())
+    check(y[rows], want, slack, "y", HALF_BF16)
+    dx, dw, db, _ = pqm.linear_backward(y, x, w, need_dbias=True)
+    yd = f64(y[rows])
+    check(dx[rows], yd @ f64(w), (N + 96) * 2 * U * (yd.abs() @ f64(w).abs()), "dx", HALF_BF16)
+    cols = torch.tensor([0, 7, 20000, 32767], device="cuda")
+    yc = f64(y[:, cols])
+    check(dw[cols], yc.t() @ f64(x), (M + 96) * 2 * U * (yc.abs().t() @ f64(x).abs()), "dw")
+    check(db[cols], yc.sum(0), 1.01 * (56 + M / 1024) * U * yc.abs().sum(0), "db")
