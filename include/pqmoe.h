@@ -761,6 +761,60 @@ pqm_status pqm_linear_backward(const uint16_t *dy, int64_t lddy, const uint16_t 
                                void *workspace, size_t workspace_bytes, hipStream_t stream);
 size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 
+/*
+ * What a policy's logits say of given tokens: the log probabilities that
+ * rollout and training are compared by ([MT] 4.5: one formula and one order of
+ * the sums on both sides), the entropy of each row, and its best alternatives.
+ * With x a row of logits, M its largest, u_i = (x_i - M) / temperature,
+ * S = sum e^u:
+ *   logprob = u_id - log S,   entropy = log S - (sum e^u u) / S,
+ *   stats = (M, log S), for the backward pass; M / temperature + log S is the
+ *       row's log-sum-exp,
+ *   top_ids, top_logprob: the top_n largest logits, equal ones in the order of
+ *       their index, and their log probabilities
+ *   logits [tokens, vocab] bf16 or binary32 (logits_dtype), row stride ld; ids
+ *   int32 [tokens]; logprob, entropy [tokens], stats [tokens, 2], top_logprob
+ *   [tokens, top_n] binary32; top_ids int32 [tokens, top_n]        (device)
+ * ids may be NULL, then logprob has to be; a row whose id lies outside
+ * [0, vocab) is left out: its logits are not read, its results are 0 and its
+ * top_ids -1.  logprob, entropy, stats may be NULL (one result is required).
+ * A logit of -inf is a token that cannot come; a row of -inf alone has
+ * logprob -inf, entropy 0, stats (-inf, 0).  A NaN or +inf makes the row's
+ * results NaN (M apart); a NaN ranks first.  The arithmetic is binary32.
+ * workspace (device, 8-byte aligned, contents irrelevant):
+ * pqm_token_logprobs_workspace bytes, 0 where a row is one workgroup's; calls
+ * that may run at the same time need separate ones.
+ * Requires 1 <= vocab <= 2^30, vocab <= ld <= 2^30, tokens < 2^31,
+ * 0 <= top_n <= 32, top_n <= vocab, 2^-60 <= temperature <= 2^60
+ * (PQM_ERR_SHAPE); tensors aligned to their element (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_token_logprobs(const void *logits, pqm_dtype logits_dtype, int64_t ld,
+                              const int32_t *ids, int64_t tokens, int64_t vocab, float temperature,
+                              float *logprob, float *entropy, float *stats, int32_t *top_ids,
+                              float *top_logprob, int64_t top_n, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+size_t pqm_token_logprobs_workspace(int64_t tokens, int64_t vocab, int64_t top_n);
+
+/*
+ * Gradient with respect to the logits, for the gradients d_logprob and
+ * d_entropy (binary32 [tokens], either may be NULL) of the two:
+ *   d_i = (d_logprob ([i = id] - p_i) - d_entropy p_i (log p_i + entropy))
+ *         / temperature
+ * rounded once to d_logits_dtype; zero in rows that are left out and in rows
+ * of -inf alone.  stats and entropy (needed with d_entropy) are the forward
+ * call's, the other arguments too.  d_logits [tokens, vocab], row stride ldd,
+ * may be the memory of logits, with the same type and stride (PQM_ERR_SHAPE),
+ * and may not overlap it otherwise.  ids may be NULL with d_logprob NULL.
+ * Same limits and errors; ldd as ld.
+ */
+pqm_status pqm_token_logprobs_backward(const void *logits, pqm_dtype logits_dtype, int64_t ld,
+                                       const int32_t *ids, int64_t tokens, int64_t vocab,
+                                       float temperature, const float *stats,
+                                       const float *entropy, const float *d_logprob,
+                                       const float *d_entropy, void *d_logits,
+                                       pqm_dtype d_logits_dtype, int64_t ldd,
+                                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,6 +72,10 @@ SIGNATURES = {
     "pqm_linear_backward": ([P, I64, P, I64, P, I32, P, P, I64, I64, I64, I64, P, P, P, P, P, SZ,
                              P], I32),
     "pqm_linear_backward_workspace": ([I64, I64, I64], SZ),
+    "pqm_token_logprobs": ([P, I32, I64, P, I64, I64, F32, P, P, P, P, P, I64, P, SZ, P], I32),
+    "pqm_token_logprobs_workspace": ([I64, I64, I64], SZ),
+    "pqm_token_logprobs_backward": ([P, I32, I64, P, I64, I64, F32, P, P, P, P, P, I32, I64, P],
+                                    I32),
 }
 
 
@@ -507,6 +511,85 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: int
           _ptr(z) if act != ACT_NONE else None, _ptr(d_x), ldd, M, N, K, _ptr(dz), _ptr(dx),
           _ptr(dw), _ptr(db), _ptr(ws), size)
     return dx, dw, db, dz
+
+
+# -------------------------------------------------------- log probabilities
+
+def _logits(t: torch.Tensor, what: str):
+    """(type, row stride) of logits [T, V] with contiguous rows."""
+    dt = _bf16_or_f32(t, what)
+    if not t.is_cuda:
+        raise TypeError("expected a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected two dimensions")
+    if t.is_contiguous():
+        return dt, t.shape[1]
+    if t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return dt, t.stride(0)
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None,
+                   temperature: float = 1.0, top_n: int = 0):
+    """Log probabilities of given tokens, entropies and the best alternatives;
+    see pqm_token_logprobs in pqmoe.h.  logits bf16 or float32 [T, V] with
+    contiguous rows; ids int32 [T], negative for rows to leave out, None for
+    alternatives alone.  Returns (logprob [T], entropy [T], stats [T, 2], top_ids
+    int32 [T, top_n], top_logprob [T, top_n]), float32; logprob is None without
+    ids, the last two without top_n."""
+    dt, ld = _logits(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    f32 = dict(dtype=torch.float32, device=dev)
+    lp = None
+    if ids is not None:
+        _want(ids, "ids", torch.int32, (T,), dev)
+        lp = torch.empty(T, **f32)
+    entropy = torch.empty(T, **f32)
+    stats = torch.empty(T, 2, **f32)
+    top_ids = top_lp = ws = None
+    if top_n:
+        top_ids = torch.empty(T, max(top_n, 0), dtype=torch.int32, device=dev)
+        top_lp = torch.empty(T, max(top_n, 0), **f32)
+    size = lib().pqm_token_logprobs_workspace(T, V, top_n)
+    if size:
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _call("pqm_token_logprobs", dev, _ptr(logits), dt, ld, _ptr(ids), T, V, temperature, _ptr(lp),
+          _ptr(entropy), _ptr(stats), _ptr(top_ids), _ptr(top_lp), top_n, _ptr(ws), size)
+    return lp, entropy, stats, top_ids, top_lp
+
+
+def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, stats: torch.Tensor,
+                            d_logprob: torch.Tensor | None, temperature: float = 1.0,
+                            entropy: torch.Tensor | None = None,
+                            d_entropy: torch.Tensor | None = None, out_dtype: int | None = None,
+                            out: torch.Tensor | None = None):
+    """Gradient of token_logprobs with respect to its logits; see
+    pqm_token_logprobs_backward in pqmoe.h.  stats and entropy are the forward
+    call's (entropy with d_entropy alone).  Returns d_logits [T, V] in the
+    logits' type unless out_dtype says otherwise; `out` may pass it, also the
+    logits themselves."""
+    dt, ld = _logits(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    if ids is not None:
+        _want(ids, "ids", torch.int32, (T,), dev)
+    _want(stats, "stats", torch.float32, (T, 2), dev)
+    for name, t in (("d_logprob", d_logprob), ("entropy", entropy), ("d_entropy", d_entropy)):
+        if t is not None:
+            _want(t, name, torch.float32, (T,), dev)
+    odt = dt if out_dtype is None else out_dtype
+    if out is None:
+        out = torch.empty(T, V, dtype=torch.float32 if odt == OUT_FP32 else torch.bfloat16,
+                          device=dev)
+        ldd = V
+    else:
+        odt, ldd = _logits(out, "out")
+        if out.shape != logits.shape or out.device != dev:
+            raise ValueError("out: expected the logits' shape and device")
+    _call("pqm_token_logprobs_backward", dev, _ptr(logits), dt, ld, _ptr(ids), T, V, temperature,
+          _ptr(stats), _ptr(entropy), _ptr(d_logprob), _ptr(d_entropy), _ptr(out), odt, ldd)
+    return out
 
 
 # ---------------------------------------------------------------- MoE glue

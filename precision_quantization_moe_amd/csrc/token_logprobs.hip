@@ -1,0 +1,581 @@
+// token_logprobs.hip -- what a policy's logits [T, V] say of given tokens: their
+// log probabilities, the entropy of each row, its best alternatives, and the
+// gradient of the first two.
+//
+// With x a row of logits, t the temperature, M its largest logit,
+//   u_i = (x_i - M) / t,  S = sum e^u,  log p_i = u_i - log S,
+//   H = log S - (sum e^u u) / S,
+//   d x_i = (g [i = id] - p_i (g + h (log p_i + H))) / t
+// for the gradients g of log p_id and h of H.  One pass reads the row: each
+// thread carries its running maximum, sum and weighted sum, and moves the sums
+// when its maximum grows.  u is formed from the difference, which neither
+// overflows nor loses digits where all logits are far from 0; in powers of two,
+// u log2(e).
+#include "pqm_device.hpp"
+#include "pqm_internal.hpp"
+#include "pqmoe.h"
+
+#include <type_traits>
+
+namespace pqm {
+
+namespace {
+
+constexpr int TL_TOP = 32;         // alternatives at most
+constexpr int TL_TILE = 2048;      // logits of a workgroup's turn: 256 threads, eight each
+constexpr int TL_PARTS = 128;      // parts of a row at most
+constexpr int TL_JOIN = 2048;      // candidates of a row's parts at most
+constexpr float TL_LOG2E = 1.44269504088896341f, TL_LN2 = 0.69314718055994531f;
+
+typedef uint64_t tl_key;  // a logit's order, then the lower index; 0: none
+
+// Sixteen bytes at any element's address: rows of an odd length start anywhere.
+struct __attribute__((packed, aligned(2))) TlWords {
+  uint32_t w[4];
+};
+
+template <bool F32>
+__device__ __forceinline__ float tl_one(const void *row, int64_t i) {
+  if (F32) return static_cast<const float *>(row)[i];
+  return bf16_lo_f32(static_cast<const uint16_t *>(row)[i]);
+}
+
+// Eight logits from i on, -inf past the end.
+template <bool F32>
+__device__ __forceinline__ void tl_load8(const void *row, int64_t i, int64_t end, float (&x)[8]) {
+  if (i + 8 <= end) {
+    if (F32) {
+      const TlWords *p = reinterpret_cast<const TlWords *>(static_cast<const float *>(row) + i);
+      const TlWords a = p[0], b = p[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = __uint_as_float(a.w[j]);
+        x[4 + j] = __uint_as_float(b.w[j]);
+      }
+    } else {
+      const TlWords a =
+          *reinterpret_cast<const TlWords *>(static_cast<const uint16_t *>(row) + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16_lo_f32(a.w[j]);
+        x[2 * j + 1] = bf16_hi_f32(a.w[j]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = i + j < end ? tl_one<F32>(row, i + j) : -__builtin_inff();
+}
+
+// Running statistics: the maximum, the sum and the sum weighted by u log2(e).
+// A NaN is no maximum, but reaches the sum.
+struct TlSums {
+  float m, s, t;
+};
+
+// Where nothing but -inf was seen, differences are taken from 0.
+__device__ __forceinline__ float tl_from(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// The exponent of a logit d below the maximum; from -200 on down all are 0 in
+// binary32, and -inf times 0 would be a NaN.
+__device__ __forceinline__ float tl_exponent(float d, float c) {
+  return __builtin_elementwise_maximum(d * c, -200.0f);
+}
+
+__device__ __forceinline__ void tl_move(TlSums &a, float m, float c) {
+  const float d = tl_exponent(a.m - tl_from(m), c), f = __builtin_amdgcn_exp2f(d);
+  a.t = f * __builtin_fmaf(a.s, d, a.t);
+  a.s *= f;
+  a.m = m;
+}
+
+__device__ __forceinline__ void tl_join(TlSums &a, TlSums b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  tl_move(a, m, c);
+  tl_move(b, m, c);
+  a.s += b.s;
+  a.t += b.t;
+}
+
+__device__ __forceinline__ void tl_add8(TlSums &a, const float (&x)[8], float c) {
+  const float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  if (m > a.m) tl_move(a, m, c);
+  const float from = tl_from(a.m);
+  float s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float u = tl_exponent(x[j] - from, c), e = __builtin_amdgcn_exp2f(u);
+    s[j & 1] += e;
+    t[j & 1] = __builtin_fmaf(e, u, t[j & 1]);
+  }
+  a.s += s[0] + s[1];
+  a.t += t[0] + t[1];
+}
+
+// The workgroup's statistics in thread 0.
+__device__ __forceinline__ TlSums tl_reduce(TlSums a, float c, TlSums *sh) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const TlSums b = {__shfl_down(a.m, o, 64), __shfl_down(a.s, o, 64), __shfl_down(a.t, o, 64)};
+    tl_join(a, b, c);
+  }
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 4; ++w) tl_join(a, sh[w], c);
+  }
+  return a;
+}
+
+// A logit's place in the order: NaN first, -0 as +0; above 0 for every logit.
+__device__ __forceinline__ uint32_t tl_order(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return x != x ? 0xFFFFFFFFu : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float tl_value(uint32_t o) {
+  return o == 0xFFFFFFFFu ? __builtin_nanf("")
+                          : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ tl_key tl_make(float x, int64_t i) {
+  return (tl_key)tl_order(x) << 32 | (0xFFFFFFFFu - (uint32_t)i);
+}
+
+// The n best keys so far, in order.
+struct TlTop {
+  tl_key kept[TL_TOP];
+  tl_key best[256];
+  tl_key cand[TL_TOP + 8 * TL_TOP];
+  int count;
+  tl_key bar;
+};
+
+__device__ __forceinline__ void tl_top_init(TlTop &s) {
+  if (threadIdx.x < TL_TOP) s.kept[threadIdx.x] = 0;
+  __syncthreads();
+}
+
+// Takes in eight keys a thread.  At most n threads hold one of the n best among
+// the threads' own best; keys below the n-th of those best cannot be among the n
+// best of all, so no more than 8 n candidates are left however the logits are
+// ordered, and ranking them by counting stays cheap.
+__device__ __forceinline__ void tl_top_add(TlTop &s, const tl_key (&k)[8], int n) {
+  tl_key top = k[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) top = k[j] > top ? k[j] : top;
+  const tl_key last = s.kept[n - 1];
+  const int hits = __syncthreads_count(top > last);
+  if (hits == 0) return;
+  if (threadIdx.x < n) s.cand[threadIdx.x] = s.kept[threadIdx.x];
+  s.best[threadIdx.x] = top;
+  if (threadIdx.x == 0) {
+    s.count = n;
+    s.bar = last + 1;
+  }
+  __syncthreads();
+  if (hits > n) {
+    int above = 0;
+#pragma unroll 8
+    for (int i = 0; i < 256; ++i) above += s.best[i] > top ? 1 : 0;
+    if (above == n - 1 && top > last) s.bar = top;  // keys differ: one thread
+    __syncthreads();
+  }
+  const tl_key bar = s.bar;
+  if (top >= bar) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k[j] >= bar) s.cand[atomicAdd(&s.count, 1)] = k[j];
+  }
+  __syncthreads();
+  const int count = s.count;
+  for (int i = threadIdx.x; i < count; i += 256) {
+    const tl_key mine = s.cand[i];
+    int above = 0;
+    for (int j = 0; j < count; ++j) above += s.cand[j] > mine ? 1 : 0;
+    if (above < n && mine != 0) s.kept[above] = mine;
+  }
+  __syncthreads();
+}
+
+struct TlArgs {
+  const void *x;
+  int64_t ld;
+  const int32_t *ids;
+  int64_t V;
+  float temperature, c;  // c = log2(e) / temperature
+  float *logprob, *entropy, *stats;
+  int32_t *top_ids;
+  float *top_logprob;
+  int n;
+  int parts;
+  int64_t part;  // logits of a part
+  uint8_t *ws;
+};
+
+// A part's record: its statistics, then its keys.
+__device__ __forceinline__ uint8_t *tl_record(const TlArgs &a, int64_t row, int part) {
+  return a.ws + (row * a.parts + part) * (16 + 8 * a.n);
+}
+
+// The row's id; -1 for a row to leave out, 0 without ids.
+__device__ __forceinline__ int64_t tl_id(const TlArgs &a, int64_t row) {
+  if (!a.ids) return 0;
+  const int64_t i = a.ids[row];
+  return i < 0 || i >= a.V ? -1 : i;
+}
+
+// The row's results from its statistics (thread 0) and keys.
+template <bool F32>
+__device__ __forceinline__ void tl_finish(const TlArgs &a, int64_t row, int64_t id, const TlSums &s,
+                                          const TlTop *top, float *sh) {
+  const bool none = s.m == -__builtin_inff() && s.s == 0.0f;  // -inf alone
+  if (threadIdx.x == 0) {
+    const float log_s = none ? 0.0f : logf(s.s);
+    if (a.stats) {
+      a.stats[2 * row] = s.m;
+      a.stats[2 * row + 1] = log_s;
+    }
+    if (a.entropy) a.entropy[row] = none ? 0.0f : fmaxf(log_s - TL_LN2 * (s.t / s.s), 0.0f);
+    if (a.entropy && !none && s.s != s.s) a.entropy[row] = s.s;
+    if (a.logprob) {
+      const float x = tl_one<F32>(static_cast<const uint8_t *>(a.x) +
+                                      row * a.ld * (F32 ? 4 : 2), id);
+      a.logprob[row] = (x - tl_from(s.m)) / a.temperature - log_s;
+    }
+    sh[0] = s.m;
+    sh[1] = log_s;
+  }
+  if (!top) return;
+  __syncthreads();
+  if (threadIdx.x < a.n) {
+    const tl_key k = top->kept[threadIdx.x];
+    a.top_ids[row * a.n + threadIdx.x] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
+    a.top_logprob[row * a.n + threadIdx.x] =
+        (tl_value((uint32_t)(k >> 32)) - tl_from(sh[0])) / a.temperature - sh[1];
+  }
+}
+
+// A row that is left out.
+__device__ __forceinline__ void tl_skip(const TlArgs &a, int64_t row) {
+  if (threadIdx.x == 0) {
+    if (a.logprob) a.logprob[row] = 0.0f;
+    if (a.entropy) a.entropy[row] = 0.0f;
+    if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
+  }
+  if (threadIdx.x < a.n) {
+    a.top_ids[row * a.n + threadIdx.x] = -1;
+    a.top_logprob[row * a.n + threadIdx.x] = 0.0f;
+  }
+}
+
+}  // namespace
+
+// One part of one row a workgroup; a row of one part is finished here.
+template <bool F32, bool TOP>
+__global__ __launch_bounds__(256) void k_token_logprobs(TlArgs a) {
+  __shared__ TlSums sh[4];
+  __shared__ float fin[2];
+  __shared__ typename std::conditional<TOP, TlTop, int>::type top;
+  const int64_t row = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - row * a.parts);
+  const int64_t id = tl_id(a, row);
+  if (id < 0) {
+    if (a.parts == 1) tl_skip(a, row);
+    return;
+  }
+  const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ld * (F32 ? 4 : 2);
+  const int64_t i0 = part * a.part, end = min(a.V, i0 + a.part);
+  TlSums s = {-__builtin_inff(), 0.0f, 0.0f};
+  if constexpr (TOP) {
+    tl_top_init(top);
+    for (int64_t i = i0; i < end; i += TL_TILE) {  // every thread takes every turn
+      const int64_t at = i + 8 * threadIdx.x;
+      float v[8];
+      tl_load8<F32>(x, at, end, v);
+      tl_add8(s, v, a.c);
+      tl_key k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = at + j < end ? tl_make(v[j], at + j) : 0;
+      tl_top_add(top, k, a.n);
+    }
+  } else {
+    int64_t at = i0 + 8 * threadIdx.x;
+    for (; at + 3 * TL_TILE + 8 <= end; at += 4 * TL_TILE) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) tl_load8<F32>(x, at + u * TL_TILE, a.V, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) tl_add8(s, v[u], a.c);
+    }
+    for (; at < end; at += TL_TILE) {
+      float v[8];
+      tl_load8<F32>(x, at, end, v);
+      tl_add8(s, v, a.c);
+    }
+  }
+  s = tl_reduce(s, a.c, sh);
+  if (a.parts == 1) {
+    if constexpr (TOP) tl_finish<F32>(a, row, id, s, &top, fin);
+    else tl_finish<F32>(a, row, id, s, nullptr, fin);
+    return;
+  }
+  uint8_t *rec = tl_record(a, row, part);
+  if (threadIdx.x == 0) {
+    float *f = reinterpret_cast<float *>(rec);
+    f[0] = s.m;
+    f[1] = s.s;
+    f[2] = s.t;
+  }
+  if constexpr (TOP) {
+    if (threadIdx.x < a.n)
+      reinterpret_cast<tl_key *>(rec + 16)[threadIdx.x] = top.kept[threadIdx.x];
+  }
+}
+
+// The parts of a row, joined in one order.
+template <bool F32, bool TOP>
+__global__ __launch_bounds__(256) void k_token_logprobs_join(TlArgs a) {
+  __shared__ TlSums sh[4];
+  __shared__ float fin[2];
+  __shared__ typename std::conditional<TOP, TlTop, int>::type top;
+  const int64_t row = blockIdx.x, id = tl_id(a, row);
+  if (id < 0) return tl_skip(a, row);
+  TlSums s = {-__builtin_inff(), 0.0f, 0.0f};
+  if (threadIdx.x < a.parts) {
+    const float *f = reinterpret_cast<const float *>(tl_record(a, row, threadIdx.x));
+    s = TlSums{f[0], f[1], f[2]};
+  }
+  if constexpr (TOP) {
+    tl_top_init(top);
+    tl_key k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = threadIdx.x + 256 * j;
+      k[j] = i < a.parts * a.n
+                 ? reinterpret_cast<const tl_key *>(tl_record(a, row, i / a.n) + 16)[i % a.n]
+                 : 0;
+    }
+    tl_top_add(top, k, a.n);
+  }
+  s = tl_reduce(s, a.c, sh);
+  if constexpr (TOP) tl_finish<F32>(a, row, id, s, &top, fin);
+  else tl_finish<F32>(a, row, id, s, nullptr, fin);
+}
+
+namespace {
+
+struct TlBack {
+  const void *x;
+  int64_t ld;
+  const int32_t *ids;
+  int64_t V;
+  float temperature, c;
+  const float *stats, *entropy, *d_logprob, *d_entropy;
+  void *dx;
+  int64_t ldd;
+  int parts;
+};
+
+constexpr int TB_TURNS = 4;  // eight logits a thread each
+
+template <bool F32>
+__device__ __forceinline__ void tl_store8(void *row, int64_t i, int64_t end, const float (&v)[8]) {
+  if (i + 8 <= end) {
+    if (F32) {
+      TlWords *p = reinterpret_cast<TlWords *>(static_cast<float *>(row) + i);
+      TlWords a, b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a.w[j] = __float_as_uint(v[j]);
+        b.w[j] = __float_as_uint(v[4 + j]);
+      }
+      p[0] = a;
+      p[1] = b;
+    } else {
+      TlWords a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a.w[j] = pk_bf16_rne(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<TlWords *>(static_cast<uint16_t *>(row) + i) = a;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (i + j >= end) break;
+    if (F32) static_cast<float *>(row)[i + j] = v[j];
+    else static_cast<uint16_t *>(row)[i + j] = (uint16_t)pk_bf16_rne(v[j], 0.0f);
+  }
+}
+
+}  // namespace
+
+// Gradient: with l = log2 p, d x = [i = id] g / t - p (A + B l), A = (g + h H) / t,
+// B = h ln 2 / t.
+template <bool F32, bool OUTF32>
+__global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
+  const int64_t row = blockIdx.x / a.parts;
+  const int64_t at = (blockIdx.x - row * a.parts) * (int64_t)(TB_TURNS * TL_TILE) +
+                     8 * threadIdx.x;
+  const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ld * (F32 ? 4 : 2);
+  uint8_t *dx = static_cast<uint8_t *>(a.dx) + row * a.ldd * (OUTF32 ? 4 : 2);
+  int64_t id = a.ids ? a.ids[row] : 0;
+  const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+  const bool skip = id < 0 || id >= a.V || (m == -__builtin_inff() && log_s == 0.0f);
+  if (!a.ids) id = -1;
+  if (skip) {
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < TB_TURNS; ++u) tl_store8<OUTF32>(dx, at + u * TL_TILE, a.V, zero);
+    return;
+  }
+  const float ls = log_s * TL_LOG2E;
+  const float g = a.d_logprob ? a.d_logprob[row] / a.temperature : 0.0f;
+  const float h = a.d_entropy ? a.d_entropy[row] / a.temperature : 0.0f;
+  const float A = a.d_entropy ? __builtin_fmaf(h, a.entropy[row], g) : g, B = h * TL_LN2;
+  float v[TB_TURNS][8];
+#pragma unroll
+  for (int u = 0; u < TB_TURNS; ++u) tl_load8<F32>(x, at + u * TL_TILE, a.V, v[u]);
+#pragma unroll
+  for (int u = 0; u < TB_TURNS; ++u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float l =
+          __builtin_elementwise_maximum(__builtin_fmaf(v[u][j] - m, a.c, -ls), -200.0f);
+      v[u][j] = -__builtin_amdgcn_exp2f(l) * __builtin_fmaf(B, l, A);
+    }
+    const int64_t rel = id - (at + u * TL_TILE);
+    if (rel >= 0 && rel < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (rel == j) v[u][j] += g;
+    }
+    tl_store8<OUTF32>(dx, at + u * TL_TILE, a.V, v[u]);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+namespace {
+
+struct TlPlan {
+  int parts;
+  int64_t part;
+};
+
+// Parts of a row: as many as give the card 1024 workgroups, none below a turn.
+TlPlan tl_plan(int64_t tokens, int64_t V, int64_t n) {
+  const int64_t turns = (V + TL_TILE - 1) / TL_TILE;
+  int64_t parts = (1024 + tokens - 1) / tokens;
+  if (parts > TL_PARTS) parts = TL_PARTS;
+  if (n && parts > TL_JOIN / n) parts = TL_JOIN / n;
+  if (parts > turns) parts = turns;
+  const int64_t each = (turns + parts - 1) / parts;
+  return {(int)((turns + each - 1) / each), each * TL_TILE};
+}
+
+size_t tl_bytes(int64_t tokens, int64_t V, int64_t n) {
+  const TlPlan p = tl_plan(tokens, V, n);
+  return p.parts == 1 ? 0 : (size_t)tokens * p.parts * (16 + 8 * n);
+}
+
+bool tl_sizes(int64_t tokens, int64_t V, int64_t n) {
+  return tokens >= 0 && tokens < ((int64_t)1 << 31) && V >= 1 && V <= ((int64_t)1 << 30) && n >= 0 &&
+         n <= TL_TOP && n <= V;
+}
+
+bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; }
+
+template <bool F32>
+hipError_t tl_forward(const TlArgs &a, int64_t tokens, hipStream_t st) {
+  const dim3 grid((unsigned)(tokens * a.parts)), rows((unsigned)tokens), block(256);
+  if (a.n) hipLaunchKernelGGL((k_token_logprobs<F32, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_token_logprobs<F32, false>), grid, block, 0, st, a);
+  const hipError_t r = hipGetLastError();
+  if (r != hipSuccess || a.parts == 1) return r;
+  if (a.n) hipLaunchKernelGGL((k_token_logprobs_join<F32, true>), rows, block, 0, st, a);
+  else hipLaunchKernelGGL((k_token_logprobs_join<F32, false>), rows, block, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace pqm
+
+extern "C" {
+
+size_t pqm_token_logprobs_workspace(int64_t tokens, int64_t vocab, int64_t top_n) {
+  using namespace pqm;
+  return !tl_sizes(tokens, vocab, top_n) || tokens == 0 ? 0 : tl_bytes(tokens, vocab, top_n);
+}
+
+pqm_status pqm_token_logprobs(const void *logits, pqm_dtype logits_dtype, int64_t ld,
+                              const int32_t *ids, int64_t tokens, int64_t vocab, float temperature,
+                              float *logprob, float *entropy, float *stats, int32_t *top_ids,
+                              float *top_logprob, int64_t top_n, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  using namespace pqm;
+  if (logits_dtype != PQM_OUT_BF16 && logits_dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
+  if (!tl_sizes(tokens, vocab, top_n) || ld < vocab || ld > ((int64_t)1 << 30))
+    return PQM_ERR_SHAPE;
+  if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return PQM_ERR_SHAPE;
+  const bool f32 = logits_dtype == PQM_OUT_FP32;
+  const TlPlan p = tokens ? tl_plan(tokens, vocab, top_n) : TlPlan{1, vocab};
+  if (tokens * p.parts >= ((int64_t)1 << 31)) return PQM_ERR_SHAPE;
+  if (tokens == 0) return PQM_OK;
+  if (!logits || (!logprob && !entropy && !stats && !top_n) || (logprob && !ids) ||
+      (top_n && (!top_ids || !top_logprob)))
+    return PQM_ERR_NULL;
+  if (!al(logits, f32 ? 4 : 2) || !al(ids, 4) || !al(logprob, 4) || !al(entropy, 4) ||
+      !al(stats, 4) || !al(top_ids, 4) || !al(top_logprob, 4))
+    return PQM_ERR_ALIGN;
+  const size_t need = tl_bytes(tokens, vocab, top_n);
+  if (need) {
+    if (!workspace) return PQM_ERR_NULL;
+    if (workspace_bytes < need) return PQM_ERR_WORKSPACE;
+    if (!al(workspace, 8)) return PQM_ERR_ALIGN;
+  }
+  const TlArgs a = {logits, ld, ids, vocab, temperature, (float)(1.4426950408889634 / temperature),
+                    logprob, entropy, stats, top_ids, top_logprob, (int)top_n, p.parts, p.part,
+                    static_cast<uint8_t *>(workspace)};
+  return st_of(f32 ? tl_forward<true>(a, tokens, stream) : tl_forward<false>(a, tokens, stream));
+}
+
+pqm_status pqm_token_logprobs_backward(const void *logits, pqm_dtype logits_dtype, int64_t ld,
+                                       const int32_t *ids, int64_t tokens, int64_t vocab,
+                                       float temperature, const float *stats,
+                                       const float *entropy, const float *d_logprob,
+                                       const float *d_entropy, void *d_logits,
+                                       pqm_dtype d_logits_dtype, int64_t ldd,
+                                       hipStream_t stream) {
+  using namespace pqm;
+  if ((logits_dtype != PQM_OUT_BF16 && logits_dtype != PQM_OUT_FP32) ||
+      (d_logits_dtype != PQM_OUT_BF16 && d_logits_dtype != PQM_OUT_FP32))
+    return PQM_ERR_ENUM;
+  if (!tl_sizes(tokens, vocab, 0) || ld < vocab || ld > ((int64_t)1 << 30) || ldd < vocab ||
+      ldd > ((int64_t)1 << 30))
+    return PQM_ERR_SHAPE;
+  if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return PQM_ERR_SHAPE;
+  if (d_logits && d_logits == logits && (ld != ldd || logits_dtype != d_logits_dtype))
+    return PQM_ERR_SHAPE;
+  const int64_t parts = (vocab + TB_TURNS * TL_TILE - 1) / (TB_TURNS * TL_TILE);
+  if (tokens * parts >= ((int64_t)1 << 31)) return PQM_ERR_SHAPE;
+  if (tokens == 0) return PQM_OK;
+  if (!logits || !stats || !d_logits || (!d_logprob && !d_entropy) || (d_logprob && !ids) ||
+      (d_entropy && !entropy))
+    return PQM_ERR_NULL;
+  const bool f32 = logits_dtype == PQM_OUT_FP32, o32 = d_logits_dtype == PQM_OUT_FP32;
+  if (!al(logits, f32 ? 4 : 2) || !al(d_logits, o32 ? 4 : 2) || !al(ids, 4) || !al(stats, 4) ||
+      !al(entropy, 4) || !al(d_logprob, 4) || !al(d_entropy, 4))
+    return PQM_ERR_ALIGN;
+  const TlBack a = {logits, ld, ids, vocab, temperature, (float)(1.4426950408889634 / temperature),
+                    stats, entropy, d_logprob, d_entropy, d_logits, ldd, (int)parts};
+  const auto kernel = f32 ? o32 ? k_token_logprobs_backward<true, true>
+                                : k_token_logprobs_backward<true, false>
+                      : o32 ? k_token_logprobs_backward<false, true>
+                            : k_token_logprobs_backward<false, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tokens * parts)), dim3(256), 0, stream, a);
+  return st_of(hipGetLastError());
+}
+
+}  // extern "C"
