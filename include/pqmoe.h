@@ -703,6 +703,51 @@ pqm_status pqm_moe_gemv_swiglu_nvfp4(const uint16_t *x, const int32_t *ids, cons
                                      uint16_t *d, hipStream_t stream);
 
 /*
+ * A whole expert layer for a few tokens (decode), from the residual stream on,
+ * in one call: what pqm_rmsnorm_quantize_mxfp8 (without its encoding), the
+ * router's product, pqm_moe_gate, the two few-row products and pqm_moe_combine
+ * do one after the other.
+ *   h = bf16(x + residual)                       (residual NULL: h = x)
+ *   y = bf16(h rstd norm_w), the nearest bf16 values, rstd as there
+ *   z = y gate_w^T; topk_ids, prob: pqm_moe_gate of z (score, renormalize, scale)
+ *   d[t, j] = bf16(silu(g) u prob[t, j]), (g, u) = y[t] W1_e^T, e = topk_ids[t, j]
+ *   out[t] = bf16(sum_j d[t, j] W2_e^T), summed in binary32
+ * With shared_expert 1 the weights have one expert more, number E, which every
+ * token meets with prob 1 as row j = k; it is not among topk_ids.
+ *   x, residual, h, y, out [tokens, hidden] bf16; norm_w [hidden] in norm_dtype
+ *   (bf16 or binary32); gate_w [E, hidden] bf16; topk_ids int32 and prob
+ *   binary32 [tokens, k]; d [tokens, k + shared_expert, inter] bf16  (device)
+ *   w1_q [G, 2 inter, hidden / 2] (gate rows, then up rows), w1_scale
+ *   [G, 2 inter, hidden / 16], w1_outer [G], w2_q [G, hidden, inter / 2],
+ *   w2_scale [G, hidden, inter / 16], w2_outer [G], G = E + shared_expert, as
+ *   pqm_quantize_nvfp4_per_token makes them with one outer scale per expert
+ * The logits are sums of exact products, in binary64 over partial sums of 32,
+ * so that two close ones keep their order; they are rounded to binary32.  d and
+ * out are sums in binary32 of exact products.  A NaN in a token's row makes that
+ * token's results NaN and no other's.  The last bits of d and out may depend on
+ * how many tokens and which experts a call has, never on the run.
+ * workspace (device, 16-byte aligned, contents irrelevant):
+ * pqm_moe_decode_nvfp4_workspace bytes; calls that may run at the same time
+ * need separate ones.  No output may overlap an input or another output.
+ * Requires tokens <= 64, hidden and inter multiples of 32 in 32 .. 16384,
+ * 1 <= k <= 16, k <= E <= 1024, 2^-100 <= eps < infinity (PQM_ERR_SHAPE);
+ * shared_expert and renormalize 0 or 1 (PQM_ERR_ENUM); bf16 tensors, norm_w,
+ * w1_q and w2_q 16-byte aligned, the others 4-byte (PQM_ERR_ALIGN).
+ */
+pqm_status pqm_moe_decode_nvfp4(const uint16_t *x, const uint16_t *residual, const void *norm_w,
+                                pqm_dtype norm_dtype, float eps, const uint16_t *gate_w,
+                                int64_t tokens, int64_t hidden, int64_t inter, int64_t num_experts,
+                                int64_t k, int shared_expert, pqm_score score, int renormalize,
+                                float scale, const uint8_t *w1_q, const uint8_t *w1_scale,
+                                const float *w1_outer, const uint8_t *w2_q,
+                                const uint8_t *w2_scale, const float *w2_outer, uint16_t *h,
+                                uint16_t *y, int32_t *topk_ids, float *prob, uint16_t *d,
+                                uint16_t *out, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+size_t pqm_moe_decode_nvfp4_workspace(int64_t tokens, int64_t hidden, int64_t inter,
+                                      int64_t num_experts, int64_t k, int shared_expert);
+
+/*
  * Dense products of bf16 operands (a router, an output head, any projection
  * that is not an expert's), with what follows them in the same pass:
  *   z = x W^T + bias,   y = act(z) + residual

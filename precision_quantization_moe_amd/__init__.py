@@ -18,5 +18,5 @@ from ._binding import (  # noqa: F401
     validate_offsets, OFFSETS_FIRST_NOT_ZERO, OFFSETS_DECREASING, OFFSETS_MISALIGNED,
     OFFSETS_PAST_END, LIB_PATH, moe_gate, moe_gate_backward, moe_gemv_nvfp4, moe_gemv_swiglu_nvfp4,
     rmsnorm_backward, rmsnorm_quantize_mxfp8, ACT_GELU, ACT_NONE, ACT_SILU, linear, linear_backward,
-    token_logprobs, token_logprobs_backward,
+    token_logprobs, token_logprobs_backward, moe_decode_nvfp4,
 )

@@ -72,6 +72,9 @@ SIGNATURES = {
     "pqm_linear_backward": ([P, I64, P, I64, P, I32, P, P, I64, I64, I64, I64, P, P, P, P, P, SZ,
                              P], I32),
     "pqm_linear_backward_workspace": ([I64, I64, I64], SZ),
+    "pqm_moe_decode_nvfp4": ([P, P, P, I32, F32, P, I64, I64, I64, I64, I64, I32, I32, I32, F32, P,
+                              P, P, P, P, P, P, P, P, P, P, P, P, SZ, P], I32),
+    "pqm_moe_decode_nvfp4_workspace": ([I64, I64, I64, I64, I64, I32], SZ),
     "pqm_token_logprobs": ([P, I32, I64, P, I64, I64, F32, P, P, P, P, P, I64, P, SZ, P], I32),
     "pqm_token_logprobs_workspace": ([I64, I64, I64], SZ),
     "pqm_token_logprobs_backward": ([P, I32, I64, P, I64, I64, F32, P, P, P, P, P, I32, I64, P],
@@ -430,6 +433,54 @@ def moe_gemv_swiglu_nvfp4(x: torch.Tensor, ids: torch.Tensor, prob: torch.Tensor
     _call("pqm_moe_gemv_swiglu_nvfp4", dev, _ptr(x), _ptr(ids), _ptr(prob), rows, divisor,
           _ptr(w_q), _ptr(w_scale), _ptr(w_outer), rps, G, inter, K, _ptr(d))
     return d
+
+
+def moe_decode_nvfp4(x: torch.Tensor, residual: torch.Tensor | None, norm_w: torch.Tensor,
+                     gate_w: torch.Tensor, w1_q, w1_scale, w1_outer, w2_q, w2_scale, w2_outer,
+                     k: int, inter: int, shared: bool = False, score: int = SCORE_SOFTMAX,
+                     renormalize: bool = True, scale: float = 1.0, eps: float = 1e-6):
+    """A whole expert layer for up to 64 tokens, from the residual stream on; see
+    pqm_moe_decode_nvfp4 in pqmoe.h.  x, residual (may be None) bf16 [T, H],
+    norm_w bf16 or float32 [H], gate_w bf16 [E, H]; weights with one outer scale
+    per expert, as moe_layer.quantize_expert_weights_nvfp4 returns them, of E
+    experts, or of E + 1 with `shared`, whose last one every token meets.
+    Returns (out [T, H], h [T, H], y [T, H] bf16, ids int32 and prob float32
+    [T, k], d bf16 [T * (k + shared), inter])."""
+    _bf16_2d(x)
+    T, H = x.shape
+    E, dev = gate_w.shape[0], x.device
+    sh = 1 if shared else 0
+    G = E + sh
+    if inter < 0 or k < 1:
+        raise PqmError(2, "pqm_moe_decode_nvfp4")
+    _want(x, "x", torch.bfloat16, (T, H), dev)
+    if residual is not None:
+        _want(residual, "residual", torch.bfloat16, (T, H), dev)
+    wdt = _bf16_or_f32(norm_w, "norm_w")
+    _want(norm_w, "norm_w", norm_w.dtype, (H,), dev)
+    _want(gate_w, "gate_w", torch.bfloat16, (E, H), dev)
+    for name, t, dtype, n in (("w1_q", w1_q, torch.uint8, inter * H),
+                              ("w1_scale", w1_scale, torch.uint8, inter * H // 8),
+                              ("w1_outer", w1_outer, torch.float32, 1),
+                              ("w2_q", w2_q, torch.uint8, H * inter // 2),
+                              ("w2_scale", w2_scale, torch.uint8, H * inter // 16),
+                              ("w2_outer", w2_outer, torch.float32, 1)):
+        if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+            raise TypeError(f"{name}: expected a contiguous {dtype} tensor on {dev}")
+        if t.numel() != G * n:
+            raise ValueError(f"{name}: expected {n} values for each of {G} experts, got {t.numel()}")
+    size = lib().pqm_moe_decode_nvfp4_workspace(T, H, inter, E, k, sh)
+    bf16 = dict(dtype=torch.bfloat16, device=dev)
+    out, h, y = torch.empty(T, H, **bf16), torch.empty(T, H, **bf16), torch.empty(T, H, **bf16)
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+    prob = torch.empty(T, k, dtype=torch.float32, device=dev)
+    d = torch.empty(T * (k + sh), inter, **bf16)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    _call("pqm_moe_decode_nvfp4", dev, _ptr(x), _ptr(residual), _ptr(norm_w), wdt, eps,
+          _ptr(gate_w), T, H, inter, E, k, sh, score, int(renormalize), scale, _ptr(w1_q),
+          _ptr(w1_scale), _ptr(w1_outer), _ptr(w2_q), _ptr(w2_scale), _ptr(w2_outer), _ptr(h),
+          _ptr(y), _ptr(ids), _ptr(prob), _ptr(d), _ptr(out), _ptr(ws), size)
+    return out, h, y, ids, prob, d
 
 
 # ---------------------------------------------------------- dense products
