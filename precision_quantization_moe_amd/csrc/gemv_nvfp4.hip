@@ -522,6 +522,16 @@ pqm_status gemv_check(const GemvArgs &a, const int32_t *ids, int64_t rows, int64
 }
 
 }  // namespace
+
+hipError_t launch_gemv_nvfp4(const uint16_t *x, const int32_t *ids, const float *prob, int64_t rows,
+                             int64_t divisor, const uint8_t *w, const uint8_t *w_scale,
+                             const float *w_outer, int64_t w_rows_per_scale, int64_t G, int64_t N,
+                             int64_t K, void *out, bool out_fp32, hipStream_t st) {
+  const GemvArgs a = {x, (int)rows, (int)divisor, w, w_scale, w_outer, w_rows_per_scale,
+                      (int)G, N, K, prob, out, 0};
+  return launch_gemv(a, ids, prob != nullptr, out_fp32, st);
+}
+
 }  // namespace pqm
 
 extern "C" {

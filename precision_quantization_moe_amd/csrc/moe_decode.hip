@@ -9,7 +9,7 @@
 // read once and that few steps wait for one another: a layer of one token takes
 // 21 MB, 4 us of the memory's time.
 //
-// An expert meets a token at most once, so its rows are a 64-bit set of tokens.
+// An expert meets a token at most once, so the rows of one are a set of tokens.
 #include "gate_device.hpp"
 #include "gemv_device.hpp"
 #include "norm_device.hpp"
@@ -22,8 +22,19 @@ namespace pqm {
 namespace {
 
 constexpr int DC_TOKENS = 64, DC_EXPERTS = 1024, DC_K = 16, DC_WIDTH = 16384;
+constexpr int DC_FEW = 16;       // tokens of the one-kernel form: an expert's rows are one tile
+constexpr int DC_WAVES = 16;     // of a workgroup of that form, one workgroup a CU
+constexpr int DC_GRID = 256;
+constexpr int DC_CLASSES = 8;    // tickets and signals, a cache line each
+
 // Tokens of a workgroup of the router, whose rows are 8 KB of LDS each at NC 1.
 constexpr int dr_tokens(int nc) { return 4 / nc; }
+
+struct DcSync {
+  struct {
+    uint32_t ticket, pad0[63], done, pad1[63];
+  } of[DC_CLASSES];
+};
 
 struct DcArgs {
   const uint16_t *x, *res;
@@ -41,10 +52,16 @@ struct DcArgs {
   int32_t *ids;
   float *prob;
   uint16_t *d, *out;
-  float *logits;    // [T][E]
-  float *partial;   // [S][T][H]
-  uint32_t *count;  // [H / 16]
-  int ks, S;        // waves that share a contraction; parts of the experts
+  // workspace
+  float *logits;        // [T][E]
+  uint16_t *y16;        // [T][H] y in scaled binary16
+  float *back;          // [T] what undoes the scale
+  float *partial;       // [S][T][H]
+  uint32_t *count;      // [H / 16]
+  DcSync *sync;
+  int32_t *all_ids;     // [T][c], the shared expert's among them
+  float *all_prob;
+  int ks, S;            // waves that share a contraction; parts of the experts
 };
 
 __device__ __forceinline__ int dc_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -62,13 +79,16 @@ __global__ __launch_bounds__(512) void k_decode_router(DcArgs a) {
   constexpr int DR_TOKENS = dr_tokens(NC);
   extern __shared__ __align__(16) uint8_t lds[];  // y: rows of H values and 16 bytes
   __shared__ double red[8][DR_TOKENS];
+  __shared__ uint32_t top[8][DR_TOKENS];
   __shared__ double sums[8][DR_TOKENS][16];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, ln = lane & 15;
   const int wave = dc_uniform(tid >> 6);
   const int t0 = blockIdx.y * DR_TOKENS, n = min(DR_TOKENS, a.T - t0), e0 = blockIdx.x * 16;
   const int H = a.H, pitch = 2 * H + 16, blocks = (H + 63) / 64;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // for the kernel behind this one
     for (int i = tid; i < H / 16; i += 512) a.count[i] = 0;
+    if (tid < DC_CLASSES) a.sync->of[tid].ticket = a.sync->of[tid].done = 0;
+  }
   const __amdgpu_buffer_rsrc_t wb =
       gv_buffer(a.gate_w + (int64_t)e0 * H, (int64_t)min(16, a.E - e0) * H * 2);
   const auto load = [&](gv_u4 (&w)[8], int i0) {  // four blocks of this wave
@@ -82,6 +102,12 @@ __global__ __launch_bounds__(512) void k_decode_router(DcArgs a) {
   gv_u4 w[8];
   load(w, 0);
 
+  float wf[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * 512 + tid) * 8;
+    if (c < H) load_w8<WF32>(a.norm_w, c, wf[i]);
+  }
   uint32_t v[DR_TOKENS][NC][4];
   double sq[DR_TOKENS] = {};
 #pragma unroll
@@ -122,28 +148,65 @@ __global__ __launch_bounds__(512) void k_decode_router(DcArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) total += red[i][t];
     const double root = inverse_root(total / (double)H + (double)a.eps);
+    uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (i * 512 + tid) * 8;
       if (c >= H) continue;
-      float wf[8];
-      load_w8<WF32>(a.norm_w, c, wf);
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // binary64 throughout: y is the nearest bf16 value
         o[j] = pk_bf16_rne(
-            before_bf16((double)bf16_lo_f32(v[t][i][j]) * (double)wf[2 * j] * root),
-            before_bf16((double)bf16_hi_f32(v[t][i][j]) * (double)wf[2 * j + 1] * root));
+            before_bf16((double)bf16_lo_f32(v[t][i][j]) * (double)wf[i][2 * j] * root),
+            before_bf16((double)bf16_hi_f32(v[t][i][j]) * (double)wf[i][2 * j + 1] * root));
       *reinterpret_cast<uint4 *>(lds + t * pitch + 2 * c) = make_uint4(o[0], o[1], o[2], o[3]);
       if (blockIdx.x == 0) {
         const int64_t at = (int64_t)(t0 + t) * H + c;
         *reinterpret_cast<uint4 *>(a.h + at) =
             make_uint4(v[t][i][0], v[t][i][1], v[t][i][2], v[t][i][3]);
         *reinterpret_cast<uint4 *>(a.y + at) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[t][i][j] = o[j];
+          most = pk_max_u16(most, o[j] & 0x7FFF7FFFu);
+        }
       }
+    }
+    if (blockIdx.x == 0) {
+      most = max(most & 0xFFFFu, most >> 16);
+      most = group_max<64>(most);
+      if (lane == 0) top[wave][t] = most;
     }
   }
   __syncthreads();
+  // y again in binary16, under the power of two that brings the row's largest value
+  // to 2^14 .. 2^15: bf16 has 8 significant bits, so values down to 2^-31 of the
+  // largest stay exact, and weights in binary16 take half the instructions of bf16.
+  if (blockIdx.x == 0 && a.y16) {
+#pragma unroll
+    for (int t = 0; t < DR_TOKENS; ++t) {
+      if (t >= n) break;
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = max(most, top[i][t]);
+      const int ex = min(127, 14 + 127 - (int)(most >> 7));
+      const float up = __builtin_ldexpf(1.0f, ex);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = (i * 512 + tid) * 8;
+        if (c >= H) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo_f32(v[t][i][j]) * up,
+                                                   bf16_hi_f32(v[t][i][j]) * up));
+        *reinterpret_cast<uint4 *>(a.y16 + (int64_t)(t0 + t) * H + c) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (tid == 0) a.back[t0 + t] = __builtin_ldexpf(1.0f, -ex);
+    }
+  }
 
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   for (int i0 = 0; wave + 8 * i0 < blocks; i0 += 4) {
@@ -176,10 +239,10 @@ __global__ __launch_bounds__(512) void k_decode_router(DcArgs a) {
 
 namespace {
 
-// The gate of token t by one wave, expert 64 i + lane in register i: the choice,
-// the scores and the renormalisation of pqm_moe_gate.
+// A token's gate by one wave, expert 64 i + lane in register i: the choice, the
+// scores and the renormalisation of pqm_moe_gate, to the token's k ids and probs.
 template <int VPL>
-__device__ __forceinline__ void dc_gate(const DcArgs &a, const float (&z)[VPL], int t, int32_t *ids,
+__device__ __forceinline__ void dc_gate(const DcArgs &a, const float (&z)[VPL], int32_t *ids,
                                         float *prob) {
   const int l = threadIdx.x & 63;
   float v[VPL];
@@ -232,88 +295,82 @@ __device__ __forceinline__ void dc_gate(const DcArgs &a, const float (&z)[VPL], 
   }
   if (!a.softmax && top != top) w = top;
   if (l < a.k) {
-    ids[t * a.k + l] = my_id;
-    prob[t * a.k + l] = w * a.scale;
+    ids[l] = my_id;
+    prob[l] = w * a.scale;
   }
 }
 
-// Every token's gate, one wave a token, the next one's logits ahead.
+// The same from the logits; past the last token nothing.
 template <int VPL>
-__device__ __forceinline__ void dc_gates(const DcArgs &a, int32_t *ids, float *prob) {
-  const int l = threadIdx.x & 63, wave = dc_uniform(threadIdx.x >> 6);
+__device__ __forceinline__ void dc_gate_of(const DcArgs &a, int t, int32_t *ids, float *prob) {
+  const int l = threadIdx.x & 63;
+  if (t >= a.T) return;
   const __amdgpu_buffer_rsrc_t zb = gv_buffer(a.logits, (int64_t)a.T * a.E * 4);
-  const auto load = [&](float (&z)[VPL], int t) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      z[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          zb, (int)(64 * i + l < a.E ? (uint32_t)(t * a.E + 64 * i + l) * 4 : GV_NONE), 0, 0));
-  };
   float z[VPL];
-  load(z, wave);  // past the last token: zeros
-  for (int t = wave; t < a.T; t += 8) {
-    float next[VPL];
-    load(next, t + 8);
-    dc_gate<VPL>(a, z, t, ids, prob);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) z[i] = next[i];
-  }
+  for (int i = 0; i < VPL; ++i)
+    z[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        zb, (int)(64 * i + l < a.E ? (uint32_t)(t * a.E + 64 * i + l) * 4 : GV_NONE), 0, 0));
+  dc_gate<VPL>(a, z, ids, prob);
 }
 
-// Which experts are met, and by which tokens.
+// Which tokens meet an expert, and as which of their choices.
 struct DcSets {
-  uint64_t rows[DC_EXPERTS + 1];
-  uint16_t met[DC_EXPERTS + 1];
-  int32_t ids[DC_TOKENS * DC_K];
-  int count[8];
+  uint32_t rows[DC_EXPERTS];
+  uint8_t slot[DC_FEW][DC_EXPERTS];
 };
 
-// Fills s.rows and s.met from s.ids; the number of experts met.  All threads call
-// it, after a barrier behind the ids.
-__device__ __forceinline__ int dc_sets(const DcArgs &a, DcSets &s) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int groups = a.E + (a.c - a.k);
-  for (int e = tid; e < groups; e += 512)
-    s.rows[e] = e < a.E ? 0 : a.T == 64 ? ~0ull : (1ull << a.T) - 1;
-  __syncthreads();
-  for (int i = tid; i < a.T * a.k; i += 512)
-    atomicOr(reinterpret_cast<unsigned long long *>(&s.rows[s.ids[i]]), 1ull << (i / a.k));
-  __syncthreads();
-  int n = 0;
-  for (int e0 = 0; e0 < groups; e0 += 512) {
-    const int e = e0 + tid;
-    const uint64_t b = __ballot(e < groups && s.rows[e] != 0);
-    if (lane == 0) s.count[wave] = __popcll(b);
-    __syncthreads();
-    int at = n + __popcll(b & ((1ull << lane) - 1));
+// The experts met, in order, the shared one last: every wave keeps them as sets of
+// 64 in scalar registers, which takes no barrier and no list.
+template <int VPL>
+struct DcMet {
+  uint64_t in[VPL];
+  int n;
+
+  __device__ __forceinline__ DcMet(const DcArgs &a, const DcSets &s) {
+    const int lane = threadIdx.x & 63;
+    n = a.c - a.k;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      if (w < wave) at += s.count[w];
-      n += s.count[w];
+    for (int i = 0; i < VPL; ++i) {
+      const int e = 64 * i + lane;
+      in[i] = __ballot(e < a.E && s.rows[e] != 0);
+      n += __popcll(in[i]);
     }
-    if (b >> lane & 1) s.met[at] = (uint16_t)e;
-    __syncthreads();
   }
-  return dc_uniform(n);
+  // The i-th.
+  __device__ __forceinline__ int operator()(const DcArgs &a, int i) const {
+    const int lane = threadIdx.x & 63;
+    int e = a.E;
+#pragma unroll
+    for (int w = 0; w < VPL; ++w) {
+      const int here = __popcll(in[w]);
+      if (i >= 0 && i < here) {
+        const uint64_t at = __ballot((in[w] >> lane & 1) &&
+                                     __popcll(in[w] & ((1ull << lane) - 1)) == i);
+        e = 64 * w + __ffsll((unsigned long long)at) - 1;
+      }
+      i -= here;
+    }
+    return dc_uniform(e);
+  }
+};
+
+__device__ __forceinline__ uint32_t dc_rows(const DcArgs &a, const DcSets &s, int e) {
+  return e == a.E ? (1u << a.T) - 1 : (uint32_t)dc_uniform((int)s.rows[e]);
 }
 
-// Lane r gets the token of row r of a set (its r-th member; behind the members
-// come the others).
-__device__ __forceinline__ int dc_members(uint64_t rows) {
-  const int lane = threadIdx.x & 63, c = __popcll(rows);
-  const int before = __popcll(rows & ((1ull << lane) - 1));
-  const int at = rows >> lane & 1 ? before : c + lane - before;
-  return __builtin_amdgcn_ds_permute(4 * at, lane);
-}
-
-__device__ __forceinline__ uint64_t dc_uniform64(uint64_t v) {
-  return (uint64_t)(uint32_t)dc_uniform((int)(v >> 32)) << 32 | (uint32_t)dc_uniform((int)v);
+// The token of row l % 16 of a set of up to 16 (its members in order).
+__device__ __forceinline__ int dc_member(uint32_t rows) {
+  const int lane = threadIdx.x & 63, c = __popc(rows);
+  const int before = __popc(rows & ((1u << (lane & 31)) - 1));
+  const int at = rows >> (lane & 31) & 1 ? before : c + (lane & 31) - before;
+  const int members = __builtin_amdgcn_ds_permute(4 * (at + (lane & 32)), lane & 31);
+  return __builtin_amdgcn_ds_bpermute(4 * (lane & 15), members);
 }
 
 // Which of its token's rows an expert's row is.
 __device__ __forceinline__ int dc_slot(const DcArgs &a, const DcSets &s, int t, int e) {
-  int j = a.k;  // the shared expert's
-  for (int i = 0; i < a.k; ++i) j = s.ids[t * a.k + i] == e ? i : j;
-  return j;
+  return e == a.E ? a.k : s.slot[t & (DC_FEW - 1)][e];
 }
 
 // A 16-row weight tile's part of a 256-wide chunk: eight rows a load, eight lanes
@@ -339,276 +396,384 @@ __device__ __forceinline__ void dc_load(DcChunk &b, __amdgpu_buffer_rsrc_t wq,
           (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ws, vs + 2, 0, 0) << 16;
 }
 
-// A chunk of N weight tiles times MT tiles of 16 rows, whose values start at xo
-// (GV_NONE: no row) of xb.  Few of the rows' values are held at a time: 8 tiles'
-// worth of registers.
-template <int MT, int N>
-__device__ __forceinline__ void dc_multiply(gv_f4 (&acc)[N][MT], const DcChunk (&b)[N],
-                                            __amdgpu_buffer_rsrc_t xb, const uint32_t (&xo)[MT],
+// What a chunk's product takes of 16 rows, whose values start at xo (GV_NONE: no
+// row) of xb: lane group g has the chunk's values 64 g .. + 63.  No branch: the
+// loads have to stay in their order, or the waits for them would wait for the next
+// chunk's weights too.  FRESH: written by other workgroups of this kernel.
+template <bool FRESH>
+__device__ __forceinline__ void dc_load_x(gv_u4 (&x)[8], __amdgpu_buffer_rsrc_t xb, uint32_t xo,
+                                          int K, int ch) {
+  const uint32_t kk = 256 * ch + 64 * ((threadIdx.x & 63) >> 4);
+  const uint32_t lo = (xo + 2 * kk) | (kk < (uint32_t)K ? 0 : GV_NONE);
+  const uint32_t hi = (xo + 2 * kk) | (kk + 32 < (uint32_t)K ? 0 : GV_NONE);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    x[j] = __builtin_amdgcn_raw_buffer_load_b128(xb, (int)(j < 4 ? lo : hi), 16 * j,
+                                                 FRESH ? 16 : 0);
+}
+
+// Eight weights in binary16: exact, and half the instructions of bf16.
+__device__ __forceinline__ gv_h8 dc_decode16(uint32_t u, _Float16 f) {
+  const gv_h2 s = {f, f};
+  const gv_h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.0f, 0) * s;
+  const gv_h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.0f, 1) * s;
+  const gv_h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.0f, 2) * s;
+  const gv_h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.0f, 3) * s;
+  return gv_h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A chunk of a weight tile times 16 rows, in binary16 or bf16.
+template <bool HALF>
+__device__ __forceinline__ void dc_multiply(gv_f4 &acc, const DcChunk &b, const gv_u4 (&x)[8],
                                             const GvTurn &turn, int K, int ch) {
-  constexpr int JB = 8 / MT;
   const int lane = threadIdx.x & 63, g = lane >> 4, ln = lane & 15;
+  gv_u4 q[2];
+  turn(b.q, q);
+  int sw = __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)b.s);
   // past the row's end stand the next row's scales, maybe NaN: x is 0 there, the
   // scale has to be so too
   const int left = K - 256 * ch - 64 * g;
-  gv_u4 x[JB][MT];
-  const auto load_x = [&](int j0) {
+  if (left < 64) sw = left == 32 ? sw & 0xFFFF : 0;
+  if constexpr (HALF) {
+    const gv_h2 f[2] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, false),
+                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, true)};
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int j = 0; j < 8; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          dc_decode16(q[j >> 2][j & 3], f[j >> 2][(j >> 1) & 1]),
+          __builtin_bit_cast(gv_h8, x[j]), acc, 0, 0, 0);
+  } else {
+    const float f[4] = {__builtin_amdgcn_cvt_f32_fp8(sw, 0), __builtin_amdgcn_cvt_f32_fp8(sw, 1),
+                        __builtin_amdgcn_cvt_f32_fp8(sw, 2), __builtin_amdgcn_cvt_f32_fp8(sw, 3)};
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        x[j][m] = __builtin_amdgcn_raw_buffer_load_b128(
-            xb,
-            (int)(8 * (j0 + j) < left && xo[m] != GV_NONE
-                      ? xo[m] + 2 * (256 * ch + 64 * g + 8 * (j0 + j))
-                      : GV_NONE),
-            0, 0);
-  };
-  load_x(0);
-  gv_u4 q[N][2];
-  float f[N][4];
-#pragma unroll
-  for (int t = 0; t < N; ++t) {
-    turn(b[t].q, q[t]);
-    int sw = __builtin_amdgcn_ds_bpermute(16 * ln + 4 * g, (int)b[t].s);
-    if (left < 64) sw = left == 32 ? sw & 0xFFFF : 0;
-    f[t][0] = __builtin_amdgcn_cvt_f32_fp8(sw, 0);
-    f[t][1] = __builtin_amdgcn_cvt_f32_fp8(sw, 1);
-    f[t][2] = __builtin_amdgcn_cvt_f32_fp8(sw, 2);
-    f[t][3] = __builtin_amdgcn_cvt_f32_fp8(sw, 3);
-  }
-#pragma unroll
-  for (int j0 = 0; j0 < 8; j0 += JB) {
-    if (j0) load_x(j0);
-#pragma unroll
-    for (int j = 0; j < JB; ++j)
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        const gv_bf8 w = gv_decode(q[t][(j0 + j) >> 2][(j0 + j) & 3], f[t][(j0 + j) >> 1]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              w, __builtin_bit_cast(gv_bf8, x[j][m]), acc[t][m], 0, 0, 0);
-      }
+    for (int j = 0; j < 8; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gv_decode(q[j >> 2][j & 3], f[j >> 1]),
+                                                    __builtin_bit_cast(gv_bf8, x[j]), acc, 0, 0, 0);
   }
 }
 
-// One expert's 16 columns of d, its rows m0 .. m0 + 16 MT - 1: ks waves share the
-// contraction.
-template <int MT, bool WORDS>
-__device__ __forceinline__ void dc_up(const DcArgs &a, const DcSets &s, const float *prob, int e,
-                                      uint64_t rows, int m0, int tile, const GvTurn &turn,
-                                      gv_f4 (*red)[2][64]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, ln = lane & 15;
-  const int wave = dc_uniform(threadIdx.x >> 6), kw = wave & (a.ks - 1);
-  const int K = a.H, chunks = (K + 255) / 256, c = __popcll(rows);
-  const bool live = 16 * tile < a.I;  // otherwise a wave past the last tile
-  const int64_t r0 = (int64_t)e * 2 * a.I + (live ? 16 * tile : 0), r1 = r0 + a.I;
-  const int n = live ? 16 : 0;
-  const __amdgpu_buffer_rsrc_t gq = gv_buffer(a.w1 + r0 * (K / 2), (int64_t)n * (K / 2)),
-                               gs = gv_buffer(a.s1 + r0 * (K / 16), (int64_t)n * (K / 16)),
-                               uq = gv_buffer(a.w1 + r1 * (K / 2), (int64_t)n * (K / 2)),
-                               us = gv_buffer(a.s1 + r1 * (K / 16), (int64_t)n * (K / 16)),
-                               xb = gv_buffer(a.y, (int64_t)a.T * K * 2);
-  const int token = dc_members(rows);
-  uint32_t xo[MT];
-  int tok[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    tok[m] = __builtin_amdgcn_ds_bpermute(4 * (m0 + 16 * m + ln), token);
-    xo[m] = m0 + 16 * m + ln < c ? (uint32_t)tok[m] * K * 2 : GV_NONE;
+// The next ticket of a class (one lane).
+__device__ __forceinline__ uint32_t dc_draw(DcSync *sync, int cls) {
+  return __hip_atomic_fetch_add(&sync->of[cls].ticket, 1u, __ATOMIC_RELAXED,
+                                __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int dc_drawn(uint32_t ticket, int cls, int total) {
+  return ticket < (uint32_t)((total - cls + DC_CLASSES - 1) / DC_CLASSES)
+             ? cls + DC_CLASSES * (int)ticket
+             : -1;
+}
+
+// With its own class at an end, a workgroup looks at all of them at once (the first
+// wave) and draws where there are any left.  -1: every item is drawn, each by a
+// workgroup that runs.
+__device__ __forceinline__ int dc_sweep(DcSync *sync, int total) {
+  const int lane = threadIdx.x & 63, cls = lane % DC_CLASSES;
+  int got = -1;
+  uint32_t v = lane < DC_CLASSES ? __hip_atomic_load(&sync->of[cls].ticket, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT)
+                                 : 0xFFFFFFFFu;
+  uint64_t open = __ballot(dc_drawn(v, cls, total) >= 0);
+  while (got < 0 && open) {  // each turn draws or closes a class
+    const int who = __ffsll((unsigned long long)open) - 1;
+    if (lane == who) v = dc_draw(sync, cls);
+    got = __builtin_amdgcn_readlane(dc_drawn(v, cls, total), who);
+    open &= ~(1ull << who);
   }
-  gv_f4 acc[2][MT] = {};
-  DcChunk b[2];
-  const auto load = [&](int ch) {
-    dc_load<WORDS>(b[0], gq, gs, K, ch, ch < chunks);
-    dc_load<WORDS>(b[1], uq, us, K, ch, ch < chunks);
-  };
-  load(kw);
-  for (int ch = kw; ch < chunks; ch += a.ks) {
-    const DcChunk cur[2] = {b[0], b[1]};
-    load(ch + a.ks);
-    dc_multiply<MT, 2>(acc, cur, xb, xo, turn, K, ch);
+  return got;
+}
+
+}  // namespace
+
+// Gate, gate_up, down projection and sum in one kernel, one workgroup a CU.
+//
+// gate_up's items (an expert, 16 / ks tiles of 16 columns; ks waves share a tile's
+// contraction) are drawn by ticket, so whoever waits for the last of them waits for
+// workgroups that run and wait for nothing themselves: the wait ends however many
+// workgroups the card holds at once, also beside other calls.  Eight counters, since
+// one address takes 10 ns a draw: 256 workgroups draw in 2.8 us from one and in 1.1
+// from eight, and meet in 3.8 and 1.4.  d goes past the L2 (each XCD has its own),
+// and what is read of it too.
+//
+// The down projection's items are 16 columns and a part of the experts met; its waves
+// take (expert, chunk) in turn, each with sums of its own, the first chunk's weights
+// asked for before the wait.  The workgroup that finishes a column's last part adds
+// the parts in their order.
+template <int VPL, bool WORDS1, bool WORDS2>
+__global__ __launch_bounds__(64 * DC_WAVES, 4) void k_decode_experts(DcArgs a) {
+  __shared__ DcSets s;
+  __shared__ int32_t ids[DC_FEW * DC_K];
+  __shared__ float prob[DC_FEW * DC_K];
+  __shared__ __align__(16) uint8_t turns[DC_WAVES][2048];
+  __shared__ gv_f4 red[2][DC_WAVES][2][64];
+  __shared__ int drawn[2], last;
+  float(*const sums)[DC_FEW * 16] = reinterpret_cast<float(*)[DC_FEW * 16]>(red);
+  static_assert(sizeof(red) >= 4 * DC_WAVES * DC_FEW * 16, "the down projection's sums");
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, ln = lane & 15;
+  const int wave = dc_uniform(tid >> 6);
+  const GvTurn turn(turns[wave], lane);
+
+  uint32_t ticket = 0;
+  const int cls = blockIdx.x % DC_CLASSES;
+  if (tid == 0) ticket = dc_draw(a.sync, cls);
+  for (int e = tid; e < a.E; e += 64 * DC_WAVES) s.rows[e] = 0;
+  __syncthreads();
+  for (int t = wave; t < a.T; t += DC_WAVES) {
+    dc_gate_of<VPL>(a, t, ids + t * a.k, prob + t * a.k);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (lane < a.k) {
+      const int e = ids[t * a.k + lane];
+      atomicOr(&s.rows[e], 1u << t);
+      s.slot[t][e] = (uint8_t)lane;
+      if (blockIdx.x == 0) {
+        a.ids[t * a.k + lane] = e;
+        a.prob[t * a.k + lane] = prob[t * a.k + lane];
+      }
+    }
   }
-  const float outer = a.g1[e];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    gv_f4 vg = acc[0][m], vu = acc[1][m];
-    if (a.ks > 1) {
-      red[wave][0][lane] = vg;
-      red[wave][1][lane] = vu;
+  __syncthreads();
+  const DcMet<VPL> met(a, s);
+
+  const int per = DC_WAVES / a.ks, kw = wave & (a.ks - 1), tiles = a.I / 16;
+  const int tg = (tiles + per - 1) / per, total = met.n * tg;
+  int finished = 0;
+  {
+    const int K = a.H, chunks = (K + 255) / 256;
+    const __amdgpu_buffer_rsrc_t xb = gv_buffer(a.y16, (int64_t)a.T * K * 2);
+    if (tid == 0) drawn[1] = dc_drawn(ticket, cls, total);
+    __syncthreads();
+    int item = dc_uniform(drawn[1]), buf = 0;
+    for (;;) {
+      if (item < 0) {
+        // Its class is at an end: every wave's part of d has to arrive before the
+        // workgroup says so, and what is left of other classes is taken.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0 && finished)
+          __hip_atomic_fetch_add(&a.sync->of[cls].done, (uint32_t)finished, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+        finished = 0;
+        if (wave == 0) {
+          const int t = dc_sweep(a.sync, total);
+          if (lane == 0) drawn[buf ^ 1] = t;
+        }
+        __syncthreads();
+        item = dc_uniform(drawn[buf ^ 1]);
+        if (item < 0) break;
+      }
+      const int i = item / tg, tile = (item - i * tg) * per + wave / a.ks;
+      const int e = met(a, i);
+      const uint32_t rows = dc_rows(a, s, e);
+      const bool live = tile < tiles;
+      const int64_t r0 = (int64_t)e * 2 * a.I + (live ? 16 * tile : 0), r1 = r0 + a.I;
+      const int64_t n = live ? 16 : 0;
+      const __amdgpu_buffer_rsrc_t gq = gv_buffer(a.w1 + r0 * (K / 2), n * (K / 2)),
+                                   gs = gv_buffer(a.s1 + r0 * (K / 16), n * (K / 16)),
+                                   uq = gv_buffer(a.w1 + r1 * (K / 2), n * (K / 2)),
+                                   us = gv_buffer(a.s1 + r1 * (K / 16), n * (K / 16));
+      const auto load = [&](DcChunk (&b)[2], int ch) {
+        dc_load<WORDS1>(b[0], gq, gs, K, ch, ch < chunks);
+        dc_load<WORDS1>(b[1], uq, us, K, ch, ch < chunks);
+      };
+      DcChunk b0[2], b1[2];
+      load(b0, kw);
+      const int tok = dc_member(rows);
+      const bool row = ln < __popc(rows);
+      const uint32_t xo = row ? (uint32_t)tok * K * 2 : GV_NONE;
+      gv_f4 acc[2] = {};
+      // The next chunk's weights go out behind this one's rows, so that the wait for
+      // the rows leaves them in flight; two sets of registers, since a copy would wait.
+      const auto turn_of = [&](const DcChunk (&b)[2], DcChunk (&next)[2], int ch) {
+        gv_u4 x[8];
+        dc_load_x<false>(x, xb, xo, K, ch);
+        __builtin_amdgcn_sched_barrier(0);
+        if (ch == kw && tid == 0) ticket = dc_draw(a.sync, cls);  // the next item's
+        load(next, ch + a.ks);
+        __builtin_amdgcn_sched_barrier(0);
+        dc_multiply<true>(acc[0], b[0], x, turn, K, ch);
+        dc_multiply<true>(acc[1], b[1], x, turn, K, ch);
+      };
+      for (int ch = kw; ch < chunks; ch += 2 * a.ks) {
+        turn_of(b0, b1, ch);
+        if (ch + a.ks >= chunks) break;
+        turn_of(b1, b0, ch + a.ks);
+      }
+      red[buf][wave][0][lane] = acc[0];
+      red[buf][wave][1][lane] = acc[1];
+      if (tid == 0) drawn[buf] = dc_drawn(ticket, cls, total);
+      // tile t of the item is wave t's to finish
+      const int mine = (item - i * tg) * per + wave;
+      const bool ends = wave < per && mine < tiles && row;
+      float outer = 0.0f, back = 0.0f, p = 1.0f;
+      int j = 0;
+      if (ends) {
+        outer = a.g1[e];
+        back = a.back[tok];
+        j = dc_slot(a, s, tok, e);
+        if (j < a.k) p = prob[tok * a.k + j];
+      }
       __syncthreads();
-      if (kw == 0) {
-        for (int i = 1; i < a.ks; ++i) {
-          vg += red[wave + i][0][lane];
-          vu += red[wave + i][1][lane];
+      const int next = dc_uniform(drawn[buf]);
+      if (ends) {
+        gv_f4 vg = red[buf][wave * a.ks][0][lane], vu = red[buf][wave * a.ks][1][lane];
+        for (int q = 1; q < a.ks; ++q) {
+          vg += red[buf][wave * a.ks + q][0][lane];
+          vu += red[buf][wave * a.ks + q][1][lane];
+        }
+        float o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = swiglu_f32(vg[q] * back * outer, vu[q] * back * outer, p);
+        __hip_atomic_store(
+            reinterpret_cast<uint64_t *>(a.d + (int64_t)(tok * a.c + j) * a.I + 16 * mine + 4 * g),
+            (uint64_t)pk_bf16_rne(o[2], o[3]) << 32 | pk_bf16_rne(o[0], o[1]), __ATOMIC_RELAXED,
+            __HIP_MEMORY_SCOPE_AGENT);
+      }
+      ++finished;
+      item = next;
+      buf ^= 1;
+    }
+  }
+
+  const int K = a.I, chunks = (K + 255) / 256, NT = a.H / 16;
+  const __amdgpu_buffer_rsrc_t xb = gv_buffer(a.d, (int64_t)a.T * a.c * K * 2);
+  bool waited = false;
+  for (int item = blockIdx.x; item < NT * a.S; item += gridDim.x) {
+    const int part = item / NT, tile = item - part * NT;
+    const int i0 = met.n * part / a.S, i1 = met.n * (part + 1) / a.S, units = (i1 - i0) * chunks;
+    // a chunk of an expert: its weights, and where the rows' values start
+    struct Unit {
+      DcChunk b;
+      float outer;
+      uint32_t xo;
+      int tok, ch;
+    };
+    const auto load = [&](Unit &t, int u) {
+      const bool in = u < units;
+      const int i = u / chunks, e = in ? met(a, i0 + i) : 0;
+      t.ch = u - i * chunks;
+      const int64_t r0 = (int64_t)e * a.H + 16 * tile;
+      dc_load<WORDS2>(t.b, gv_buffer(a.w2 + r0 * (K / 2), 8 * (int64_t)K),
+                      gv_buffer(a.s2 + r0 * (K / 16), (int64_t)K), K, t.ch, in);
+      t.outer = a.g2[e];
+      const uint32_t rows = dc_rows(a, s, e);
+      const int tok = dc_member(rows);
+      const uint32_t at = (uint32_t)(tok * a.c + dc_slot(a, s, tok, e)) * K * 2;
+      t.xo = ln < __popc(rows) ? at : GV_NONE;
+      t.tok = tok;
+    };
+    Unit u0, u1;
+    load(u0, wave);
+    for (int i = lane; i < a.T * 4; i += 64)
+      reinterpret_cast<gv_f4 *>(sums[wave])[i] = gv_f4{0, 0, 0, 0};
+    if (!waited) {
+      if (wave == 0) {
+        for (;;) {
+          const uint32_t v = lane < DC_CLASSES
+                                 ? __hip_atomic_load(&a.sync->of[lane].done, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT)
+                                 : 0;
+          int n = 0;
+#pragma unroll
+          for (int q = 0; q < DC_CLASSES; ++q) n += __builtin_amdgcn_readlane((int)v, q);
+          if (n == total) break;
+          __builtin_amdgcn_s_sleep(4);
         }
       }
       __syncthreads();
+      waited = true;
     }
-    if (kw == 0 && live && xo[m] != GV_NONE) {
-      const int t = tok[m], j = dc_slot(a, s, t, e);
-      const float p = j < a.k ? prob[t * a.k + j] : 1.0f;
-      float o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = swiglu_f32(vg[i] * outer, vu[i] * outer, p);
-      *reinterpret_cast<uint2 *>(a.d + (int64_t)(t * a.c + j) * a.I + 16 * tile + 4 * g) =
-          make_uint2(pk_bf16_rne(o[0], o[1]), pk_bf16_rne(o[2], o[3]));
-    }
-  }
-}
-
-}  // namespace
-
-// Gate and gate_up.
-template <int MAXMT, int VPL, bool WORDS>
-__global__ __launch_bounds__(512, 4) void k_decode_up(DcArgs a) {
-  __shared__ DcSets s;
-  __shared__ float prob[DC_TOKENS * DC_K];
-  __shared__ __align__(16) uint8_t turns[8][2048];
-  __shared__ gv_f4 red[8][2][64];
-  dc_gates<VPL>(a, s.ids, prob);
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.T * a.k; i += 512) {
-      a.ids[i] = s.ids[i];
-      a.prob[i] = prob[i];
-    }
-  const int D = dc_sets(a, s);
-  const int wave = dc_uniform(threadIdx.x >> 6), per = 8 / a.ks;
-  const int tg = (a.I / 16 + per - 1) / per;
-  const GvTurn turn(turns[wave], threadIdx.x & 63);
-  for (int item = blockIdx.x; item < D * tg; item += gridDim.x) {
-    const int i = item / tg, tile = (item - i * tg) * per + wave / a.ks;
-    const int e = dc_uniform(s.met[i]);
-    const uint64_t rows = dc_uniform64(s.rows[e]);
-    const int c = __popcll(rows);
-    // more than 32 rows of an expert read its weights again
-    for (int m0 = 0; m0 < c; m0 += 32) {
-      if (MAXMT == 1 || c - m0 <= 16) dc_up<1, WORDS>(a, s, prob, e, rows, m0, tile, turn, red);
-      else dc_up<MAXMT, WORDS>(a, s, prob, e, rows, m0, tile, turn, red);
-    }
-  }
-}
-
-namespace {
-
-// One chunk of one expert's part of 16 output columns, its rows m0 .., added to the
-// wave's sums.
-template <int MT>
-__device__ __forceinline__ void dc_down(const DcArgs &a, const DcSets &s, int e, uint64_t rows,
-                                        int m0, const DcChunk &b, float outer, const GvTurn &turn, int ch,
-                                        float *sums) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, ln = lane & 15;
-  const int K = a.I, c = __popcll(rows);
-  const __amdgpu_buffer_rsrc_t xb = gv_buffer(a.d, (int64_t)a.T * a.c * K * 2);
-  const int token = dc_members(rows);
-  uint32_t xo[MT];
-  int tok[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    tok[m] = __builtin_amdgcn_ds_bpermute(4 * (m0 + 16 * m + ln), token);
-    xo[m] = GV_NONE;
-    if (m0 + 16 * m + ln < c) xo[m] = (uint32_t)(tok[m] * a.c + dc_slot(a, s, tok[m], e)) * K * 2;
-  }
-  gv_f4 acc[1][MT] = {};
-  const DcChunk one[1] = {b};
-  dc_multiply<MT, 1>(acc, one, xb, xo, turn, K, ch);
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    if (xo[m] != GV_NONE) {
-      gv_f4 *p = reinterpret_cast<gv_f4 *>(sums + tok[m] * 16 + 4 * g);
-      *p += acc[0][m] * outer;
-    }
-}
-
-}  // namespace
-
-// Down projection and sum: a workgroup takes 16 output columns and a part of the
-// experts met; its waves take their chunks in turn, each with sums of its own.
-// The workgroup that finishes a column's last part adds the parts in their order.
-template <int MAXMT, bool WORDS>
-__global__ __launch_bounds__(512, 4) void k_decode_down(DcArgs a) {
-  extern __shared__ __align__(16) float sums[];  // [8][T][16]
-  __shared__ DcSets s;
-  __shared__ __align__(16) uint8_t turns[8][2048];
-  __shared__ int last;
-  const int tid = threadIdx.x, wave = dc_uniform(tid >> 6);
-  for (int i = tid; i < a.T * a.k; i += 512) s.ids[i] = a.ids[i];
-  __syncthreads();
-  const int D = dc_sets(a, s);
-  const int K = a.I, chunks = (K + 255) / 256, NT = a.H / 16;
-  const GvTurn turn(turns[wave], tid & 63);
-  float *mine = sums + wave * a.T * 16;
-  for (int item = blockIdx.x; item < NT * a.S; item += gridDim.x) {
-    const int part = item / NT, tile = item - part * NT;
-    const int i0 = D * part / a.S, i1 = D * (part + 1) / a.S, units = (i1 - i0) * chunks;
-    for (int i = tid & 63; i < a.T * 4; i += 64)
-      reinterpret_cast<gv_f4 *>(mine)[i] = gv_f4{0, 0, 0, 0};
-    const auto load = [&](DcChunk &b, float &outer, int u) {
-      const bool in = u < units;
-      const int e = in ? dc_uniform(s.met[i0 + u / chunks]) : 0;
-      const int64_t r0 = (int64_t)e * a.H + 16 * tile;
-      dc_load<WORDS>(b, gv_buffer(a.w2 + r0 * (K / 2), 8 * (int64_t)K),
-                     gv_buffer(a.s2 + r0 * (K / 16), (int64_t)K), K, u % chunks, in);
-      outer = a.g2[e];
+    const auto turn_of = [&](const Unit &t, Unit &next, int u) {
+      gv_u4 x[8];
+      dc_load_x<true>(x, xb, t.xo, K, t.ch);
+      __builtin_amdgcn_sched_barrier(0);
+      load(next, u + DC_WAVES);
+      __builtin_amdgcn_sched_barrier(0);
+      gv_f4 acc = {0, 0, 0, 0};
+      dc_multiply<false>(acc, t.b, x, turn, K, t.ch);
+      if (t.xo != GV_NONE) *reinterpret_cast<gv_f4 *>(sums[wave] + t.tok * 16 + 4 * g) += acc * t.outer;
     };
-    DcChunk b;
-    float outer;
-    load(b, outer, wave);
-    for (int u = wave; u < units; u += 8) {
-      const DcChunk cur = b;
-      const float o = outer;
-      load(b, outer, u + 8);
-      const int e = dc_uniform(s.met[i0 + u / chunks]);
-      const uint64_t rows = dc_uniform64(s.rows[e]);
-      const int c = __popcll(rows);
-      for (int m0 = 0; m0 < c; m0 += 32) {
-        if (MAXMT == 1 || c - m0 <= 16) dc_down<1>(a, s, e, rows, m0, cur, o, turn, u % chunks, mine);
-        else dc_down<MAXMT>(a, s, e, rows, m0, cur, o, turn, u % chunks, mine);
-      }
+    for (int u = wave; u < units; u += 2 * DC_WAVES) {
+      turn_of(u0, u1, u);
+      if (u + DC_WAVES >= units) break;
+      turn_of(u1, u0, u + DC_WAVES);
     }
     __syncthreads();
-    for (int i = tid; i < a.T * 8; i += 512) {
-      const int t = i >> 3, c = 2 * (i & 7);
-      float v0 = 0.0f, v1 = 0.0f;
+    const int t = tid >> 3, c = 2 * (tid & 7);
+    const bool one = tid < a.T * 8;
+    const int64_t o = (int64_t)t * a.H + 16 * tile + c;
+    float v0 = 0.0f, v1 = 0.0f;
+    if (one) {
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        v0 += sums[(w * a.T + t) * 16 + c];
-        v1 += sums[(w * a.T + t) * 16 + c + 1];
+      for (int w = 0; w < DC_WAVES; ++w) {
+        v0 += sums[w][t * 16 + c];
+        v1 += sums[w][t * 16 + c + 1];
       }
       if (a.S == 1) {
-        *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + 16 * tile + c) =
-            pk_bf16_rne(v0, v1);
+        *reinterpret_cast<uint32_t *>(a.out + o) = pk_bf16_rne(v0, v1);
       } else {
-        float *p = a.partial + ((int64_t)part * a.T + t) * a.H + 16 * tile + c;
-        __hip_atomic_store(p, v0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(p + 1, v1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(reinterpret_cast<uint64_t *>(a.partial + (int64_t)part * a.T * a.H + o),
+                           (uint64_t)__float_as_uint(v1) << 32 | __float_as_uint(v0),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
     if (a.S > 1) {
-      __threadfence();
+      // The sums went past the L2 and are waited for; a fence would write back the
+      // whole L2, for each wave.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (tid == 0)
-        last = __hip_atomic_fetch_add(&a.count[tile], 1u, __ATOMIC_ACQ_REL,
+        last = __hip_atomic_fetch_add(&a.count[tile], 1u, __ATOMIC_RELAXED,
                                       __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.S - 1;
       __syncthreads();
-      if (last) {
-        for (int i = tid; i < a.T * 8; i += 512) {
-          const int t = i >> 3, c = 2 * (i & 7);
-          float v0 = 0.0f, v1 = 0.0f;
-          for (int q = 0; q < a.S; ++q) {
-            const float *p = a.partial + ((int64_t)q * a.T + t) * a.H + 16 * tile + c;
-            v0 += __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            v1 += __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          }
-          *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.H + 16 * tile + c) =
-              pk_bf16_rne(v0, v1);
+      if (last && one) {
+        v0 = v1 = 0.0f;
+        for (int q = 0; q < a.S; ++q) {
+          const uint64_t v =
+              __hip_atomic_load(reinterpret_cast<uint64_t *>(a.partial + (int64_t)q * a.T * a.H + o),
+                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          v0 += __uint_as_float((uint32_t)v);
+          v1 += __uint_as_float((uint32_t)(v >> 32));
         }
+        *reinterpret_cast<uint32_t *>(a.out + o) = pk_bf16_rne(v0, v1);
       }
     }
     __syncthreads();
   }
+}
+
+// More tokens: the gate by itself, then the few-row products of gemv_nvfp4.hip
+// over all rows (the shared expert's among them), then the sum.
+template <int VPL>
+__global__ __launch_bounds__(256) void k_decode_gate(DcArgs a) {
+  __shared__ int32_t ids[4 * DC_K];
+  __shared__ float prob[4 * DC_K];
+  const int wave = dc_uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + wave;
+  if (t >= a.T) return;
+  dc_gate_of<VPL>(a, t, ids + wave * a.k, prob + wave * a.k);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (lane < a.c) {
+    const bool routed = lane < a.k;
+    const int32_t id = routed ? ids[wave * a.k + lane] : a.E;
+    const float p = routed ? prob[wave * a.k + lane] : 1.0f;
+    a.all_ids[t * a.c + lane] = id;
+    a.all_prob[t * a.c + lane] = p;
+    if (routed) {
+      a.ids[t * a.k + lane] = id;
+      a.prob[t * a.k + lane] = p;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_decode_sum(const float *__restrict__ rows, int T, int c,
+                                                    int H, uint16_t *__restrict__ out) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= T * H) return;
+  const int t = i / H, n = i - t * H;
+  gv_f4 v = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int j = 0; j < c; ++j)
+    v += *reinterpret_cast<const gv_f4 *>(rows + ((int64_t)t * c + j) * H + n);
+  *reinterpret_cast<uint2 *>(out + i) = make_uint2(pk_bf16_rne(v[0], v[1]), pk_bf16_rne(v[2], v[3]));
 }
 
 namespace {
@@ -617,18 +782,29 @@ struct DcPlan {
   int ks, S;
 };
 
-// By size alone: waves share a contraction until there are 4096 of them, and the
-// experts are parted until there are 1024 workgroups of the down projection, each
-// wave with a chunk at least.
+// By size alone, for as many experts met as there can be: the shape that leaves the
+// fewest turns of a wave, where an item costs half a turn of its own.
 DcPlan dc_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int shared) {
-  const int64_t met = (T * k < E ? T * k : E) + shared;
+  const int64_t met = (T * k < E ? T * k : E) + shared, chunks = (H + 255) / 256;
   DcPlan p = {1, 1};
-  while (p.ks < 8 && met * (I / 16) * p.ks < 4096 && 2 * p.ks <= (H + 255) / 256) p.ks *= 2;
-  int64_t s = (1024 + H / 16 - 1) / (H / 16);
-  const int64_t most = met * ((I + 255) / 256) / 8;
-  if (s > most) s = most;
-  if (s > met) s = met;
-  p.S = (int)(s < 1 ? 1 : s);
+  int64_t best = 0;
+  for (int ks = 1; ks <= DC_WAVES && ks <= chunks; ks *= 2) {
+    const int64_t per = DC_WAVES / ks, items = met * ((I / 16 + per - 1) / per);
+    const int64_t cost = (items + DC_GRID - 1) / DC_GRID * (2 * ((chunks + ks - 1) / ks) + 1);
+    if (ks == 1 || cost <= best) {
+      best = cost;
+      p.ks = ks;
+    }
+  }
+  const int64_t tiles = H / 16, units = met * ((I + 255) / 256);
+  for (int S = 1; S <= 8 && S <= met; ++S) {
+    const int64_t turns = ((units + S - 1) / S + DC_WAVES - 1) / DC_WAVES;
+    const int64_t cost = (tiles * S + DC_GRID - 1) / DC_GRID * (2 * turns + 1) + (S > 1 ? 3 : 0);
+    if (S == 1 || cost < best) {
+      best = cost;
+      p.S = S;
+    }
+  }
   return p;
 }
 
@@ -637,16 +813,31 @@ bool dc_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
          I <= DC_WIDTH && I % 32 == 0 && E >= 1 && E <= DC_EXPERTS && k >= 1 && k <= DC_K && k <= E;
 }
 
+// Offsets into the workspace.
 struct DcLayout {
-  size_t partial, count, bytes;
+  size_t y16, back, partial, count, sync, ids, prob, rows, bytes;
 };
 
 DcLayout dc_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int shared) {
-  const DcPlan p = dc_plan(T, H, I, E, k, shared);
   DcLayout l;
-  l.partial = (size_t)(T * E * 4 + 15) / 16 * 16;
-  l.count = l.partial + (p.S > 1 ? (size_t)p.S * T * H * 4 : 0);
-  l.bytes = l.count + (size_t)H / 16 * 4;
+  size_t at = 0;
+  const auto take = [&](int64_t n) {
+    const size_t r = at;
+    at += (size_t)(n + 255) / 256 * 256;
+    return r;
+  };
+  const bool few = T <= DC_FEW;
+  const int64_t rows = T * (k + shared);
+  take(T * E * 4);
+  l.y16 = take(few ? T * H * 2 : 0);
+  l.back = take(few ? T * 4 : 0);
+  l.partial = take(few ? dc_plan(T, H, I, E, k, shared).S * T * H * 4 : 0);
+  l.count = take(H / 16 * 4);
+  l.sync = take(sizeof(DcSync));
+  l.ids = take(few ? 0 : rows * 4);
+  l.prob = take(few ? 0 : rows * 4);
+  l.rows = take(few ? 0 : rows * H * 4);
+  l.bytes = at;
   return l;
 }
 
@@ -661,31 +852,36 @@ void dc_router(const DcArgs &a, bool wf32, hipStream_t st) {
   else hipLaunchKernelGGL((k_decode_router<NC, false>), grid, dim3(512), lds, st, a);
 }
 
-template <int MAXMT, int VPL>
-void dc_launch_up(const DcArgs &a, unsigned grid, hipStream_t st) {
-  if (a.H % 64 == 0)
-    hipLaunchKernelGGL((k_decode_up<MAXMT, VPL, true>), dim3(grid), dim3(512), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_decode_up<MAXMT, VPL, false>), dim3(grid), dim3(512), 0, st, a);
+template <int VPL>
+hipError_t dc_few(const DcArgs &a, hipStream_t st) {
+  const auto kernel = a.H % 64 == 0 ? a.I % 64 == 0 ? k_decode_experts<VPL, true, true>
+                                                    : k_decode_experts<VPL, true, false>
+                      : a.I % 64 == 0 ? k_decode_experts<VPL, false, true>
+                                      : k_decode_experts<VPL, false, false>;
+  hipLaunchKernelGGL(kernel, dim3(DC_GRID), dim3(64 * DC_WAVES), 0, st, a);
+  return hipGetLastError();
 }
 
-template <int MAXMT>
-hipError_t dc_experts(const DcArgs &a, hipStream_t st) {
-  const int64_t met = (a.T * a.k < a.E ? a.T * a.k : a.E) + (a.c - a.k);
-  const int64_t per = 8 / a.ks, items = met * ((a.I / 16 + per - 1) / per);
-  const unsigned grid = (unsigned)(items < 512 ? items : 512);
-  if (a.E <= 64) dc_launch_up<MAXMT, 1>(a, grid, st);
-  else if (a.E <= 128) dc_launch_up<MAXMT, 2>(a, grid, st);
-  else if (a.E <= 256) dc_launch_up<MAXMT, 4>(a, grid, st);
-  else dc_launch_up<MAXMT, 16>(a, grid, st);
-  const hipError_t r = hipGetLastError();
+template <int VPL>
+hipError_t dc_many(const DcArgs &a, float *rows, hipStream_t st) {
+  hipLaunchKernelGGL(k_decode_gate<VPL>, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
+  hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
-  const int64_t down = (int64_t)(a.H / 16) * a.S;
-  const dim3 dgrid((unsigned)(down < 512 ? down : 512));
-  const size_t lds = (size_t)8 * a.T * 16 * 4;
-  if (a.I % 64 == 0) hipLaunchKernelGGL((k_decode_down<MAXMT, true>), dgrid, dim3(512), lds, st, a);
-  else hipLaunchKernelGGL((k_decode_down<MAXMT, false>), dgrid, dim3(512), lds, st, a);
+  const int64_t n = (int64_t)a.T * a.c, G = a.E + (a.c - a.k);
+  r = launch_gemv_nvfp4(a.y, a.all_ids, a.all_prob, n, a.c, a.w1, a.s1, a.g1, 2 * a.I, G, a.I, a.H,
+                        a.d, false, st);
+  if (r != hipSuccess) return r;
+  r = launch_gemv_nvfp4(a.d, a.all_ids, nullptr, n, 1, a.w2, a.s2, a.g2, a.H, G, a.H, a.I, rows,
+                        true, st);
+  if (r != hipSuccess) return r;
+  hipLaunchKernelGGL(k_decode_sum, dim3((unsigned)((a.T * a.H / 4 + 255) / 256)), dim3(256), 0, st,
+                     rows, a.T, a.c, a.H, a.out);
   return hipGetLastError();
+}
+
+template <int VPL>
+hipError_t dc_experts(const DcArgs &a, float *rows, hipStream_t st) {
+  return a.T <= DC_FEW ? dc_few<VPL>(a, st) : dc_many<VPL>(a, rows, st);
 }
 
 }  // namespace
@@ -734,14 +930,23 @@ pqm_status pqm_moe_decode_nvfp4(const uint16_t *x, const uint16_t *residual, con
                     (int)num_experts, (int)k, (int)k + shared_expert, score == PQM_SCORE_SOFTMAX,
                     renormalize, scale, w1_q, w1_scale, w1_outer, w2_q, w2_scale, w2_outer, h, y,
                     topk_ids, prob, d, out, reinterpret_cast<float *>(ws),
+                    tokens <= DC_FEW ? reinterpret_cast<uint16_t *>(ws + l.y16) : nullptr,
+                    reinterpret_cast<float *>(ws + l.back),
                     reinterpret_cast<float *>(ws + l.partial),
-                    reinterpret_cast<uint32_t *>(ws + l.count), p.ks, p.S};
+                    reinterpret_cast<uint32_t *>(ws + l.count),
+                    reinterpret_cast<DcSync *>(ws + l.sync),
+                    reinterpret_cast<int32_t *>(ws + l.ids),
+                    reinterpret_cast<float *>(ws + l.prob), p.ks, p.S};
   const bool wf32 = norm_dtype == PQM_OUT_FP32;
   if (hidden <= 4096) dc_router<1>(a, wf32, stream);
   else if (hidden <= 8192) dc_router<2>(a, wf32, stream);
   else dc_router<4>(a, wf32, stream);
   if (hipGetLastError() != hipSuccess) return PQM_ERR_HIP;
-  const hipError_t r = tokens <= 16 ? dc_experts<1>(a, stream) : dc_experts<2>(a, stream);
+  float *rows = reinterpret_cast<float *>(ws + l.rows);
+  const hipError_t r = num_experts <= 64    ? dc_experts<1>(a, rows, stream)
+                       : num_experts <= 128 ? dc_experts<2>(a, rows, stream)
+                       : num_experts <= 256 ? dc_experts<4>(a, rows, stream)
+                                            : dc_experts<16>(a, rows, stream);
   return r == hipSuccess ? PQM_OK : PQM_ERR_HIP;
 }
 
