@@ -28,6 +28,7 @@ typedef __attribute__((address_space(3))) ln_v4s ln_lds_v4s;
 constexpr uint32_t LN_NONE = 0x80000000u;  // an offset past every buffer below: reads give 0
 constexpr int64_t LN_MAX = 1 << 22;        // row strides: 256 rows of 2-byte values stay below 2^31
 constexpr int LN_FEW = 64;                 // rows of the few-row kernel
+constexpr int64_t LN_SHARE = 4096;         // outputs from which its tiles share
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t ln_buffer(const void *p, int64_t bytes) {
   const int n = (int)(bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes);
@@ -47,22 +48,24 @@ struct LnEpi {
   int vec;  // rows of y, z and res hold whole, aligned groups of eight
 };
 
-// s(z) of the activation, and its slope.
+// -s(z) log2(e) of the activation.
 __device__ __forceinline__ float ln_squash(float z, int act) {
-  return act == PQM_ACT_SILU ? z : 1.5957691216057308f * z * (1.0f + 0.044715f * z * z);
+  constexpr float L = 1.4426950408889634f, G = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+  return act == PQM_ACT_SILU ? -L * z : z * __builtin_fmaf(z * z, -L * G * 0.044715f, -L * G);
 }
 __device__ __forceinline__ float ln_act(float z, int act) {
   if (act == PQM_ACT_NONE) return z;
-  return z * __builtin_amdgcn_rcpf(1.0f + __expf(-ln_squash(z, act)));
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(ln_squash(z, act)));
 }
 // act'(z) = v + z v (1 - v) s'(z) with v the sigmoid of s; v (1 - v) is even in
 // s, so it is formed with e^-|s|, which cannot overflow.
 __device__ __forceinline__ float ln_slope(float z, int act) {
   const float s = ln_squash(z, act);
-  const float ds = act == PQM_ACT_SILU ? 1.0f
-                                       : 1.5957691216057308f * (1.0f + 0.134145f * z * z);
-  const float t = __expf(-fabsf(s)), r = __builtin_amdgcn_rcpf(1.0f + t);
-  const float v = s < 0.0f ? t * r : r, w = t * r * r;
+  const float ds = act == PQM_ACT_SILU
+                       ? 1.0f
+                       : __builtin_fmaf(z * z, 1.5957691216057308f * 0.134145f, 1.5957691216057308f);
+  const float t = __builtin_amdgcn_exp2f(-fabsf(s)), r = __builtin_amdgcn_rcpf(1.0f + t);
+  const float v = s > 0.0f ? t * r : r, w = t * r * r;
   // far out w is 0 and z ds may be infinite
   return w == 0.0f && s == s ? v : v + z * ds * w;
 }
@@ -81,14 +84,22 @@ __device__ __forceinline__ void ln_put1(const LnEpi &e, int64_t r, int64_t c, fl
 }
 
 // Eight neighbouring outputs of row r from column c on, where rows hold whole,
-// aligned groups of eight (e.vec).
-__device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, float (&v)[8]) {
+// aligned groups of eight (e.vec); q, b: ln_res8 and ln_bias8 of them, which their
+// callers ask for early.
+__device__ __forceinline__ ln_u4 ln_res8(const LnEpi &e, int64_t r, int64_t c) {
+  if (!e.res) return ln_u4{0, 0, 0, 0};
+  return *reinterpret_cast<const ln_u4 *>(e.res + r * e.ldr + c);
+}
+__device__ __forceinline__ void ln_bias8(const LnEpi &e, int64_t c, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = e.bias ? e.bias[c + i] : 0.0f;
+}
+__device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, float (&v)[8],
+                                        const ln_u4 &q, const float (&b)[8]) {
   const int64_t at = r * e.N + c;
-  ln_u4 q = {0, 0, 0, 0};
-  if (e.res) q = *reinterpret_cast<const ln_u4 *>(e.res + r * e.ldr + c);
   if (e.bias) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += e.bias[c + i];
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
   if (e.z) {
     const ln_u4 o = {pk_bf16_rne(v[0], v[1]), pk_bf16_rne(v[2], v[3]), pk_bf16_rne(v[4], v[5]),
@@ -130,9 +141,9 @@ struct LnTile {
   float *partial;     // [splits][I][J] when the contraction is split
 };
 
-template <int TM_, int TN_>
+template <int TM_, int TN_, int NS_>
 struct Ln {
-  static constexpr int TM = TM_, TN = TN_, NS = 4;
+  static constexpr int TM = TM_, TN = TN_, NS = NS_;
   static constexpr int SLOT = (TM + TN) * 64, RING = NS * SLOT;
   static constexpr int FI = TM / 64, FJ = TN / 64;  // 32-wide fragments of a wave (2 x 2 waves)
   static constexpr int CA = TM / 64, CB = TN / 64, OPS = CA + CB;
@@ -155,52 +166,62 @@ __device__ __forceinline__ int ln_swz(int r) {
 
 // One operand's loads.  A lane's 16-byte chunk c of a step is row c / 4, piece
 // c % 4 (KL) or contraction row c / (W / 8), piece c % (W / 8) (ML); it goes to
-// LDS byte 16 c, so the swizzle is in where it comes from.
+// LDS byte 16 c, so the swizzle is in where it comes from.  What lies past the
+// operand's end reads as 0: rows and, of an ML operand, contraction past the end of
+// the buffer; a KL operand's contraction past its end by an offset past the buffer.
 template <int W, bool ML>
 struct LnSrc {
-  const uint8_t *base;
-  int64_t left, step;     // bytes from base to the end; base's way per step
+  const uint8_t *base;    // of the next step to load
+  int64_t step;           // base's way per step, bytes
+  int left;               // contraction left from base on
+  int rows, ld2;          // KL: bytes to the end of the last row's start; ML: of a row used
   uint32_t off[W / 64];
   int piece;              // KL: the lane's piece of a step
-  int64_t kleft;          // KL: contraction left from base on
 
   __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t first, int64_t lines,
                                        int64_t k0, int64_t K) {
     const int tid = threadIdx.x;
+    const int n = (int)min((int64_t)W, lines - first);
+    left = (int)(K - k0);
+    ld2 = (int)ld * 2;
     if (ML) {  // lines: outputs; first: the first of them
       base = reinterpret_cast<const uint8_t *>(p + k0 * ld + first);
-      left = ((K - k0 - 1) * ld + min((int64_t)W, lines - first)) * 2;
       step = 64 * ld;
+      rows = 2 * n;
+      piece = 0;
 #pragma unroll
       for (int i = 0; i < W / 64; ++i) {
         const int c = tid + 256 * i, r = c / (W / 8), x = (c % (W / 8)) ^ (4 * ln_swz<W>(r));
-        off[i] = (uint32_t)(r * ld * 2 + 16 * x);
+        off[i] = (uint32_t)(r * ld2 + 16 * x);
       }
-      piece = 0;
-      kleft = 0;
     } else {
       base = reinterpret_cast<const uint8_t *>(p + first * ld + k0);
-      left = ((min((int64_t)W, lines - first) - 1) * ld + K - k0) * 2;
       step = 64;
+      rows = (n - 1) * ld2;
       piece = 8 * ((tid & 3) ^ ((tid >> 4) & 3));
-      kleft = K - k0;
 #pragma unroll
       for (int i = 0; i < W / 64; ++i)
-        off[i] = (uint32_t)(((tid >> 2) + 64 * i) * ld * 2 + 2 * piece);
+        off[i] = (uint32_t)(((tid >> 2) + 64 * i) * ld2 + 2 * piece);
     }
   }
-  // Chunk i of step kt to LDS address m0 (the wave's).
-  __device__ __forceinline__ void load(int kt, int i, uint32_t m0) const {
-    const __amdgpu_buffer_rsrc_t r = ln_buffer(base + kt * step, left - kt * step);
-    const uint32_t o = ML || kt * 32 + piece < kleft ? off[i] : LN_NONE;
+  // Chunk i of the next step to LDS address m0 (the wave's).
+  __device__ __forceinline__ void load(int i, uint32_t m0) const {
+    const int l = min(left, 32), bytes = ML ? (l - 1) * ld2 + rows : rows + 2 * left;
+    const uint32_t o = ML || piece < left ? off[i] : LN_NONE;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void *)(uintptr_t)m0, 16, (int)o, 0, 0, 0);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0,
+                                          left > 0 ? bytes : 0, 0x00020000),
+        (__attribute__((address_space(3))) void *)(uintptr_t)m0, 16, (int)o, 0, 0, 0);
+  }
+  __device__ __forceinline__ void next() {
+    base += step;
+    left -= 32;
   }
 };
 
 template <int TM, int TN>
 struct LnFrags {
-  ln_u4 a[Ln<TM, TN>::FI][2], b[Ln<TM, TN>::FJ][2];  // [fragment][16-wide half of the step]
+  ln_u4 a[TM / 64][2], b[TN / 64][2];  // [fragment][16-wide half of the step]
 };
 
 // A fragment of 32 outputs (32x32x16: lane l holds output l % 32, contraction
@@ -234,9 +255,10 @@ __device__ __forceinline__ void ln_read(const uint8_t *reg, int first, ln_u4 (&f
 
 }  // namespace
 
-template <int KIND, int TM, int TN>
-__global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnEpi e) {
-  using C = Ln<TM, TN>;
+template <int KIND, int TM, int TN, int NS>
+__global__ __launch_bounds__(256, NS * (TM + TN) * 64 > 81920 ? 1 : 2) void k_linear(LnTile t,
+                                                                                  LnEpi e) {
+  using C = Ln<TM, TN, NS>;
   constexpr bool AM = KIND == LN_TN, BM = KIND != LN_NT;
   constexpr int FI = C::FI, FJ = C::FJ;
   __shared__ __align__(16) uint8_t lds[C::LDS];
@@ -260,10 +282,12 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
   B.init(t.b, t.ldb, j0, t.J, k0, k1);
   const uint32_t dst =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u);
-  const auto load = [&](int kt, int slot, int q) {
+  const auto load = [&](int slot, int q) {
     const uint32_t m0 = dst + slot * C::SLOT;
-    if (q < C::CA) A.load(kt, q, m0 + q * 4096);
-    else B.load(kt, q - C::CA, m0 + TM * 64 + (q - C::CA) * 4096);
+    if (q < C::CA) A.load(q, m0 + q * 4096);
+    else B.load(q - C::CA, m0 + TM * 64 + (q - C::CA) * 4096);
+    if (q == C::CA - 1) A.next();
+    if (q == C::OPS - 1) B.next();
   };
   const auto read_a = [&](int slot, int f, LnFrags<TM, TN> &F) {
     ln_read<TM, AM>(lds + slot * C::SLOT, wm * (TM / 2) + 32 * f, F.a[f]);
@@ -281,10 +305,10 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   const int nk = (int)((k1 - k0 + 31) / 32);
-#pragma unroll
+#pragma unroll 1  // code that runs once waits for its own instructions
   for (int s = 0; s < C::NS; ++s)
 #pragma unroll
-    for (int q = 0; q < C::OPS; ++q) load(s, s, q);
+    for (int q = 0; q < C::OPS; ++q) load(s, q);
   LnFrags<TM, TN> F0, F1;
   ln_vm_wait<(C::NS - 1) * C::OPS>();
   __builtin_amdgcn_s_barrier();
@@ -294,10 +318,10 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
   for (int f = 0; f < FJ; ++f) read_b(0, f, F0);
 
   // A step: its fragments are in registers; after each matrix instruction comes a
-  // slice of the other work: the loads of step kt + NS into the slot that every
-  // wave has left, and the fragments of step kt + 1.
-  const auto step = [&](int kt, int slot, const LnFrags<TM, TN> &cur, LnFrags<TM, TN> &next) {
-    ln_vm_wait<(C::NS - 2) * C::OPS>();  // step kt + 1 has landed
+  // slice of the other work: the fragments of the next step, and the loads of the step
+  // NS ahead into the slot that every wave has left.
+  const auto step = [&](int slot, const LnFrags<TM, TN> &cur, LnFrags<TM, TN> &next) {
+    ln_vm_wait<(C::NS - 2) * C::OPS>();  // the next step has landed
     ln_lgkm_wait0();
     __builtin_amdgcn_s_barrier();
     const int after = slot == C::NS - 1 ? 0 : slot + 1;
@@ -313,16 +337,16 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
         // the next fragments first: the next step waits for them
         if (w < FI) read_a(after, w, next);
         else if (w < FI + FJ) read_b(after, w - FI, next);
-        else load(kt + C::NS, slot, w - FI - FJ);
+        else load(slot, w - FI - FJ);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   int slot = 0;
   for (int kt = 0; kt < nk; kt += 2) {
-    step(kt, slot, F0, F1);
+    step(slot, F0, F1);
     slot = slot == C::NS - 1 ? 0 : slot + 1;
-    step(kt + 1, slot, F1, F0);  // past the end it multiplies zeros
+    step(slot, F1, F0);  // past the end it multiplies zeros
     slot = slot == C::NS - 1 ? 0 : slot + 1;
   }
   ln_vm_wait<0>();  // no load may still target the LDS that the epilogue uses
@@ -331,10 +355,21 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
   // A lane holds row l % 32, columns 8 (i / 4) + 4 (l / 32) + i % 4: through LDS,
   // 32 rows of the wave at a time, so that rows leave as whole lines.
   uint8_t *mine = lds + wave * 32 * C::PITCH;
-  constexpr int LPR = TN / 2 / 8, RPI = 64 / LPR;  // lanes a row, rows a turn
+  constexpr int LPR = TN / 2 / 8, RPI = 64 / LPR, NR = 32 / RPI;  // lanes a row, rows a turn, turns
   const int64_t col = j0 + wn * (TN / 2) + 8 * (lane % LPR);
+  const float *p = reinterpret_cast<const float *>(mine + lane / LPR * C::PITCH) + 8 * (lane % LPR);
+  const bool vec = t.partial ? t.J % 8 == 0 : e.vec;
+  float bias[8];
+  if (vec && !t.partial) ln_bias8(e, min(col, t.J - 8), bias);
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
+    const int64_t row = i0 + wm * (TM / 2) + 32 * i + lane / LPR;  // of the first turn
+    ln_u4 res[NR];
+    if (vec && !t.partial) {  // all 32 rows' residual at once
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        res[r] = ln_res8(e, min(row + r * RPI, t.I - 1), min(col, t.J - 8));
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
@@ -345,30 +380,32 @@ __global__ __launch_bounds__(256, TM == 256 ? 1 : 2) void k_linear(LnTile t, LnE
             ln_f4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                   acc[i][j][4 * q + 3]};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 1
-    for (int r = lane / LPR; r < 32; r += RPI) {
-      const int64_t row = i0 + wm * (TM / 2) + 32 * i + r;
-      if (row >= t.I || col >= t.J) break;
-      const float *p = reinterpret_cast<const float *>(mine + r * C::PITCH) + 8 * (lane % LPR);
-      float *w = t.partial ? t.partial + (split * t.I + row) * t.J + col : nullptr;
-      if (w ? t.J % 8 == 0 : e.vec) {
-        const ln_f4 lo = *reinterpret_cast<const ln_f4 *>(p);
-        const ln_f4 hi = *reinterpret_cast<const ln_f4 *>(p + 4);
-        if (w) {
-          reinterpret_cast<ln_f4 *>(w)[0] = lo;
-          reinterpret_cast<ln_f4 *>(w)[1] = hi;
+    if (vec) {
+      float *w = t.partial + (split * t.I + row) * t.J + col;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const ln_f4 *o = reinterpret_cast<const ln_f4 *>(p + r * RPI * (C::PITCH / 4));
+        const ln_f4 lo = o[0], hi = o[1];
+        if (row + r * RPI >= t.I || col >= t.J) continue;
+        if (t.partial) {
+          ln_f4 *to = reinterpret_cast<ln_f4 *>(w + r * RPI * t.J);
+          to[0] = lo;
+          to[1] = hi;
         } else {
-          float o[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          ln_put8(e, row, col, o);
-        }
-      } else {
-        const int n = (int)min((int64_t)8, t.J - col);
-#pragma unroll 1
-        for (int c = 0; c < n; ++c) {
-          if (w) w[c] = p[c];
-          else ln_put1(e, row, col + c, p[c]);
+          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          ln_put8(e, row + r * RPI, col, v, res[r], bias);
         }
       }
+    } else {
+      const int n = (int)min((int64_t)8, t.J - col);
+#pragma unroll 1
+      for (int r = 0; r < NR && row + r * RPI < t.I; ++r)
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+          const float v = p[r * RPI * (C::PITCH / 4) + c];
+          if (t.partial) t.partial[(split * t.I + row + r * RPI) * t.J + col + c] = v;
+          else ln_put1(e, row + r * RPI, col + c, v);
+        }
     }
   }
 }
@@ -381,24 +418,33 @@ __global__ __launch_bounds__(256) void k_linear_join(const float *__restrict__ p
        g += (int64_t)gridDim.x * 256) {
     const int64_t row = g / groups, col = 8 * (g - row * groups);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < splits; ++s) {
-      const float *p = partial + (s * I + row) * J + col;
-      if (J % 8 == 0) {
-        const ln_f4 lo = reinterpret_cast<const ln_f4 *>(p)[0];
-        const ln_f4 hi = reinterpret_cast<const ln_f4 *>(p)[1];
+    const float *p = partial + row * J + col;
+    const int64_t step = I * J;
+    ln_u4 res = {0, 0, 0, 0};
+    float bias[8];
+    if (e.vec) {
+      res = ln_res8(e, row, col);
+      ln_bias8(e, col, bias);
+    }
+    if (J % 8 == 0) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const ln_f4 lo = *reinterpret_cast<const ln_f4 *>(p + s * step);
+        const ln_f4 hi = *reinterpret_cast<const ln_f4 *>(p + s * step + 4);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           v[c] += lo[c];
           v[4 + c] += hi[c];
         }
-      } else {
+      }
+    } else {
+      for (int s = 0; s < splits; ++s)
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (col + c < J) v[c] += p[c];
-      }
+          if (col + c < J) v[c] += p[s * step + c];
     }
     if (e.vec) {
-      ln_put8(e, row, col, v);
+      ln_put8(e, row, col, v, res, bias);
     } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -409,131 +455,161 @@ __global__ __launch_bounds__(256) void k_linear_join(const float *__restrict__ p
 
 // ------------------------------------------------------------- few rows
 //
-// Up to 64 rows of x: what counts is reading W once.  A wave multiplies 16 rows
-// of W, straight from memory to registers, by MT tiles of 16 rows of x with a
-// 16x16x32 matrix instruction; KS of a workgroup's waves share a contraction
-// and are joined through LDS.
-template <int MT>
-__global__ __launch_bounds__(256, 4) void k_linear_few(const uint16_t *__restrict__ x, int64_t ldx,
+// Up to 64 rows of x: what counts is reading W once.  A wave multiplies NT tiles of
+// 16 rows of W, straight from memory to registers, by MT tiles of 16 rows of x with a
+// 16x16x32 matrix instruction; ks of a workgroup's waves share a contraction and are
+// joined through LDS.  Bound by memory (8 rows to 32768 outputs of 2048: 134 MB in
+// 29.9 us, 4.5 TB/s) and from 32 rows on by the L1, which brings x to every wave.
+// Every load of a turn goes out before the first is used; a streaming hint costs a
+// tenth, since two loads share a line.
+template <int MT, int NT>
+__global__ __launch_bounds__(512, 4) void k_linear_few(const uint16_t *__restrict__ x, int64_t ldx,
                                                        const uint16_t *__restrict__ w, int64_t M,
                                                        int64_t K, int ks, LnEpi e) {
-  __shared__ ln_f4 red[4][MT][64];
+  __shared__ ln_f4 red[8][MT * NT][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, ln = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % ks, tile = wave / ks;
-  const int64_t n0 = ((int64_t)blockIdx.x * (4 / ks) + tile) * 16;
-  const __amdgpu_buffer_rsrc_t wb = ln_buffer(w + n0 * K, min((int64_t)16, e.N - n0) * K * 2);
-  const __amdgpu_buffer_rsrc_t xb = ln_buffer(x, ((M - 1) * ldx + K) * 2);
-  const uint32_t wo = (uint32_t)(ln * K + 8 * g) * 2;
-  uint32_t xo[MT];
+  const int64_t n0 = ((int64_t)blockIdx.x * (8 / ks) + tile) * (16 * NT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const __amdgpu_buffer_rsrc_t wb = ln_buffer(w + n0 * K, min((int64_t)16 * NT, e.N - n0) * K * 2);
+  const int rows = (int)min((int64_t)16 * MT, M - m0);
+  const __amdgpu_buffer_rsrc_t xb = ln_buffer(x + m0 * ldx, ((rows - 1) * ldx + K) * 2);
+  uint32_t wo[NT], xo[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xo[m] = 16 * m + ln < M ? (uint32_t)((16 * m + ln) * ldx + 8 * g) * 2 : LN_NONE;
-  ln_f4 acc[MT] = {};
-  constexpr int U = MT == 1 ? 8 : MT == 2 ? 4 : 2;  // steps of 32 in flight
+  for (int t = 0; t < NT; ++t) wo[t] = (uint32_t)((16 * t + ln) * K + 8 * g) * 2;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int r = 16 * m + ln;
+    xo[m] = r < rows ? (uint32_t)(r * ldx + 8 * g) * 2 : LN_NONE;
+  }
+  ln_f4 acc[MT][NT] = {};
+  constexpr int U = MT == 1 ? 8 / NT : MT == 2 ? 4 : MT == 3 ? 3 : 2;  // steps of 32 in flight
   const int steps = (int)((K + 31) / 32), each = (steps + ks - 1) / ks;
   const int s1 = min(steps, (kw + 1) * each);
   for (int s = kw * each; s < s1; s += U) {
-    ln_u4 wv[U], xv[U][MT];
+    ln_u4 wv[U][NT], xv[U][MT];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int k = 32 * (s + i) + 8 * g;
-      const bool in = s + i < s1 && k < K;
-      wv[i] = __builtin_amdgcn_raw_buffer_load_b128(wb, (int)(in ? wo + 64 * (s + i) : LN_NONE), 0,
-                                                    2);
+      const uint32_t none = s + i < s1 && 32 * (s + i) + 8 * g < K ? 0 : LN_NONE;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        wv[i][t] = __builtin_amdgcn_raw_buffer_load_b128(wb, (int)((wo[t] + 64 * (s + i)) | none),
+                                                         0, 0);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        xv[i][m] = __builtin_amdgcn_raw_buffer_load_b128(
-            xb, (int)(in && 16 * m + ln < M ? xo[m] + 64 * (s + i) : LN_NONE), 0, 0);
+        xv[i][m] = __builtin_amdgcn_raw_buffer_load_b128(xb, (int)((xo[m] + 64 * (s + i)) | none),
+                                                         0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(ln_bf8, wv[i]),
-                                                         __builtin_bit_cast(ln_bf8, xv[i][m]),
-                                                         acc[m], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(ln_bf8, wv[i][t]), __builtin_bit_cast(ln_bf8, xv[i][m]),
+              acc[m][t], 0, 0, 0);
   }
   if (ks > 1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) red[wave][m][lane] = acc[m];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) red[wave][m * NT + t][lane] = acc[m][t];
     __syncthreads();
     if (kw > 0) return;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      for (int s = 1; s < ks; ++s) acc[m] += red[wave + s][m][lane];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        for (int s = 1; s < ks; ++s) acc[m][t] += red[wave + s][m * NT + t][lane];
   }
-  // lane: row 16 m + l % 16 of x, outputs n0 + 4 (l / 16) ..: joined in pairs of
+  // lane: row 16 m + l % 16 of x, outputs n0 + 16 t + 4 (l / 16) ..: joined in pairs of
   // lane groups to eight neighbouring outputs
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    float v[8];
+  for (int t = 0; t < NT; ++t) {
+    const int64_t col = n0 + 16 * t + 4 * g;
+    float bias[8] = {};
+    if (e.vec && col + 8 <= e.N) ln_bias8(e, col, bias);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = acc[m][i];
-      v[4 + i] = __shfl_down(acc[m][i], 16, 64);
-    }
-    const int64_t row = 16 * m + ln, col = n0 + 4 * g;
-    if ((g & 1) || row >= M || col >= e.N) continue;
-    if (e.vec) {
-      ln_put8(e, row, col, v);
-    } else {
+    for (int m = 0; m < MT; ++m) {
+      float v[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (col + c < e.N) ln_put1(e, row, col + c, v[c]);
+      for (int i = 0; i < 4; ++i) {
+        v[i] = acc[m][t][i];
+        v[4 + i] = __shfl_down(acc[m][t][i], 16, 64);
+      }
+      const int64_t row = m0 + 16 * m + ln;
+      if ((g & 1) || row >= M || col >= e.N) continue;
+      if (e.vec) {
+        ln_put8(e, row, col, v, ln_res8(e, row, col), bias);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (col + c < e.N) ln_put1(e, row, col + c, v[c]);
+      }
     }
   }
 }
 
 // ------------------------------------------------- dz and the bias gradient
 
-constexpr int LZ_ROWS = 64;  // rows of a workgroup's partial sums
+constexpr int LZ_ROWS = 32;  // rows of a workgroup's partial sums
 
 // dz = bf16(dy act'(z)) (act none: dy itself, not written) and, per LZ_ROWS
-// rows, the column sums of dz.  A thread takes eight columns of every fourth row.
+// rows, the column sums of dz.  A thread takes eight columns of every 256 / CT-th
+// row, four rows asked for at once; CT threads a row, as many as fill it.
+template <int CT>
 __global__ __launch_bounds__(256) void k_linear_dz(const uint16_t *__restrict__ dy, int64_t lddy,
-                                                   const uint16_t *__restrict__ z, int act,
-                                                   int64_t M, int64_t N, uint16_t *dz,
+                                                   const uint16_t *z, int act, int64_t M,
+                                                   int64_t N, uint16_t *dz,
                                                    float *__restrict__ sums) {
-  __shared__ float part[3][64][8];
-  const int c8 = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t col = ((int64_t)blockIdx.y * 64 + c8) * 8, r0 = (int64_t)blockIdx.x * LZ_ROWS;
+  constexpr int RT = 256 / CT, NR = LZ_ROWS / RT, NB = NR < 4 ? NR : 4;
+  __shared__ float part[RT][CT][9];
+  const int c8 = threadIdx.x % CT, q = threadIdx.x / CT;
+  const int64_t col = ((int64_t)blockIdx.y * CT + c8) * 8;
+  const int64_t r0 = (int64_t)blockIdx.x * LZ_ROWS + q;
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (col < N) {
-#pragma unroll 4
-    for (int i = q; i < LZ_ROWS; i += 4) {
-      const int64_t r = r0 + i;
-      if (r >= M) break;
-      ln_u4 d = *reinterpret_cast<const ln_u4 *>(dy + r * lddy + col);
+#pragma unroll 1
+  for (int h = 0; h < NR; h += NB) {
+    ln_u4 d[NB], zz[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int64_t r = r0 + (h + i) * RT;
+      const bool in = col < N && r < M;
+      d[i] = zz[i] = ln_u4{0, 0, 0, 0};
+      if (in) d[i] = *reinterpret_cast<const ln_u4 *>(dy + r * lddy + col);
+      if (in && act != PQM_ACT_NONE) zz[i] = *reinterpret_cast<const ln_u4 *>(z + r * N + col);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int64_t r = r0 + (h + i) * RT;
       if (act != PQM_ACT_NONE) {
-        const ln_u4 zz = *reinterpret_cast<const ln_u4 *>(z + r * N + col);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          d[j] = pk_bf16_rne(bf16_lo_f32(d[j]) * ln_slope(bf16_lo_f32(zz[j]), act),
-                             bf16_hi_f32(d[j]) * ln_slope(bf16_hi_f32(zz[j]), act));
-        *reinterpret_cast<ln_u4 *>(dz + r * N + col) = d;
+          d[i][j] = pk_bf16_rne(bf16_lo_f32(d[i][j]) * ln_slope(bf16_lo_f32(zz[i][j]), act),
+                                bf16_hi_f32(d[i][j]) * ln_slope(bf16_hi_f32(zz[i][j]), act));
+        if (col < N && r < M) *reinterpret_cast<ln_u4 *>(dz + r * N + col) = d[i];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[2 * j] += bf16_lo_f32(d[j]);
-        s[2 * j + 1] += bf16_hi_f32(d[j]);
+        s[2 * j] += bf16_lo_f32(d[i][j]);
+        s[2 * j + 1] += bf16_hi_f32(d[i][j]);
       }
     }
   }
   if (!sums) return;
-  if (q > 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[q - 1][c8][j] = s[j];
-  }
+  for (int j = 0; j < 8; ++j) part[q][c8][j] = s[j];
   __syncthreads();
-  if (q > 0 || col >= N) return;
+  for (int c = threadIdx.x; c < 8 * CT; c += 256) {
+    const int64_t at = (int64_t)blockIdx.y * CT * 8 + c;
+    float v = 0.0f;
 #pragma unroll
-  for (int p = 0; p < 3; ++p)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += part[p][c8][j];
-  ln_f4 *o = reinterpret_cast<ln_f4 *>(sums + blockIdx.x * N + col);
-  o[0] = ln_f4{s[0], s[1], s[2], s[3]};
-  o[1] = ln_f4{s[4], s[5], s[6], s[7]};
+    for (int p = 0; p < RT; ++p) v += part[p][c >> 3][c & 7];
+    if (at < N) sums[blockIdx.x * N + at] = v;
+  }
 }
 
 // The partial sums' sum in one order: 16 columns a workgroup, 16 threads a column.
@@ -543,8 +619,10 @@ __global__ __launch_bounds__(256) void k_linear_colsum(const float *__restrict__
   const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
   const int64_t col = (int64_t)blockIdx.x * 16 + c;
   float v = 0.0f;
-  if (col < N)
+  if (col < N) {
+#pragma unroll 8
     for (int64_t p = q; p < parts; p += 16) v += sums[p * N + col];
+  }
   s[q][c] = v;
   __syncthreads();
   if (q > 0 || col >= N) return;
@@ -564,7 +642,7 @@ namespace {
 
 struct LnPlan {
   int tm, tn, splits;
-  int64_t part;
+  int64_t part, ns;  // ns: an estimate, for 128 x 128 tiles
 };
 
 int64_t ln_tiles(int64_t I, int64_t J, int tm, int tn) {
@@ -572,22 +650,27 @@ int64_t ln_tiles(int64_t I, int64_t J, int tm, int tn) {
 }
 
 // Tiles and splits by size alone.
-LnPlan ln_plan(int kind, int64_t I, int64_t J, int64_t K) {
-  LnPlan p = {128, 128, 1, (K + 31) / 32 * 32};
-  const int64_t big = ln_tiles(I, J, 256, 256);
-  if (big >= 200) {
+//
+// 256 x 256 tiles from 200 of them on (8190 x 4096 x 2048: 976 TFLOP/s, 128 x 128
+// 750).  Below that 128 x 128, whose step of 32 takes 0.24 us on a CU (LDS) and,
+// from about 200 workgroups on, 1.25 ns a workgroup (the L2s give 13 TB/s); splitting
+// the contraction pays where the steps saved outweigh a launch of 4 us and the
+// partial sums' way out and back.
+LnPlan ln_plan(int64_t I, int64_t J, int64_t K) {
+  LnPlan p = {128, 128, 1, (K + 31) / 32 * 32, 0};
+  if (ln_tiles(I, J, 256, 256) >= 200) {
     p.tm = p.tn = 256;
     return p;
   }
-  const int64_t tiles = ln_tiles(I, J, 128, 128);
-  const int64_t steps = (K + 31) / 32;
-  // split while that fills more of the card's 512 places, 8 steps a part at least
-  int64_t splits = 1;
-  while (tiles * splits * 2 <= 512 && steps / (splits * 2) >= 8 && splits < 64) splits *= 2;
-  if (splits > 1) {
-    const int64_t each = (steps + splits - 1) / splits;
-    p.part = each * 32;
-    p.splits = (int)((steps + each - 1) / each);
+  const int64_t tiles = ln_tiles(I, J, 128, 128), steps = (K + 31) / 32;
+  for (int64_t s = 1; s <= 64 && (s == 1 || (tiles * s <= 256 && steps / s >= 4)); ++s) {
+    const int64_t each = (steps + s - 1) / s, n = tiles * s;
+    const int64_t ns = each * (n > 192 ? n * 5 / 4 : 240) + (s > 1 ? 4000 + s * I * J / 600 : 0);
+    if (s == 1 || ns < p.ns) {
+      p.ns = ns;
+      p.part = each * 32;
+      p.splits = (int)((steps + each - 1) / each);
+    }
   }
   return p;
 }
@@ -596,21 +679,24 @@ size_t ln_partial_bytes(const LnPlan &p, int64_t I, int64_t J) {
   return p.splits > 1 ? (size_t)p.splits * I * J * 4 : 0;
 }
 
-template <int KIND, int TM, int TN>
+template <int KIND, int TM, int TN, int NS>
 hipError_t ln_launch_tile(const LnTile &t, const LnEpi &e, int splits, hipStream_t st) {
-  hipLaunchKernelGGL((k_linear<KIND, TM, TN>), dim3((unsigned)((int64_t)t.mt * t.nt * splits)),
-                     dim3(256), 0, st, t, e);
+  hipLaunchKernelGGL((k_linear<KIND, TM, TN, NS>),
+                     dim3((unsigned)((int64_t)t.mt * t.nt * splits)), dim3(256), 0, st, t, e);
   return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t ln_product(const uint16_t *a, int64_t lda, const uint16_t *b, int64_t ldb, int64_t I,
                       int64_t J, int64_t K, const LnEpi &e, float *ws, hipStream_t st) {
-  const LnPlan p = ln_plan(KIND, I, J, K);
+  const LnPlan p = ln_plan(I, J, K);
   const LnTile t = {a, b, lda, ldb, I, J, K, p.part, (int)((I + p.tm - 1) / p.tm),
                     (int)((J + p.tn - 1) / p.tn), p.splits > 1 ? ws : nullptr};
-  const hipError_t r = p.tm == 256 ? ln_launch_tile<KIND, 256, 256>(t, e, p.splits, st)
-                                   : ln_launch_tile<KIND, 128, 128>(t, e, p.splits, st);
+  // Up to one workgroup a CU: eight steps in flight; more: four, two workgroups a CU.
+  const bool deep = (int64_t)t.mt * t.nt * p.splits <= 256;
+  const hipError_t r = p.tm == 256 ? ln_launch_tile<KIND, 256, 256, 4>(t, e, p.splits, st)
+                       : deep      ? ln_launch_tile<KIND, 128, 128, 8>(t, e, p.splits, st)
+                                   : ln_launch_tile<KIND, 128, 128, 4>(t, e, p.splits, st);
   if (r != hipSuccess || p.splits == 1) return r;
   const int64_t groups = I * ((J + 7) / 8);
   const unsigned grid = (unsigned)(groups > 256 * 4096 ? 4096 : (groups + 255) / 256);
@@ -618,16 +704,38 @@ hipError_t ln_product(const uint16_t *a, int64_t lda, const uint16_t *b, int64_t
   return hipGetLastError();
 }
 
+template <int MT, int NT>
+hipError_t ln_launch_few(const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t M, int64_t N,
+                         int64_t K, const LnEpi &e, hipStream_t st) {
+  const int64_t tiles = (N + 16 * NT - 1) / (16 * NT), steps = (K + 31) / 32;
+  int ks = 1;
+  while (ks < 8 && tiles * ks < 4096 && steps / (2 * ks) >= 4) ks *= 2;
+  const dim3 grid((unsigned)((tiles + 8 / ks - 1) / (8 / ks)), (unsigned)((M + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((k_linear_few<MT, NT>), grid, dim3(512), 0, st, x, ldx, w, M, K, ks, e);
+  return hipGetLastError();
+}
+
+// Whether rows straight from memory are the faster way: up to LN_FEW rows always
+// (64 rows to 2048 outputs of 2048: 10.3 us, 16 in tiles), and while 16 x 16 outputs a
+// wave, each with its operands from the L2, cost less than tiles (256 rows to 128
+// outputs of 2048: 6.5 us, 10 in tiles; 512 rows to 512 of 2048: 17.6, 13.2).
+bool ln_is_few(int64_t M, int64_t N, int64_t K) {
+  if (M <= LN_FEW) return true;
+  const int64_t units = ((M + 15) / 16) * ((N + 15) / 16);
+  if (units > (1 << 16)) return false;
+  const LnPlan p = ln_plan(M, N, K);
+  return p.tm == 128 && units * K / 160 < 2000 + p.ns;
+}
+
+// Few tiles of W: each 16 rows of x are a workgroup's own, since W comes from the L2
+// a second time for less than x takes through one CU.  Many: x's tiles share W, and
+// W's tiles share x in pairs.
 hipError_t ln_few(const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t M, int64_t N,
                   int64_t K, const LnEpi &e, hipStream_t st) {
-  const int64_t tiles = (N + 15) / 16, steps = (K + 31) / 32;
-  int ks = 1;
-  while (ks < 4 && tiles * ks < 2048 && steps / (2 * ks) >= 4) ks *= 2;
-  const dim3 grid((unsigned)((tiles + 4 / ks - 1) / (4 / ks)));
-  const auto kernel = M <= 16 ? k_linear_few<1> : M <= 32 ? k_linear_few<2>
-                      : M <= 48 ? k_linear_few<3> : k_linear_few<4>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, x, ldx, w, M, K, ks, e);
-  return hipGetLastError();
+  if (M <= 16 || M > LN_FEW || N < LN_SHARE) return ln_launch_few<1, 1>(x, ldx, w, M, N, K, e, st);
+  if (M <= 32) return ln_launch_few<2, 2>(x, ldx, w, M, N, K, e, st);
+  if (M <= 48) return ln_launch_few<3, 2>(x, ldx, w, M, N, K, e, st);
+  return ln_launch_few<4, 2>(x, ldx, w, M, N, K, e, st);
 }
 
 bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -640,12 +748,12 @@ bool ln_sizes(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t ln_forward_bytes(int64_t M, int64_t N, int64_t K) {
-  return M <= LN_FEW ? 0 : ln_partial_bytes(ln_plan(LN_NT, M, N, K), M, N);
+  return ln_is_few(M, N, K) ? 0 : ln_partial_bytes(ln_plan(M, N, K), M, N);
 }
 
 size_t ln_backward_bytes(int64_t M, int64_t N, int64_t K) {
-  const size_t a = ln_partial_bytes(ln_plan(LN_NN, M, K, N), M, K);
-  const size_t b = ln_partial_bytes(ln_plan(LN_TN, N, K, M), N, K);
+  const size_t a = ln_partial_bytes(ln_plan(M, K, N), M, K);
+  const size_t b = ln_partial_bytes(ln_plan(N, K, M), N, K);
   const size_t c = (size_t)((M + LZ_ROWS - 1) / LZ_ROWS) * N * 4;
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
@@ -688,7 +796,7 @@ pqm_status pqm_linear(const uint16_t *x, int64_t ldx, const uint16_t *w, const f
   }
   const int vec = N % 8 == 0 && (!residual || (al(residual, 16) && ldr % 8 == 0));
   const LnEpi e = {bias, residual, ldr, y, z, N, act, y_dtype == PQM_OUT_FP32, vec};
-  return st_of(M <= LN_FEW ? ln_few(x, ldx, w, M, N, K, e, stream)
+  return st_of(ln_is_few(M, N, K) ? ln_few(x, ldx, w, M, N, K, e, stream)
                            : ln_product<LN_NT>(x, ldx, w, K, M, N, K, e,
                                                static_cast<float *>(workspace), stream));
 }
@@ -731,8 +839,10 @@ pqm_status pqm_linear_backward(const uint16_t *dy, int64_t lddy, const uint16_t 
   float *ws = static_cast<float *>(workspace);
   if (act != PQM_ACT_NONE || dbias) {
     const unsigned parts = (unsigned)((M + LZ_ROWS - 1) / LZ_ROWS);
-    hipLaunchKernelGGL(k_linear_dz, dim3(parts, (unsigned)((N + 511) / 512)), dim3(256), 0, stream,
-                       dy, lddy, z, act, M, N, dz, dbias ? ws : nullptr);
+    const int ct = N > 256 ? 64 : N > 128 ? 32 : 16;
+    const auto kernel = ct == 64 ? k_linear_dz<64> : ct == 32 ? k_linear_dz<32> : k_linear_dz<16>;
+    hipLaunchKernelGGL(kernel, dim3(parts, (unsigned)((N + 8 * ct - 1) / (8 * ct))), dim3(256), 0,
+                       stream, dy, lddy, z, act, M, N, dz, dbias ? ws : nullptr);
     if (hipGetLastError() != hipSuccess) return PQM_ERR_HIP;
     if (dbias) {
       hipLaunchKernelGGL(k_linear_colsum, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, ws,
