@@ -145,10 +145,9 @@ __device__ __forceinline__ tl_key tl_make(float x, int64_t i) {
 // The n best keys so far, in order.
 struct TlTop {
   tl_key kept[TL_TOP];
-  tl_key best[256];
-  tl_key cand[TL_TOP + 8 * TL_TOP];
+  tl_key bar[4];
+  __align__(16) tl_key cand[TL_TOP + 4 * 8 * TL_TOP + 8];
   int count;
-  tl_key bar;
 };
 
 __device__ __forceinline__ void tl_top_init(TlTop &s) {
@@ -156,32 +155,35 @@ __device__ __forceinline__ void tl_top_init(TlTop &s) {
   __syncthreads();
 }
 
-// Takes in eight keys a thread.  At most n threads hold one of the n best among
-// the threads' own best; keys below the n-th of those best cannot be among the n
-// best of all, so no more than 8 n candidates are left however the logits are
-// ordered, and ranking them by counting stays cheap.
+// Takes in eight keys a thread.  With b the n-th of the lanes' own best in a wave, at
+// least n keys are not below b, so none below the largest of the waves' b is among the
+// n best; and no wave has more than n lanes whose best reaches it, so no more than 32 n
+// candidates are left however the logits are ordered (n and a few as a rule), and
+// ranking them by counting stays cheap.
 __device__ __forceinline__ void tl_top_add(TlTop &s, const tl_key (&k)[8], int n) {
+  const int wave = threadIdx.x >> 6;
   tl_key top = k[0];
 #pragma unroll
   for (int j = 1; j < 8; ++j) top = k[j] > top ? k[j] : top;
   const tl_key last = s.kept[n - 1];
-  const int hits = __syncthreads_count(top > last);
-  if (hits == 0) return;
-  if (threadIdx.x < n) s.cand[threadIdx.x] = s.kept[threadIdx.x];
-  s.best[threadIdx.x] = top;
-  if (threadIdx.x == 0) {
-    s.count = n;
-    s.bar = last + 1;
+  if (__syncthreads_count(top > last) == 0) return;
+  int above = 0;
+#pragma unroll 16
+  for (int i = 0; i < 64; ++i) {
+    const tl_key o = (tl_key)(uint32_t)__builtin_amdgcn_readlane((int)(top >> 32), i) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)top, i);
+    above += o > top ? 1 : 0;
   }
+  const uint64_t at = __ballot(above == n - 1 && top > last);  // keys differ: one lane, or none
+  if ((threadIdx.x & 63) == 0) s.bar[wave] = last + 1;
+  if (at >> (threadIdx.x & 63) & 1) s.bar[wave] = top;
+  for (int i = threadIdx.x; i < (int)(sizeof(s.cand) / sizeof(tl_key)); i += 256)
+    s.cand[i] = i < n ? s.kept[i] : 0;
+  if (threadIdx.x == 0) s.count = n;
   __syncthreads();
-  if (hits > n) {
-    int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < 256; ++i) above += s.best[i] > top ? 1 : 0;
-    if (above == n - 1 && top > last) s.bar = top;  // keys differ: one thread
-    __syncthreads();
-  }
-  const tl_key bar = s.bar;
+  tl_key bar = s.bar[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) bar = s.bar[w] > bar ? s.bar[w] : bar;
   if (top >= bar) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -191,9 +193,16 @@ __device__ __forceinline__ void tl_top_add(TlTop &s, const tl_key (&k)[8], int n
   const int count = s.count;
   for (int i = threadIdx.x; i < count; i += 256) {
     const tl_key mine = s.cand[i];
-    int above = 0;
-    for (int j = 0; j < count; ++j) above += s.cand[j] > mine ? 1 : 0;
-    if (above < n && mine != 0) s.kept[above] = mine;
+    int better = 0;
+    for (int j = 0; j < count; j += 8) {  // zeros behind the last
+      const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(s.cand + j);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const ulonglong2 v = p[q];
+        better += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0);
+      }
+    }
+    if (better < n && mine != 0) s.kept[better] = mine;
   }
   __syncthreads();
 }
