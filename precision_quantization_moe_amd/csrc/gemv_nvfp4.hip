@@ -31,6 +31,7 @@ struct GemvArgs {
   int64_t N, K;  // N: output columns; ACT weights have 2 N rows
   const float *prob;
   void *out;
+  int GW;  // experts with weights; those from it on have the last one's
   int byrow;  // blockIdx.y is a row of ids and stands for its expert if no earlier row chose it;
               // otherwise it is the expert, and G the rows without one
 };
@@ -127,7 +128,8 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
   const int cols = (int)min((int64_t)COLS, a.N - n0);
   const int K = (int)a.K, chunks = (K + 255) / 256;
   // The tile's weight rows as buffers: what lies past their end reads as 0.
-  const int64_t r0 = (int64_t)(e < 0 ? 0 : e) * NW + n0 + (t ? (ACT ? a.N : 16) : 0);
+  const int ew = min(e, a.GW - 1);
+  const int64_t r0 = (int64_t)(e < 0 ? 0 : ew) * NW + n0 + (t ? (ACT ? a.N : 16) : 0);
   const int rows = ACT ? cols : max(0, min(16, cols - 16 * t));
   const __amdgpu_buffer_rsrc_t wq = gv_buffer(a.w + r0 * (K / 2), (int64_t)rows * (K / 2));
   const __amdgpu_buffer_rsrc_t ws = gv_buffer(a.ws + r0 * (K / 16), (int64_t)rows * (K / 16));
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
   GdChunk b;
   const bool early = a.byrow && e >= 0;
   load(b, early ? kw : chunks);
-  const float one = e >= 0 && a.rps == NW ? a.wo[e] : 0.0f;
+  const float one = e >= 0 && a.rps == NW ? a.wo[ew] : 0.0f;
   const int c = gv_rows<2 * KS>(a, ids, id, e, list, cnt);
   if (c == 0) return;
   if (e < 0) return gv_zero<OUTF32>(a, list, c, n0, cols);
@@ -196,12 +198,12 @@ __global__ __launch_bounds__(512, 4) void k_gemv_direct(GemvArgs a,
         float v = red[0][wave][lane][i];
 #pragma unroll
         for (int w = 1; w < KS; ++w) v += red[w][wave][lane][i];
-        v *= a.rps == NW ? one : gv_outer(a, e, NW, n);
+        v *= a.rps == NW ? one : gv_outer(a, ew, NW, n);
         if constexpr (ACT) {
           float u = red[0][1][lane][i];
 #pragma unroll
           for (int w = 1; w < KS; ++w) u += red[w][1][lane][i];
-          u *= a.rps == NW ? one : gv_outer(a, e, NW, a.N + n);
+          u *= a.rps == NW ? one : gv_outer(a, ew, NW, a.N + n);
           v = swiglu_f32(v, u, pr);
         }
         gv_store<OUTF32>(a, (int64_t)row * a.N + n, v);
@@ -276,7 +278,8 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
   const int K = (int)a.K, chunks = (K + 255) / 256, blocks = (K + GS_KB - 1) / GS_KB;
   // The workgroup's weight rows as buffers: what lies past their end reads as
   // 0; past the end of one row, x and the scales are made 0 at their use.
-  const int64_t r0 = (int64_t)e * NW + n0;
+  const int ew = min(e, a.GW - 1);
+  const int64_t r0 = (int64_t)ew * NW + n0;
   const __amdgpu_buffer_rsrc_t wq = gv_buffer(a.w + r0 * (K / 2), (int64_t)cols * (K / 2));
   const __amdgpu_buffer_rsrc_t ws = gv_buffer(a.ws + r0 * (K / 16), (int64_t)cols * (K / 16));
   const int64_t r1 = ACT ? r0 + a.N : r0;
@@ -448,9 +451,9 @@ __global__ __launch_bounds__(256, 3) void k_gemv_staged(GemvArgs a,
         for (int i = 0; i < 4; ++i) {
           const int64_t n = n0 + 16 * (uw * OT + t) + 4 * g + i;
           if (n >= a.N) break;
-          float v = acc[t][i] * back * gv_outer(a, e, NW, n);
+          float v = acc[t][i] * back * gv_outer(a, ew, NW, n);
           if constexpr (ACT) {
-            const float u = acc[t + OT][i] * back * gv_outer(a, e, NW, a.N + n);
+            const float u = acc[t + OT][i] * back * gv_outer(a, ew, NW, a.N + n);
             v = swiglu_f32(v, u, a.prob[row]);
           }
           gv_store<OUTF32>(a, o + n, v);
@@ -525,10 +528,10 @@ pqm_status gemv_check(const GemvArgs &a, const int32_t *ids, int64_t rows, int64
 
 hipError_t launch_gemv_nvfp4(const uint16_t *x, const int32_t *ids, const float *prob, int64_t rows,
                              int64_t divisor, const uint8_t *w, const uint8_t *w_scale,
-                             const float *w_outer, int64_t w_rows_per_scale, int64_t G, int64_t N,
-                             int64_t K, void *out, bool out_fp32, hipStream_t st) {
+                             const float *w_outer, int64_t w_rows_per_scale, int64_t G, int64_t GW,
+                             int64_t N, int64_t K, void *out, bool out_fp32, hipStream_t st) {
   const GemvArgs a = {x, (int)rows, (int)divisor, w, w_scale, w_outer, w_rows_per_scale,
-                      (int)G, N, K, prob, out, 0};
+                      (int)G, N, K, prob, out, (int)GW, 0};
   return launch_gemv(a, ids, prob != nullptr, out_fp32, st);
 }
 
@@ -543,7 +546,7 @@ pqm_status pqm_moe_gemv_nvfp4(const uint16_t *x, const int32_t *ids, int64_t row
   using namespace pqm;
   if (out_dtype != PQM_OUT_BF16 && out_dtype != PQM_OUT_FP32) return PQM_ERR_ENUM;
   const GemvArgs a = {x, (int)rows, (int)divisor, w_q, w_scale, w_outer, w_rows_per_scale,
-                      (int)G, N, K, nullptr, out, 0};
+                      (int)G, N, K, nullptr, out, (int)G, 0};
   const pqm_status bad = gemv_check(a, ids, rows, divisor, G, N);
   if (bad != PQM_OK || rows == 0 || N == 0) return bad;
   return st_of(launch_gemv(a, ids, false, out_dtype == PQM_OUT_FP32, stream));
@@ -556,7 +559,7 @@ pqm_status pqm_moe_gemv_swiglu_nvfp4(const uint16_t *x, const int32_t *ids, cons
                                      uint16_t *d, hipStream_t stream) {
   using namespace pqm;
   const GemvArgs a = {x, (int)rows, (int)divisor, w_q, w_scale, w_outer, w_rows_per_scale,
-                      (int)G, inter, K, prob, d, 0};
+                      (int)G, inter, K, prob, d, (int)G, 0};
   const pqm_status bad = gemv_check(a, ids, rows, divisor, G, 2 * inter);
   if (bad != PQM_OK || rows == 0 || inter == 0) return bad;
   if (!prob) return PQM_ERR_NULL;

@@ -22,9 +22,10 @@ namespace pqm {
 namespace {
 
 constexpr int DC_TOKENS = 64, DC_EXPERTS = 1024, DC_K = 16, DC_WIDTH = 16384;
-constexpr int DC_FEW = 16;       // tokens of the one-kernel form: an expert's rows are one tile
+constexpr int DC_FEW = 8;        // tokens of the one-kernel form
 constexpr int DC_WAVES = 16;     // of a workgroup of that form, one workgroup a CU
 constexpr int DC_GRID = 256;
+static_assert(DC_FEW <= 16, "an expert's rows are one tile");
 constexpr int DC_CLASSES = 8;    // tickets and signals, a cache line each
 
 // Tokens of a workgroup of the router, whose rows are 8 KB of LDS each at NC 1.
@@ -54,7 +55,7 @@ struct DcArgs {
   uint16_t *d, *out;
   // workspace
   float *logits;        // [T][E]
-  uint16_t *y16;        // [T][H] y in scaled binary16
+  uint16_t *y16;        // [T][H] y in scaled binary16; null: the form of separate products
   float *back;          // [T] what undoes the scale
   float *partial;       // [S][T][H]
   uint32_t *count;      // [H / 16]
@@ -62,6 +63,7 @@ struct DcArgs {
   int32_t *all_ids;     // [T][c], the shared expert's among them
   float *all_prob;
   int ks, S;            // waves that share a contraction; parts of the experts
+  uint32_t tg_inv;      // 2^32 over the items of an expert, rounded up
 };
 
 __device__ __forceinline__ int dc_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -70,7 +72,7 @@ __device__ __forceinline__ int dc_uniform(int v) { return __builtin_amdgcn_readf
 
 // Norm and router: 16 experts by a few tokens a workgroup, each of which
 // normalises its tokens itself (the first column of workgroups writes h and y).
-// A wave takes every eighth 64-wide block of the contraction, its first four
+// A wave takes every eighth 64-wide block of the contraction, its first eight
 // asked for before the norm.  The order of two logits decides which experts a
 // token meets, so the matrix instructions' sums of 32 products are added up in
 // binary64: a logit is off by little more than its last rounding.
@@ -399,8 +401,7 @@ __device__ __forceinline__ void dc_load(DcChunk &b, __amdgpu_buffer_rsrc_t wq,
 // What a chunk's product takes of 16 rows, whose values start at xo (GV_NONE: no
 // row) of xb: lane group g has the chunk's values 64 g .. + 63.  No branch: the
 // loads have to stay in their order, or the waits for them would wait for the next
-// chunk's weights too.  FRESH: written by other workgroups of this kernel.
-template <bool FRESH>
+// chunk's weights too.
 __device__ __forceinline__ void dc_load_x(gv_u4 (&x)[8], __amdgpu_buffer_rsrc_t xb, uint32_t xo,
                                           int K, int ch) {
   const uint32_t kk = 256 * ch + 64 * ((threadIdx.x & 63) >> 4);
@@ -408,8 +409,7 @@ __device__ __forceinline__ void dc_load_x(gv_u4 (&x)[8], __amdgpu_buffer_rsrc_t 
   const uint32_t hi = (xo + 2 * kk) | (kk + 32 < (uint32_t)K ? 0 : GV_NONE);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    x[j] = __builtin_amdgcn_raw_buffer_load_b128(xb, (int)(j < 4 ? lo : hi), 16 * j,
-                                                 FRESH ? 16 : 0);
+    x[j] = __builtin_amdgcn_raw_buffer_load_b128(xb, (int)(j < 4 ? lo : hi), 16 * j, 0);
 }
 
 // Eight weights in binary16: exact, and half the instructions of bf16.
@@ -491,8 +491,8 @@ __device__ __forceinline__ int dc_sweep(DcSync *sync, int total) {
 // workgroups that run and wait for nothing themselves: the wait ends however many
 // workgroups the card holds at once, also beside other calls.  Eight counters, since
 // one address takes 10 ns a draw: 256 workgroups draw in 2.8 us from one and in 1.1
-// from eight, and meet in 3.8 and 1.4.  d goes past the L2 (each XCD has its own),
-// and what is read of it too.
+// from eight, and meet in 3.8 and 1.4.  d goes past the L2, of which each XCD has its
+// own, and nothing of it is read before the wait.
 //
 // The down projection's items are 16 columns and a part of the experts met; its waves
 // take (expert, chunk) in turn, each with sums of its own, the first chunk's weights
@@ -535,108 +535,116 @@ __global__ __launch_bounds__(64 * DC_WAVES, 4) void k_decode_experts(DcArgs a) {
 
   const int per = DC_WAVES / a.ks, kw = wave & (a.ks - 1), tiles = a.I / 16;
   const int tg = (tiles + per - 1) / per, total = met.n * tg;
-  int finished = 0;
   {
     const int K = a.H, chunks = (K + 255) / 256;
     const __amdgpu_buffer_rsrc_t xb = gv_buffer(a.y16, (int64_t)a.T * K * 2);
     if (tid == 0) drawn[1] = dc_drawn(ticket, cls, total);
     __syncthreads();
-    int item = dc_uniform(drawn[1]), buf = 0;
-    for (;;) {
-      if (item < 0) {
-        // Its class is at an end: every wave's part of d has to arrive before the
-        // workgroup says so, and what is left of other classes is taken.
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (tid == 0 && finished)
-          __hip_atomic_fetch_add(&a.sync->of[cls].done, (uint32_t)finished, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
-        finished = 0;
-        if (wave == 0) {
-          const int t = dc_sweep(a.sync, total);
-          if (lane == 0) drawn[buf ^ 1] = t;
-        }
-        __syncthreads();
-        item = dc_uniform(drawn[buf ^ 1]);
-        if (item < 0) break;
-      }
-      const int i = item / tg, tile = (item - i * tg) * per + wave / a.ks;
-      const int e = met(a, i);
+    // the item, its expert and that one's rows, and this wave's tile of it
+    int item = dc_uniform(drawn[1]), buf = 0, finished = 0, ch = kw, e = 0, first = 0, tok = 0;
+    bool row = false;
+    float outer = 0.0f, back = 0.0f;
+    const auto open = [&]() {
+      const int i = tg == 1 ? item : (int)__umulhi((uint32_t)item, a.tg_inv);  // item / tg
+      first = (item - i * tg) * per;
+      e = met(a, i);
       const uint32_t rows = dc_rows(a, s, e);
-      const bool live = tile < tiles;
-      const int64_t r0 = (int64_t)e * 2 * a.I + (live ? 16 * tile : 0), r1 = r0 + a.I;
-      const int64_t n = live ? 16 : 0;
-      const __amdgpu_buffer_rsrc_t gq = gv_buffer(a.w1 + r0 * (K / 2), n * (K / 2)),
-                                   gs = gv_buffer(a.s1 + r0 * (K / 16), n * (K / 16)),
-                                   uq = gv_buffer(a.w1 + r1 * (K / 2), n * (K / 2)),
-                                   us = gv_buffer(a.s1 + r1 * (K / 16), n * (K / 16));
-      const auto load = [&](DcChunk (&b)[2], int ch) {
-        dc_load<WORDS1>(b[0], gq, gs, K, ch, ch < chunks);
-        dc_load<WORDS1>(b[1], uq, us, K, ch, ch < chunks);
-      };
-      DcChunk b0[2], b1[2];
-      load(b0, kw);
-      const int tok = dc_member(rows);
-      const bool row = ln < __popc(rows);
-      const uint32_t xo = row ? (uint32_t)tok * K * 2 : GV_NONE;
-      gv_f4 acc[2] = {};
-      // The next chunk's weights go out behind this one's rows, so that the wait for
-      // the rows leaves them in flight; two sets of registers, since a copy would wait.
-      const auto turn_of = [&](const DcChunk (&b)[2], DcChunk (&next)[2], int ch) {
-        gv_u4 x[8];
-        dc_load_x<false>(x, xb, xo, K, ch);
-        __builtin_amdgcn_sched_barrier(0);
-        if (ch == kw && tid == 0) ticket = dc_draw(a.sync, cls);  // the next item's
-        load(next, ch + a.ks);
-        __builtin_amdgcn_sched_barrier(0);
-        dc_multiply<true>(acc[0], b[0], x, turn, K, ch);
-        dc_multiply<true>(acc[1], b[1], x, turn, K, ch);
-      };
-      for (int ch = kw; ch < chunks; ch += 2 * a.ks) {
-        turn_of(b0, b1, ch);
-        if (ch + a.ks >= chunks) break;
-        turn_of(b1, b0, ch + a.ks);
-      }
+      tok = dc_member(rows);
+      row = ln < __popc(rows);
+      ch = kw;
+      outer = a.g1[e];
+      back = a.back[tok & (DC_FEW - 1)];
+    };
+    const auto load = [&](DcChunk (&b)[2], int ch) {
+      const int tile = first + wave / a.ks;
+      const bool in = tile < tiles && ch < chunks;
+      const int64_t r0 = (int64_t)e * 2 * a.I + (tile < tiles ? 16 * tile : 0), r1 = r0 + a.I;
+      dc_load<WORDS1>(b[0], gv_buffer(a.w1 + r0 * (K / 2), 8 * (int64_t)K),
+                      gv_buffer(a.s1 + r0 * (K / 16), (int64_t)K), K, ch, in);
+      dc_load<WORDS1>(b[1], gv_buffer(a.w1 + r1 * (K / 2), 8 * (int64_t)K),
+                      gv_buffer(a.s1 + r1 * (K / 16), (int64_t)K), K, ch, in);
+    };
+    gv_f4 acc[2] = {};
+    // A chunk, whose weights are in b; the next one's go out behind this one's rows, so
+    // that the wait for the rows leaves them in flight.  Two sets of registers in turn,
+    // since a copy would wait, and no more than two copies of this code: what runs once
+    // waits for its own instructions.  False: no item is left anywhere.
+    const auto step = [&](const DcChunk (&b)[2], DcChunk (&next)[2]) {
+      gv_u4 x[8];
+      dc_load_x(x, xb, row ? (uint32_t)tok * K * 2 : GV_NONE, K, ch);
+      __builtin_amdgcn_sched_barrier(0);
+      if (ch == kw && tid == 0) ticket = dc_draw(a.sync, cls);
+      load(next, ch + a.ks);
+      __builtin_amdgcn_sched_barrier(0);
+      dc_multiply<true>(acc[0], b[0], x, turn, K, ch);
+      dc_multiply<true>(acc[1], b[1], x, turn, K, ch);
+      ch += a.ks;
+      if (ch < chunks) return true;
       red[buf][wave][0][lane] = acc[0];
       red[buf][wave][1][lane] = acc[1];
+      acc[0] = acc[1] = gv_f4{0, 0, 0, 0};
       if (tid == 0) drawn[buf] = dc_drawn(ticket, cls, total);
       // tile t of the item is wave t's to finish
-      const int mine = (item - i * tg) * per + wave;
+      const int mine = first + wave, at = tok, j = dc_slot(a, s, tok, e);
       const bool ends = wave < per && mine < tiles && row;
-      float outer = 0.0f, back = 0.0f, p = 1.0f;
-      int j = 0;
-      if (ends) {
-        outer = a.g1[e];
-        back = a.back[tok];
-        j = dc_slot(a, s, tok, e);
-        if (j < a.k) p = prob[tok * a.k + j];
-      }
+      const float out1 = outer, undo = back;
+      float p = 1.0f;
+      if (ends && j < a.k) p = prob[tok * a.k + j];
       __syncthreads();
-      const int next = dc_uniform(drawn[buf]);
+      item = dc_uniform(drawn[buf]);
+      const int was = buf;
+      buf ^= 1;
+      ++finished;
+      if (item >= 0) {
+        open();
+        load(next, ch);
+      }
       if (ends) {
-        gv_f4 vg = red[buf][wave * a.ks][0][lane], vu = red[buf][wave * a.ks][1][lane];
+        gv_f4 vg = red[was][wave * a.ks][0][lane], vu = red[was][wave * a.ks][1][lane];
         for (int q = 1; q < a.ks; ++q) {
-          vg += red[buf][wave * a.ks + q][0][lane];
-          vu += red[buf][wave * a.ks + q][1][lane];
+          vg += red[was][wave * a.ks + q][0][lane];
+          vu += red[was][wave * a.ks + q][1][lane];
         }
         float o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = swiglu_f32(vg[q] * back * outer, vu[q] * back * outer, p);
+        for (int q = 0; q < 4; ++q) o[q] = swiglu_f32(vg[q] * undo * out1, vu[q] * undo * out1, p);
         __hip_atomic_store(
-            reinterpret_cast<uint64_t *>(a.d + (int64_t)(tok * a.c + j) * a.I + 16 * mine + 4 * g),
+            reinterpret_cast<uint64_t *>(a.d + (int64_t)(at * a.c + j) * a.I + 16 * mine + 4 * g),
             (uint64_t)pk_bf16_rne(o[2], o[3]) << 32 | pk_bf16_rne(o[0], o[1]), __ATOMIC_RELAXED,
             __HIP_MEMORY_SCOPE_AGENT);
       }
-      ++finished;
-      item = next;
-      buf ^= 1;
+      return item >= 0;
+    };
+    for (;;) {
+      if (item >= 0) {
+        open();
+        DcChunk b0[2], b1[2];
+        load(b0, ch);
+        while (step(b0, b1) && step(b1, b0)) {
+        }
+      }
+      // Its class is at an end: every wave's part of d has to arrive before the
+      // workgroup says so, and what is left of other classes is taken.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (tid == 0 && finished)
+        __hip_atomic_fetch_add(&a.sync->of[cls].done, (uint32_t)finished, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+      finished = 0;
+      if (wave == 0) {
+        const int t = dc_sweep(a.sync, total);
+        if (lane == 0) drawn[buf ^ 1] = t;
+      }
+      __syncthreads();
+      item = dc_uniform(drawn[buf ^ 1]);
+      if (item < 0) break;
     }
   }
 
   const int K = a.I, chunks = (K + 255) / 256, NT = a.H / 16;
   const __amdgpu_buffer_rsrc_t xb = gv_buffer(a.d, (int64_t)a.T * a.c * K * 2);
   bool waited = false;
-  for (int item = blockIdx.x; item < NT * a.S; item += gridDim.x) {
+  for (int item = blockIdx.x; item < NT * a.S; item += DC_GRID) {
     const int part = item / NT, tile = item - part * NT;
     const int i0 = met.n * part / a.S, i1 = met.n * (part + 1) / a.S, units = (i1 - i0) * chunks;
     // a chunk of an expert: its weights, and where the rows' values start
@@ -675,15 +683,17 @@ __global__ __launch_bounds__(64 * DC_WAVES, 4) void k_decode_experts(DcArgs a) {
 #pragma unroll
           for (int q = 0; q < DC_CLASSES; ++q) n += __builtin_amdgcn_readlane((int)v, q);
           if (n == total) break;
-          __builtin_amdgcn_s_sleep(4);
+          __builtin_amdgcn_s_sleep(2);
         }
+        // for the whole CU: nothing of d that was cached before is read
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       }
       __syncthreads();
       waited = true;
     }
     const auto turn_of = [&](const Unit &t, Unit &next, int u) {
       gv_u4 x[8];
-      dc_load_x<true>(x, xb, t.xo, K, t.ch);
+      dc_load_x(x, xb, t.xo, K, t.ch);
       __builtin_amdgcn_sched_barrier(0);
       load(next, u + DC_WAVES);
       __builtin_amdgcn_sched_barrier(0);
@@ -753,7 +763,8 @@ __global__ __launch_bounds__(256) void k_decode_gate(DcArgs a) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (lane < a.c) {
     const bool routed = lane < a.k;
-    const int32_t id = routed ? ids[wave * a.k + lane] : a.E;
+    // the shared expert's rows in groups of 16, each an expert to the products
+    const int32_t id = routed ? ids[wave * a.k + lane] : a.E + t / 16;
     const float p = routed ? prob[wave * a.k + lane] : 1.0f;
     a.all_ids[t * a.c + lane] = id;
     a.all_prob[t * a.c + lane] = p;
@@ -808,6 +819,16 @@ DcPlan dc_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int shared
   return p;
 }
 
+// One kernel up to DC_FEW tokens whose experts hold up to 96 MB: 128 experts of
+// 2048 x 768, top-8, 24.3 us for one token and 36.3 for three (26.3 and 38.4 by
+// separate products), 16 of 4096 x 1024, top-2, 42.9 for eight (46.4).  Beyond, the
+// separate products stream the weights faster: 64 experts of 5120 x 1280, top-8, three
+// tokens 69.8 us against 92.5, 16 tokens 145 against 186.
+bool dc_is_few(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int shared) {
+  const int64_t met = (T * k < E ? T * k : E) + shared;
+  return T <= DC_FEW && met * H * I / 16 * 27 <= (int64_t)96 << 20;
+}
+
 bool dc_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
   return T >= 0 && T <= DC_TOKENS && H >= 32 && H <= DC_WIDTH && H % 32 == 0 && I >= 32 &&
          I <= DC_WIDTH && I % 32 == 0 && E >= 1 && E <= DC_EXPERTS && k >= 1 && k <= DC_K && k <= E;
@@ -826,7 +847,7 @@ DcLayout dc_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int sh
     at += (size_t)(n + 255) / 256 * 256;
     return r;
   };
-  const bool few = T <= DC_FEW;
+  const bool few = dc_is_few(T, H, I, E, k, shared);
   const int64_t rows = T * (k + shared);
   take(T * E * 4);
   l.y16 = take(few ? T * H * 2 : 0);
@@ -867,12 +888,13 @@ hipError_t dc_many(const DcArgs &a, float *rows, hipStream_t st) {
   hipLaunchKernelGGL(k_decode_gate<VPL>, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, st, a);
   hipError_t r = hipGetLastError();
   if (r != hipSuccess) return r;
-  const int64_t n = (int64_t)a.T * a.c, G = a.E + (a.c - a.k);
-  r = launch_gemv_nvfp4(a.y, a.all_ids, a.all_prob, n, a.c, a.w1, a.s1, a.g1, 2 * a.I, G, a.I, a.H,
-                        a.d, false, st);
+  const int64_t n = (int64_t)a.T * a.c, GW = a.E + (a.c - a.k);
+  const int64_t G = a.c > a.k ? a.E + (a.T + 15) / 16 : a.E;
+  r = launch_gemv_nvfp4(a.y, a.all_ids, a.all_prob, n, a.c, a.w1, a.s1, a.g1, 2 * a.I, G, GW, a.I,
+                        a.H, a.d, false, st);
   if (r != hipSuccess) return r;
-  r = launch_gemv_nvfp4(a.d, a.all_ids, nullptr, n, 1, a.w2, a.s2, a.g2, a.H, G, a.H, a.I, rows,
-                        true, st);
+  r = launch_gemv_nvfp4(a.d, a.all_ids, nullptr, n, 1, a.w2, a.s2, a.g2, a.H, G, GW, a.H, a.I,
+                        rows, true, st);
   if (r != hipSuccess) return r;
   hipLaunchKernelGGL(k_decode_sum, dim3((unsigned)((a.T * a.H / 4 + 255) / 256)), dim3(256), 0, st,
                      rows, a.T, a.c, a.H, a.out);
@@ -881,7 +903,7 @@ hipError_t dc_many(const DcArgs &a, float *rows, hipStream_t st) {
 
 template <int VPL>
 hipError_t dc_experts(const DcArgs &a, float *rows, hipStream_t st) {
-  return a.T <= DC_FEW ? dc_few<VPL>(a, st) : dc_many<VPL>(a, rows, st);
+  return a.y16 ? dc_few<VPL>(a, st) : dc_many<VPL>(a, rows, st);
 }
 
 }  // namespace
@@ -926,17 +948,21 @@ pqm_status pqm_moe_decode_nvfp4(const uint16_t *x, const uint16_t *residual, con
   if (workspace_bytes < l.bytes) return PQM_ERR_WORKSPACE;
   const DcPlan p = dc_plan(tokens, hidden, inter, num_experts, k, shared_expert);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const bool few = dc_is_few(tokens, hidden, inter, num_experts, k, shared_expert);
+  // item / tg is exact for items up to 2^21 and tg from 2 to 2^10
+  const int64_t per = DC_WAVES / p.ks, tg = (inter / 16 + per - 1) / per;
+  const uint32_t tg_inv = tg == 1 ? 0 : (uint32_t)((((int64_t)1 << 32) + tg - 1) / tg);
   const DcArgs a = {x, residual, norm_w, eps, gate_w, (int)tokens, (int)hidden, (int)inter,
                     (int)num_experts, (int)k, (int)k + shared_expert, score == PQM_SCORE_SOFTMAX,
                     renormalize, scale, w1_q, w1_scale, w1_outer, w2_q, w2_scale, w2_outer, h, y,
                     topk_ids, prob, d, out, reinterpret_cast<float *>(ws),
-                    tokens <= DC_FEW ? reinterpret_cast<uint16_t *>(ws + l.y16) : nullptr,
+                    few ? reinterpret_cast<uint16_t *>(ws + l.y16) : nullptr,
                     reinterpret_cast<float *>(ws + l.back),
                     reinterpret_cast<float *>(ws + l.partial),
                     reinterpret_cast<uint32_t *>(ws + l.count),
                     reinterpret_cast<DcSync *>(ws + l.sync),
                     reinterpret_cast<int32_t *>(ws + l.ids),
-                    reinterpret_cast<float *>(ws + l.prob), p.ks, p.S};
+                    reinterpret_cast<float *>(ws + l.prob), p.ks, p.S, tg_inv};
   const bool wf32 = norm_dtype == PQM_OUT_FP32;
   if (hidden <= 4096) dc_router<1>(a, wf32, stream);
   else if (hidden <= 8192) dc_router<2>(a, wf32, stream);

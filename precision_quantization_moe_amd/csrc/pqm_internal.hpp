@@ -66,11 +66,12 @@ hipError_t launch_fc2_online_nvfp4_split(const uint16_t *p, const uint8_t *b,
                                          int out_fp32, float *gs, uint8_t *q, uint8_t *sb,
                                          float *ratio, hipStream_t st);
 // The few-row products of checked arguments: rows of ids by weights [G, N or 2 N
-// (prob given: SwiGLU), K]; out bf16 or binary32.
+// (prob given: SwiGLU), K]; out bf16 or binary32.  Experts from GW on have the weights
+// of GW - 1: its rows in groups, which different workgroups take.
 hipError_t launch_gemv_nvfp4(const uint16_t *x, const int32_t *ids, const float *prob, int64_t rows,
                              int64_t divisor, const uint8_t *w, const uint8_t *w_scale,
-                             const float *w_outer, int64_t w_rows_per_scale, int64_t G, int64_t N,
-                             int64_t K, void *out, bool out_fp32, hipStream_t st);
+                             const float *w_outer, int64_t w_rows_per_scale, int64_t G, int64_t GW,
+                             int64_t N, int64_t K, void *out, bool out_fp32, hipStream_t st);
 hipError_t launch_validate_offsets(const int64_t *off, int64_t G, int64_t M_total, int64_t align,
                                    int32_t *result, hipStream_t st);
 
