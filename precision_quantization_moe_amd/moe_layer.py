@@ -187,16 +187,28 @@ def _of_experts(E: int, name: str, w, size: int):
                          f"{w.numel()} (no shared expert here)")
 
 
-def _router_logits(y, gate_w, off):
+ROUTERS = ("grouped", "linear")
+
+
+def _linear_router(router: str) -> bool:
+    if router not in ROUTERS:
+        raise ValueError(f"router: expected one of {ROUTERS}, got {router!r}")
+    return router == "linear"
+
+
+def _router_logits(y, gate_w, off, router="grouped"):
     """y [T, H] times the router's weight [E, H], both bf16, in binary32."""
     E, H = gate_w.shape
+    if _linear_router(router):
+        return b.linear(y, gate_w, out_dtype=b.OUT_FP32)[0]
     return b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_FPROP, y, gate_w, off, E, H,
                               out_dtype=b.OUT_FP32)
 
 
 def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, k: int,
                      inter: int, plan=None, score: int = b.SCORE_SOFTMAX,
-                     renormalize: bool = True, scale: float = 1.0, eps: float = 1e-6):
+                     renormalize: bool = True, scale: float = 1.0, eps: float = 1e-6,
+                     fused: bool = False, shared: bool = False):
     """One decode step of an expert layer with NVFP4 weights for a few tokens
     (T * k <= 4096; up to about 16 assignments an expert, beyond which the
     grouped GEMM of nvfp4_moe_forward is faster): residual addition and RMS
@@ -207,7 +219,19 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
     quantize_expert_weights_nvfp4 returns them (routed experts alone: weights
     with a shared expert's group, as nvfp4_moe_forward takes them, are refused);
     plan from block_plan(T, k, device).  Returns dict(out [T, H] bf16, h (the new
-    residual stream), y, ids, prob, d)."""
+    residual stream), y, ids, prob, d).
+    fused takes the whole step, for up to 64 tokens, in one call
+    (moe_decode_nvfp4: logits that keep close experts apart, a binary32 sum of
+    the experts' rows where this one rounds each to bf16; no plan); with it,
+    `shared` says that the weights hold a shared expert behind the routed ones,
+    and d its rows behind each token's."""
+    if fused:
+        out, h, y, ids, prob, d = b.moe_decode_nvfp4(
+            x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, k, inter, shared, score,
+            renormalize, scale, eps)
+        return dict(out=out, h=h, y=y, ids=ids, prob=prob, d=d)
+    if shared:
+        raise ValueError("shared: taken by the fused step alone")
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
     E = _router(gate_w, H, x.device)
@@ -225,15 +249,18 @@ def nvfp4_moe_decode(x, residual, norm_w, gate_w, w1q, w1b, w1g, w2q, w2b, w2g, 
 def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: int, inter: int,
                             loss_coef: float = 0.01, mask=None, plan=None,
                             score: int = b.SCORE_SOFTMAX, renormalize: bool = True,
-                            scale: float = 1.0, eps: float = 1e-6):
+                            scale: float = 1.0, eps: float = 1e-6, router: str = "grouped"):
     """An expert layer's training forward pass from the residual stream on:
     residual addition, RMS norm and MXFP8 encoding in one pass, router gate
     with its balance loss, then the experts of mxfp8_moe_forward.  mask [T]
     marks padding with 0: no part in the loss, no weight, no gradient to the
     gate; its x must be finite, since its rows still pass through the products.
     The weights are those of gate_w's E experts, as quantize_expert_weights_mxfp8
-    returns them.  Returns the experts' dict and h, y, rstd, logits, ids, prob,
-    counts, prob_sum, loss."""
+    returns them.  router: the entry point of the router's product, "grouped"
+    (a grouped GEMM of one group) or "linear" (a dense product, the faster one;
+    the last bits of its binary32 logits differ).  Returns the experts' dict and
+    h, y, rstd, logits, ids, prob, counts, prob_sum, loss."""
+    _linear_router(router)
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
     E = _router(gate_w, H, x.device)
@@ -243,7 +270,7 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
         if w.element_size() != 1 or w.device != x.device or not w.is_contiguous():
             raise ValueError(f"{name}: expected the experts' contiguous bytes on {x.device}")
     qx, sx, y, h, rstd = b.rmsnorm_quantize_mxfp8(x, norm_w, eps, residual=residual, keep_y=True)
-    logits = _router_logits(y, gate_w, plan["off"])
+    logits = _router_logits(y, gate_w, plan["off"], router)
     ids, prob, counts, prob_sum, loss = b.moe_gate(logits, k, score, renormalize, scale, mask,
                                                    loss_coef)
     r = _mxfp8_experts(qx, sx, ids, prob.view(-1), w1q, w1s, w2q, w2s, E, inter, True)
@@ -255,7 +282,7 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
 def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
                        loss_coef: float = 0.01, mask=None, plan=None,
                        score: int = b.SCORE_SOFTMAX, renormalize: bool = True,
-                       scale: float = 1.0):
+                       scale: float = 1.0, router: str = "grouped"):
     """The gradients of a block's gate and norm, behind the experts' own
     backward pass.  saved: what mxfp8_moe_block_forward returned; a tensor of
     other sizes or with strides is refused.
@@ -265,11 +292,14 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
       d_h [T, H] bf16    gradient of h past the norm (may be None)
     d_logits enters its two products in bf16, their operand type, and what comes
     back through the gate is rounded to bf16 before and after it joins dy, the
-    type that rmsnorm_backward takes; all sums are binary32.
+    type that rmsnorm_backward takes; all sums are binary32.  With router
+    "linear" both products are one call of linear_backward, which adds dy before
+    its only rounding.
     Returns dict(dx [T, H] bf16, the gradient of x and of residual; d_norm_w
     [H] f32, d_gate_w [E, H] f32, d_logits [T, E] bf16)."""
     T, H = dy.shape
     dev, bf16, k = dy.device, torch.bfloat16, saved["ids"].shape[1]
+    linear = _linear_router(router)
     E = _router(gate_w, H, dev)
     plan = _plan(plan, T, k, dev)
     # the products and the combine take their sizes from here (ids and counts are
@@ -282,10 +312,13 @@ def moe_block_backward(saved, norm_w, gate_w, dy, d_prob, d_loss, d_h=None,
     off = plan["off"]
     dz = b.moe_gate_backward(saved["logits"], saved["ids"], d_prob, score, renormalize, scale,
                              mask, loss_coef, saved["counts"], d_loss, out_dtype=b.OUT_BF16)
-    d_gate_w = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_WGRAD, dz, saved["y"], off, E, H,
-                                  out_dtype=b.OUT_FP32)[0]
-    through_gate = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_DGRAD, dz, gate_w, off, H, E,
-                                      out_dtype=b.OUT_BF16)
-    dy = b.moe_combine(through_gate, plan["row"], shared=dy)
+    if linear:
+        dy, d_gate_w, _, _ = b.linear_backward(dz, saved["y"], gate_w, d_x=dy)
+    else:
+        d_gate_w = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_WGRAD, dz, saved["y"], off, E, H,
+                                      out_dtype=b.OUT_FP32)[0]
+        through_gate = b.moe_grouped_gemm(b.FMT_BF16, b.GEMM_DGRAD, dz, gate_w, off, H, E,
+                                          out_dtype=b.OUT_BF16)
+        dy = b.moe_combine(through_gate, plan["row"], shared=dy)
     dx, d_norm_w = b.rmsnorm_backward(dy, saved["h"], norm_w, saved["rstd"], d_sum=d_h)
     return dict(dx=dx, d_norm_w=d_norm_w, d_gate_w=d_gate_w, d_logits=dz)
