@@ -652,20 +652,28 @@ int64_t ln_tiles(int64_t I, int64_t J, int tm, int tn) {
 // Tiles and splits by size alone.
 //
 // 256 x 256 tiles from 200 of them on (8190 x 4096 x 2048: 976 TFLOP/s, 128 x 128
-// 750).  Below that 128 x 128, whose step of 32 takes 0.24 us on a CU (LDS) and,
-// from about 200 workgroups on, 1.25 ns a workgroup (the L2s give 13 TB/s); splitting
-// the contraction pays where the steps saved outweigh a launch of 4 us and the
-// partial sums' way out and back.
-LnPlan ln_plan(int64_t I, int64_t J, int64_t K) {
+// 750), unless the contraction is so short that the epilogue counts, which two
+// workgroups a CU overlap (dx of 8192 x 256 x 2048: 27.7 us, 23.6 in 128 x 128; of
+// 4096 x 128 x 7168: 37.4, 32.0).  Else 128 x 128; splitting the contraction pays where
+// the steps of 32 saved outweigh a launch of 4 us and the partial sums' way out and
+// back.  A step takes 0.24 us on a CU (LDS) and, from about 200 workgroups on, 1.25 ns
+// a workgroup (the L2s give 13 TB/s).  Where both operands are read across the
+// contraction (dW), whose rows come from memory and never again, one workgroup a CU
+// waits for them (0.5 us a step) and two hide half of that: up to 512 workgroups
+// (dW of 16384 x 256 x 2048: 60 us in 160, 42 in 512; 8192 x 512 x 2048: 55, 40).
+LnPlan ln_plan(int kind, int64_t I, int64_t J, int64_t K) {
   LnPlan p = {128, 128, 1, (K + 31) / 32 * 32, 0};
-  if (ln_tiles(I, J, 256, 256) >= 200) {
+  if (K > 256 && ln_tiles(I, J, 256, 256) >= 200) {
     p.tm = p.tn = 256;
     return p;
   }
   const int64_t tiles = ln_tiles(I, J, 128, 128), steps = (K + 31) / 32;
-  for (int64_t s = 1; s <= 64 && (s == 1 || (tiles * s <= 256 && steps / s >= 4)); ++s) {
+  const int64_t most = kind == LN_TN ? 512 : 256;
+  for (int64_t s = 1; s <= 64 && (s == 1 || (tiles * s <= most && steps / s >= 4)); ++s) {
     const int64_t each = (steps + s - 1) / s, n = tiles * s;
-    const int64_t ns = each * (n > 192 ? n * 5 / 4 : 240) + (s > 1 ? 4000 + s * I * J / 600 : 0);
+    const int64_t step = kind == LN_TN ? (n > 256 ? 650 : 500) : n > 192 ? n * 5 / 4 : 240;
+    const int64_t join = s == 1 ? 0 : 4000 + s * I * J / (kind == LN_TN ? 450 : 600);
+    const int64_t ns = each * step + join;
     if (s == 1 || ns < p.ns) {
       p.ns = ns;
       p.part = each * 32;
@@ -689,7 +697,7 @@ hipError_t ln_launch_tile(const LnTile &t, const LnEpi &e, int splits, hipStream
 template <int KIND>
 hipError_t ln_product(const uint16_t *a, int64_t lda, const uint16_t *b, int64_t ldb, int64_t I,
                       int64_t J, int64_t K, const LnEpi &e, float *ws, hipStream_t st) {
-  const LnPlan p = ln_plan(I, J, K);
+  const LnPlan p = ln_plan(KIND, I, J, K);
   const LnTile t = {a, b, lda, ldb, I, J, K, p.part, (int)((I + p.tm - 1) / p.tm),
                     (int)((J + p.tn - 1) / p.tn), p.splits > 1 ? ws : nullptr};
   // Up to one workgroup a CU: eight steps in flight; more: four, two workgroups a CU.
@@ -723,7 +731,7 @@ bool ln_is_few(int64_t M, int64_t N, int64_t K) {
   if (M <= LN_FEW) return true;
   const int64_t units = ((M + 15) / 16) * ((N + 15) / 16);
   if (units > (1 << 16)) return false;
-  const LnPlan p = ln_plan(M, N, K);
+  const LnPlan p = ln_plan(LN_NT, M, N, K);
   return p.tm == 128 && units * K / 160 < 2000 + p.ns;
 }
 
@@ -748,12 +756,12 @@ bool ln_sizes(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t ln_forward_bytes(int64_t M, int64_t N, int64_t K) {
-  return ln_is_few(M, N, K) ? 0 : ln_partial_bytes(ln_plan(M, N, K), M, N);
+  return ln_is_few(M, N, K) ? 0 : ln_partial_bytes(ln_plan(LN_NT, M, N, K), M, N);
 }
 
 size_t ln_backward_bytes(int64_t M, int64_t N, int64_t K) {
-  const size_t a = ln_partial_bytes(ln_plan(M, K, N), M, K);
-  const size_t b = ln_partial_bytes(ln_plan(N, K, M), N, K);
+  const size_t a = ln_partial_bytes(ln_plan(LN_NN, M, K, N), M, K);
+  const size_t b = ln_partial_bytes(ln_plan(LN_TN, N, K, M), N, K);
   const size_t c = (size_t)((M + LZ_ROWS - 1) / LZ_ROWS) * N * 4;
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
