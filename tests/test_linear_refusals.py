@@ -31,10 +31,10 @@ def caller(name, ok):
 def test_linear_arguments():
     # x ldx w bias act res ldr M N K y ydtype z ws bytes stream
     size = pqm.lib().pqm_linear_workspace
-    need = size(300, 128, 4096)
+    need = size(3000, 128, 4096)
     assert need > 0 and size(64, 128, 4096) == 0 and size(0, 128, 64) == 0 and size(300, 0, 64) == 0
     assert size(300, 128, 20) == 0 and size(-1, 128, 64) == 0 and size(1 << 40, 64, 64) == 0
-    c = caller("pqm_linear", [A, 4096, A, A, 0, A, 128, 300, 128, 4096, D, 0, D, A, need, None])
+    c = caller("pqm_linear", [A, 4096, A, A, 0, A, 128, 3000, 128, 4096, D, 0, D, A, need, None])
     assert c(a4=3) == 4 and c(a4=-1) == 4 and c(a11=2) == 4
     assert c(a7=-1) == 2 and c(a8=-1) == 2 and c(a9=0) == 2 and c(a9=4092) == 2
     assert c(a9=(1 << 22) + 8, a1=(1 << 22) + 8) == 2 and c(a8=(1 << 22) + 1) == 2
