@@ -215,7 +215,7 @@ struct LnSrc {
   }
   // Chunk i of the next step to LDS address m0 (the wave's).
   __device__ __forceinline__ void load(int i, uint32_t m0) const {
-    const int l = min(left, 32), bytes = ML ? (l - 1) * ld2 + rows : rows + 2 * left;
+    const int l = min(left, 32), bytes = ML ? (l - 1) * ld2 + rows : rows + 2 * min(left, 32);
     const uint32_t o = ML || piece < left ? off[i] : LN_NONE;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0,
@@ -740,9 +740,8 @@ hipError_t ln_launch_few(const uint16_t *x, int64_t ldx, const uint16_t *w, int6
 bool ln_is_few(int64_t M, int64_t N, int64_t K) {
   if (M <= LN_FEW) return true;
   const int64_t units = ((M + 15) / 16) * ((N + 15) / 16);
-  if (units > (1 << 16)) return false;
-  const LnPlan p = ln_plan(LN_NT, M, N, K);
-  return p.tm == 128 && units * K / 160 < 2000 + p.ns;
+  if (units > (1 << 16) || ln_tiles(M, N, 256, 256) >= 200) return false;
+  return units * K / 160 < 2000 + ln_plan(LN_NT, M, N, K).ns;
 }
 
 // Few tiles of W: each 16 rows of x are a workgroup's own, since W comes from the L2

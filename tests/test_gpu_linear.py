@@ -208,6 +208,20 @@ def test_backward_sizes(M, N, K):
     backward(M, N, K, pqm.ACT_GELU, True, False)
 
 
+@pytest.mark.parametrize("M,N,K", [(3600, 4100, 264), (3585, 3601, 520)])
+def test_forward_many_tiles(M, N, K):
+    """Contractions long enough for the largest tiles, ragged in every size."""
+    forward(M, N, K, pqm.ACT_NONE, False, False, True, False)
+    forward(M, N, K, pqm.ACT_SILU, True, True, False, True, ldx=8, ldr=5)
+
+
+@pytest.mark.parametrize("M,N,K", [(3600, 264, 3848), (3585, 520, 3592), (300, 3592, 3848), (1000, 264, 8),
+                                   (9000, 136, 264), (33000, 64, 72)])
+def test_backward_many_tiles(M, N, K):
+    """The same for dx and for dW, and dW over many rows in many parts."""
+    backward(M, N, K, pqm.ACT_NONE, True, True, ldx=8)
+
+
 @pytest.mark.parametrize("act", [pqm.ACT_NONE, pqm.ACT_SILU, pqm.ACT_GELU])
 @pytest.mark.parametrize("add,bias", [(False, False), (True, True)])
 def test_backward_epilogues(act, add, bias):

@@ -127,6 +127,17 @@ def test_stages(T, E, k, H, I, shared, softmax, renorm):
         check(o, x, res, w, gate_w, q, k, I, shared, softmax, renorm, scale)
 
 
+@pytest.mark.parametrize("T,E,k,H,I,shared", [(4, 64, 8, 2048, 1024, True), (1, 12, 8, 4096, 2080, False),
+                                              (8, 40, 8, 1056, 1536, True), (20, 16, 4, 4128, 544, True)])
+def test_large_experts(T, E, k, H, I, shared):
+    """Few tokens whose experts' weights are too many for one kernel, and odd widths."""
+    q, norm_w, gate_w, g = weights(E, H, I, T + E, shared)
+    x, r = tokens(g, T, H)
+    o = pqm.moe_decode_nvfp4(x, r, norm_w, gate_w, *q, k, I, shared, pqm.SCORE_SIGMOID, True, 1.5)
+    torch.cuda.synchronize()
+    check(o, x, r, norm_w, gate_w, q, k, I, shared, False, True, 1.5)
+
+
 def test_like_the_separate_calls():
     """Against nvfp4_moe_decode, which makes the six calls: the same norm and
     choice, and out within its roundings."""
