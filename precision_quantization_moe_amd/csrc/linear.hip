@@ -46,6 +46,7 @@ struct LnEpi {
   int64_t N;
   int act, f32;
   int vec;  // rows of y, z and res hold whole, aligned groups of eight
+  int stream;  // 1: bf16 outputs go past the caches; 2: the residual too
 };
 
 // -s(z) log2(e) of the activation.
@@ -83,12 +84,30 @@ __device__ __forceinline__ void ln_put1(const LnEpi &e, int64_t r, int64_t c, fl
     static_cast<uint16_t *>(e.y)[at] = (uint16_t)pk_bf16_rne(v, 0.0f);
 }
 
+// Keeps a streaming access from being joined with the plain one of the other branch,
+// which makes both plain.
+#define LN_APART asm volatile("")
+
 // Eight neighbouring outputs of row r from column c on, where rows hold whole,
 // aligned groups of eight (e.vec); q, b: ln_res8 and ln_bias8 of them, which their
 // callers ask for early.
 __device__ __forceinline__ ln_u4 ln_res8(const LnEpi &e, int64_t r, int64_t c) {
   if (!e.res) return ln_u4{0, 0, 0, 0};
-  return *reinterpret_cast<const ln_u4 *>(e.res + r * e.ldr + c);
+  const ln_u4 *p = reinterpret_cast<const ln_u4 *>(e.res + r * e.ldr + c);
+  if (e.stream < 2) return *p;
+  LN_APART;
+  const ln_u4 q = __builtin_nontemporal_load(p);
+  LN_APART;
+  return q;
+}
+__device__ __forceinline__ void ln_store8(const LnEpi &e, uint16_t *to, const ln_u4 &o) {
+  if (e.stream) {
+    LN_APART;
+    __builtin_nontemporal_store(o, reinterpret_cast<ln_u4 *>(to));
+    LN_APART;
+  } else {
+    *reinterpret_cast<ln_u4 *>(to) = o;
+  }
 }
 __device__ __forceinline__ void ln_bias8(const LnEpi &e, int64_t c, float (&b)[8]) {
 #pragma unroll
@@ -104,7 +123,7 @@ __device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, fl
   if (e.z) {
     const ln_u4 o = {pk_bf16_rne(v[0], v[1]), pk_bf16_rne(v[2], v[3]), pk_bf16_rne(v[4], v[5]),
                      pk_bf16_rne(v[6], v[7])};
-    *reinterpret_cast<ln_u4 *>(e.z + at) = o;
+    ln_store8(e, e.z + at, o);
   }
   if (e.act != PQM_ACT_NONE) {
 #pragma unroll
@@ -124,7 +143,7 @@ __device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, fl
   } else {
     const ln_u4 o = {pk_bf16_rne(v[0], v[1]), pk_bf16_rne(v[2], v[3]), pk_bf16_rne(v[4], v[5]),
                      pk_bf16_rne(v[6], v[7])};
-    *reinterpret_cast<ln_u4 *>(static_cast<uint16_t *>(e.y) + at) = o;
+    ln_store8(e, static_cast<uint16_t *>(e.y) + at, o);
   }
 }
 
@@ -133,11 +152,11 @@ __device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, fl
 // Four waves, 2 x 2, a tile; operands by DMA into a ring of LDS slots of 32 of the
 // contraction, fragments read one step ahead.  256 x 256: a wave's 128 x 128 outputs
 // take half the LDS bytes of 128 x 128 tiles a product, at one workgroup a CU.
-// 8190 x 4096 x 2048 with SiLU, bias, residual and z kept 170 us (the product alone by
-// the library 111): the steps 131 (1050 TFLOP/s) and two epilogues of 20, in which all
+// 8190 x 4096 x 2048 with SiLU, bias, residual and z kept 162 us (the product alone by
+// the library 111): the steps 131 (1050 TFLOP/s) and two epilogues of 16, in which all
 // CUs move their 384 KB of residual, y and z at once and multiply nothing.  Without
 // an epilogue dx of the same layer takes 123 (library 120), dW 152 (174).  The router,
-// 16384 x 128 x 2048, 22.7 us: 75 MB at 3.3 TB/s, one workgroup a CU.
+// 16384 x 128 x 2048, 22.7 us: 75 MB at 3.3 TB/s, one workgroup a CU; its dx 36, 138 MB.
 
 enum { LN_NT = 0, LN_NN = 1, LN_TN = 2 };  // y; dx (B is ML); dW (both are ML)
 
@@ -659,6 +678,17 @@ int64_t ln_tiles(int64_t I, int64_t J, int tm, int tn) {
   return ((I + tm - 1) / tm) * ((J + tn - 1) / tn);
 }
 
+// Outputs of 3 * 2^23 values on (50 MB) leave past the caches: the operands keep them
+// (8190 x 4096 x 2048 with SiLU, bias, residual and z: 168 us, 162 so; dx of 16384 x 128
+// x 2048: 46, 36, though a norm's gradients behind it, which read it, give back 13; two
+// layers of 8192 x 2048 x 8192 in a row: 549, 518).  Fewer are still
+// there for whoever reads them next (the same two layers with 1024 rows and 4096
+// outputs: 64, 73).  A residual of 2^26 values does too: it is not there anyway
+// (8192 x 8192 x 2048: 334, 306), where one of 2^25 may be (36, 46).
+int ln_stream(int64_t I, int64_t J) {
+  return I * J >= (int64_t)1 << 26 ? 2 : I * J >= (int64_t)3 << 23 ? 1 : 0;
+}
+
 // Tiles and splits by size alone.
 //
 // 256 x 256 tiles from 200 of them on (8190 x 4096 x 2048: 976 TFLOP/s, 128 x 128
@@ -812,7 +842,8 @@ pqm_status pqm_linear(const uint16_t *x, int64_t ldx, const uint16_t *w, const f
     if (!al(workspace, 16)) return PQM_ERR_ALIGN;
   }
   const int vec = N % 8 == 0 && (!residual || (al(residual, 16) && ldr % 8 == 0));
-  const LnEpi e = {bias, residual, ldr, y, z, N, act, y_dtype == PQM_OUT_FP32, vec};
+  const LnEpi e = {bias, residual, ldr, y, z, N, act, y_dtype == PQM_OUT_FP32, vec,
+                   ln_stream(M, N)};
   return st_of(ln_is_few(M, N, K) ? ln_few(x, ldx, w, M, N, K, e, stream)
                            : ln_product<LN_NT>(x, ldx, w, K, M, N, K, e,
                                                static_cast<float *>(workspace), stream));
@@ -871,12 +902,13 @@ pqm_status pqm_linear_backward(const uint16_t *dy, int64_t lddy, const uint16_t 
   const int64_t ldg = act == PQM_ACT_NONE ? lddy : N;
   if (dx) {
     const LnEpi e = {nullptr, d_x, ldd, dx, nullptr, K, PQM_ACT_NONE, 0,
-                     !d_x || (al(d_x, 16) && ldd % 8 == 0)};
+                     !d_x || (al(d_x, 16) && ldd % 8 == 0),
+                     ln_stream(M, K)};
     const hipError_t r = ln_product<LN_NN>(g, ldg, w, K, M, K, N, e, ws, stream);
     if (r != hipSuccess) return PQM_ERR_HIP;
   }
   if (dw) {
-    const LnEpi e = {nullptr, nullptr, 0, dw, nullptr, K, PQM_ACT_NONE, 1, 1};
+    const LnEpi e = {nullptr, nullptr, 0, dw, nullptr, K, PQM_ACT_NONE, 1, 1, 0};
     const hipError_t r = ln_product<LN_TN>(g, ldg, x, ldx, N, K, M, e, ws, stream);
     if (r != hipSuccess) return PQM_ERR_HIP;
   }
