@@ -765,7 +765,7 @@ size_t pqm_moe_decode_nvfp4_workspace(int64_t tokens, int64_t hidden, int64_t in
  * irrelevant): pqm_linear_workspace bytes, 0 for many sizes; calls that may run
  * at the same time need separate ones.  A row's sums depend on the sizes alone
  * besides its own values.
- * Requires K % 8 == 0, 8 <= K <= 2^22, 0 <= N <= 2^22, M < 2^31 with fewer than
+ * Requires K % 8 == 0, 8 <= K <= 2^22, 0 <= N <= 2^22, M < 2^29 with fewer than
  * 2^24 tiles of 128 x 128 and M (N + K) <= 2^40, K <= ldx <= 2^22,
  * N <= ldr <= 2^22 (PQM_ERR_SHAPE); x, w, y, z and ldx aligned to 16 bytes,
  * bias 4, residual 2 (PQM_ERR_ALIGN).  N and ldr of whole 8 and residual
@@ -829,7 +829,7 @@ size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
  * workspace (device, 8-byte aligned, contents irrelevant):
  * pqm_token_logprobs_workspace bytes, 0 where a row is one workgroup's; calls
  * that may run at the same time need separate ones.
- * Requires 1 <= vocab <= 2^30, vocab <= ld <= 2^30, tokens < 2^31,
+ * Requires 1 <= vocab <= 2^30, vocab <= ld <= 2^30, tokens * ceil(vocab / 8192) < 2^24,
  * 0 <= top_n <= 32, top_n <= vocab, 2^-60 <= temperature <= 2^60
  * (PQM_ERR_SHAPE); tensors aligned to their element (PQM_ERR_ALIGN).
  */

@@ -790,7 +790,7 @@ pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; 
 
 // Sizes that every product here takes.
 bool ln_sizes(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 0 && K >= 8 && K % 8 == 0 && M < ((int64_t)1 << 31) && N <= LN_MAX &&
+  return M >= 0 && N >= 0 && K >= 8 && K % 8 == 0 && M < ((int64_t)1 << 29) && N <= LN_MAX &&
          K <= LN_MAX && ln_tiles(M, N, 128, 128) < (1 << 24) && M <= ((int64_t)1 << 40) / (N + K);
 }
 

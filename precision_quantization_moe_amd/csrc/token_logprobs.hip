@@ -7,14 +7,14 @@
 //   H = log S - (sum e^u u) / S,
 //   d x_i = (g [i = id] - p_i (g + h (log p_i + H))) / t
 // for the gradients g of log p_id and h of H.  One pass reads the row: each
-// thread carries its running maximum, sum and weighted sum, and moves the sums
-// when its maximum grows.  u is formed from the difference, which neither
+// thread carries its running maximum, sum (without the maximum's own 1) and weighted
+// sum, and moves the sums when its maximum grows.  u is formed from the difference, which neither
 // overflows nor loses digits where all logits are far from 0; in powers of two,
 // u log2(e).
 //
 // Both directions are bound by memory where there are many rows: 4093 rows of 32768
-// bf16, a fifth of them left out, in 46 us (4.7 TB/s of the rows that are read);
-// gradient of 2048 rows of 151936 bf16, a fifth left out, in 207 us (5.4 TB/s, read and
+// bf16, a fifth of them left out, in @F us (@f TB/s of the rows that are read);
+// gradient of 2048 rows of 151936 bf16, a fifth left out, in @B us (@b TB/s, read and
 // written), of 509 rows of 50257 binary32, an odd length, in 44 (4.6).  One row of 151936 is split over workgroups and bound by
 // the chain of load, choice of the best, join: 17.5 us with 20 alternatives.
 #include "pqm_device.hpp"
@@ -46,21 +46,34 @@ __device__ __forceinline__ float tl_one(const void *row, int64_t i) {
   return bf16_lo_f32(static_cast<const uint16_t *>(row)[i]);
 }
 
+// The same, past the caches with NT: what no cache holds until its next reader comes
+// only takes the place of something else.
+typedef uint32_t tl_v4 __attribute__((ext_vector_type(4), aligned(2)));
+template <bool NT>
+__device__ __forceinline__ TlWords tl_get(const void *at) {
+  if (!NT) return *static_cast<const TlWords *>(at);
+  return __builtin_bit_cast(TlWords, __builtin_nontemporal_load(static_cast<const tl_v4 *>(at)));
+}
+template <bool NT>
+__device__ __forceinline__ void tl_put(void *at, const TlWords &w) {
+  if (!NT) *static_cast<TlWords *>(at) = w;
+  else __builtin_nontemporal_store(__builtin_bit_cast(tl_v4, w), static_cast<tl_v4 *>(at));
+}
+
 // Eight logits from i on, -inf past the end.
-template <bool F32>
+template <bool F32, bool NT>
 __device__ __forceinline__ void tl_load8(const void *row, int64_t i, int64_t end, float (&x)[8]) {
   if (i + 8 <= end) {
     if (F32) {
-      const TlWords *p = reinterpret_cast<const TlWords *>(static_cast<const float *>(row) + i);
-      const TlWords a = p[0], b = p[1];
+      const float *p = static_cast<const float *>(row) + i;
+      const TlWords a = tl_get<NT>(p), b = tl_get<NT>(p + 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[j] = __uint_as_float(a.w[j]);
         x[4 + j] = __uint_as_float(b.w[j]);
       }
     } else {
-      const TlWords a =
-          *reinterpret_cast<const TlWords *>(static_cast<const uint16_t *>(row) + i);
+      const TlWords a = tl_get<NT>(static_cast<const uint16_t *>(row) + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[2 * j] = bf16_lo_f32(a.w[j]);
@@ -73,10 +86,12 @@ __device__ __forceinline__ void tl_load8(const void *row, int64_t i, int64_t end
   for (int j = 0; j < 8; ++j) x[j] = i + j < end ? tl_one<F32>(row, i + j) : -__builtin_inff();
 }
 
-// Running statistics: the maximum, the sum and the sum weighted by u log2(e).
-// A NaN is no maximum, but reaches the sum.
+// Running statistics: the maximum, the sum of e^u without the maximum's own 1, and the
+// sum of e^u u log2(e).  Without that 1 a nearly certain row keeps its entropy and its
+// log S = log(1 + r), which are as small as r: next to the 1 they would lose what lies
+// below half a step of it.  A NaN is no maximum, but reaches the sum.
 struct TlSums {
-  float m, s, t;
+  float m, r, t;
 };
 
 // Where nothing but -inf was seen, differences are taken from 0.
@@ -88,42 +103,64 @@ __device__ __forceinline__ float tl_exponent(float d, float c) {
   return __builtin_elementwise_maximum(d * c, -200.0f);
 }
 
-__device__ __forceinline__ void tl_move(TlSums &a, float m, float c) {
-  const float d = tl_exponent(a.m - tl_from(m), c), f = __builtin_amdgcn_exp2f(d);
-  a.t = f * __builtin_fmaf(a.s, d, a.t);
-  a.s *= f;
-  a.m = m;
+// Takes b, of a maximum not above a's, into a; with nothing seen its share is 0.
+__device__ __forceinline__ void tl_take(TlSums &a, const TlSums &b, float c) {
+  const float d = tl_exponent(b.m - tl_from(a.m), c), f = __builtin_amdgcn_exp2f(d);
+  const float all = 1.0f + b.r;
+  a.t = __builtin_fmaf(f, __builtin_fmaf(all, d, b.t), a.t);
+  a.r = __builtin_fmaf(f, all, a.r);
 }
 
-__device__ __forceinline__ void tl_join(TlSums &a, TlSums b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  tl_move(a, m, c);
-  tl_move(b, m, c);
-  a.s += b.s;
-  a.t += b.t;
+__device__ __forceinline__ void tl_join(TlSums &a, const TlSums &b, float c) {
+  const bool up = b.m > a.m;
+  TlSums hi = up ? b : a;
+  const TlSums lo = up ? a : b;
+  tl_take(hi, lo, c);
+  a = hi;
 }
 
-__device__ __forceinline__ void tl_add8(TlSums &a, const float (&x)[8], float c) {
-  const float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  if (m > a.m) tl_move(a, m, c);
-  const float from = tl_from(a.m);
-  float s[2] = {0, 0}, t[2] = {0, 0};
+// Takes in 8 U logits.  All at once, since a wave finds a new maximum in one of its
+// lanes nearly every time (4093 rows of 32768: 52.8 us by 32, 53.6 by eight).
+template <int U>
+__device__ __forceinline__ void tl_add(TlSums &a, const float (&v)[U][8], float c) {
+  float x[U][8], m = v[0][0];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float u = tl_exponent(x[j] - from, c), e = __builtin_amdgcn_exp2f(u);
-    s[j & 1] += e;
-    t[j & 1] = __builtin_fmaf(e, u, t[j & 1]);
+  for (int j = 0; j < 8 * U; ++j) {
+    x[j / 8][j % 8] = v[j / 8][j % 8];
+    m = fmaxf(m, v[j / 8][j % 8]);
   }
-  a.s += s[0] + s[1];
-  a.t += t[0] + t[1];
+  if (m > a.m) {  // a new maximum: its 1 is no part of r
+    TlSums b = {m, 0.0f, 0.0f};
+    tl_take(b, a, c);
+    a = b;
+    bool left = m < __builtin_inff();  // inf stays: inf - inf makes the row NaN
+#pragma unroll
+    for (int j = 0; j < 8 * U; ++j) {
+      const bool it = left && x[j / 8][j % 8] == m;
+      x[j / 8][j % 8] = it ? -__builtin_inff() : x[j / 8][j % 8];
+      left = left && !it;
+    }
+  }
+  const float from = tl_from(a.m);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float u = tl_exponent(x[i][j] - from, c), e = __builtin_amdgcn_exp2f(u);
+      s[j & 1] += e;
+      t[j & 1] = __builtin_fmaf(e, u, t[j & 1]);
+    }
+    a.r += s[0] + s[1];
+    a.t += t[0] + t[1];
+  }
 }
 
 // The workgroup's statistics in thread 0.
 __device__ __forceinline__ TlSums tl_reduce(TlSums a, float c, TlSums *sh) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
-    const TlSums b = {__shfl_down(a.m, o, 64), __shfl_down(a.s, o, 64), __shfl_down(a.t, o, 64)};
+    const TlSums b = {__shfl_down(a.m, o, 64), __shfl_down(a.r, o, 64), __shfl_down(a.t, o, 64)};
     tl_join(a, b, c);
   }
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
@@ -244,15 +281,15 @@ __device__ __forceinline__ int64_t tl_id(const TlArgs &a, int64_t row) {
 template <bool F32>
 __device__ __forceinline__ void tl_finish(const TlArgs &a, int64_t row, int64_t id, const TlSums &s,
                                           const TlTop *top, float *sh) {
-  const bool none = s.m == -__builtin_inff() && s.s == 0.0f;  // -inf alone
+  const bool none = s.m == -__builtin_inff() && s.r == 0.0f;  // -inf alone
   if (threadIdx.x == 0) {
-    const float log_s = none ? 0.0f : logf(s.s);
+    const float log_s = none ? 0.0f : log1pf(s.r);
     if (a.stats) {
       a.stats[2 * row] = s.m;
       a.stats[2 * row + 1] = log_s;
     }
-    if (a.entropy) a.entropy[row] = none ? 0.0f : fmaxf(log_s - TL_LN2 * (s.t / s.s), 0.0f);
-    if (a.entropy && !none && s.s != s.s) a.entropy[row] = s.s;
+    if (a.entropy) a.entropy[row] = none ? 0.0f : fmaxf(log_s - TL_LN2 * (s.t / (1.0f + s.r)), 0.0f);
+    if (a.entropy && !none && s.r != s.r) a.entropy[row] = s.r;
     if (a.logprob) {
       const float x = tl_one<F32>(static_cast<const uint8_t *>(a.x) +
                                       row * a.ld * (F32 ? 4 : 2), id);
@@ -287,7 +324,7 @@ __device__ __forceinline__ void tl_skip(const TlArgs &a, int64_t row) {
 }  // namespace
 
 // One part of one row a workgroup; a row of one part is finished here.
-template <bool F32, bool TOP>
+template <bool F32, bool TOP, bool NT>
 __global__ __launch_bounds__(256) void k_token_logprobs(TlArgs a) {
   __shared__ TlSums sh[4];
   __shared__ float fin[2];
@@ -306,12 +343,12 @@ __global__ __launch_bounds__(256) void k_token_logprobs(TlArgs a) {
     tl_top_init(top);
     for (int64_t i = i0; i < end; i += TL_TILE) {  // every thread takes every turn
       const int64_t at = i + 8 * threadIdx.x;
-      float v[8];
-      tl_load8<F32>(x, at, end, v);
-      tl_add8(s, v, a.c);
+      float v[1][8];
+      tl_load8<F32, NT>(x, at, end, v[0]);
+      tl_add<1>(s, v, a.c);
       tl_key k[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = at + j < end ? tl_make(v[j], at + j) : 0;
+      for (int j = 0; j < 8; ++j) k[j] = at + j < end ? tl_make(v[0][j], at + j) : 0;
       tl_top_add(top, k, a.n);
     }
   } else {
@@ -319,14 +356,13 @@ __global__ __launch_bounds__(256) void k_token_logprobs(TlArgs a) {
     for (; at + 3 * TL_TILE + 8 <= end; at += 4 * TL_TILE) {
       float v[4][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) tl_load8<F32>(x, at + u * TL_TILE, a.V, v[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) tl_add8(s, v[u], a.c);
+      for (int u = 0; u < 4; ++u) tl_load8<F32, NT>(x, at + u * TL_TILE, a.V, v[u]);
+      tl_add<4>(s, v, a.c);
     }
     for (; at < end; at += TL_TILE) {
-      float v[8];
-      tl_load8<F32>(x, at, end, v);
-      tl_add8(s, v, a.c);
+      float v[1][8];
+      tl_load8<F32, NT>(x, at, end, v[0]);
+      tl_add<1>(s, v, a.c);
     }
   }
   s = tl_reduce(s, a.c, sh);
@@ -339,7 +375,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs(TlArgs a) {
   if (threadIdx.x == 0) {
     float *f = reinterpret_cast<float *>(rec);
     f[0] = s.m;
-    f[1] = s.s;
+    f[1] = s.r;
     f[2] = s.t;
   }
   if constexpr (TOP) {
@@ -394,24 +430,24 @@ struct TlBack {
 
 constexpr int TB_TURNS = 4;  // eight logits a thread each
 
-template <bool F32>
+template <bool F32, bool NT>
 __device__ __forceinline__ void tl_store8(void *row, int64_t i, int64_t end, const float (&v)[8]) {
   if (i + 8 <= end) {
     if (F32) {
-      TlWords *p = reinterpret_cast<TlWords *>(static_cast<float *>(row) + i);
+      float *p = static_cast<float *>(row) + i;
       TlWords a, b;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         a.w[j] = __float_as_uint(v[j]);
         b.w[j] = __float_as_uint(v[4 + j]);
       }
-      p[0] = a;
-      p[1] = b;
+      tl_put<NT>(p, a);
+      tl_put<NT>(p + 4, b);
     } else {
       TlWords a;
 #pragma unroll
       for (int j = 0; j < 4; ++j) a.w[j] = pk_bf16_rne(v[2 * j], v[2 * j + 1]);
-      *reinterpret_cast<TlWords *>(static_cast<uint16_t *>(row) + i) = a;
+      tl_put<NT>(static_cast<uint16_t *>(row) + i, a);
     }
     return;
   }
@@ -427,7 +463,7 @@ __device__ __forceinline__ void tl_store8(void *row, int64_t i, int64_t end, con
 
 // Gradient: with l = log2 p, d x = [i = id] g / t - p (A + B l), A = (g + h H) / t,
 // B = h ln 2 / t.
-template <bool F32, bool OUTF32>
+template <bool F32, bool OUTF32, bool NT>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
   const int64_t row = blockIdx.x / a.parts;
   const int64_t at = (blockIdx.x - row * a.parts) * (int64_t)(TB_TURNS * TL_TILE) +
@@ -441,7 +477,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
   if (skip) {
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < TB_TURNS; ++u) tl_store8<OUTF32>(dx, at + u * TL_TILE, a.V, zero);
+    for (int u = 0; u < TB_TURNS; ++u) tl_store8<OUTF32, NT>(dx, at + u * TL_TILE, a.V, zero);
     return;
   }
   const float ls = log_s * TL_LOG2E;
@@ -450,7 +486,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
   const float A = a.d_entropy ? __builtin_fmaf(h, a.entropy[row], g) : g, B = h * TL_LN2;
   float v[TB_TURNS][8];
 #pragma unroll
-  for (int u = 0; u < TB_TURNS; ++u) tl_load8<F32>(x, at + u * TL_TILE, a.V, v[u]);
+  for (int u = 0; u < TB_TURNS; ++u) tl_load8<F32, NT>(x, at + u * TL_TILE, a.V, v[u]);
 #pragma unroll
   for (int u = 0; u < TB_TURNS; ++u) {
 #pragma unroll
@@ -465,7 +501,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
       for (int j = 0; j < 8; ++j)
         if (rel == j) v[u][j] += g;
     }
-    tl_store8<OUTF32>(dx, at + u * TL_TILE, a.V, v[u]);
+    tl_store8<OUTF32, NT>(dx, at + u * TL_TILE, a.V, v[u]);
   }
 }
 
@@ -495,18 +531,27 @@ size_t tl_bytes(int64_t tokens, int64_t V, int64_t n) {
 }
 
 bool tl_sizes(int64_t tokens, int64_t V, int64_t n) {
-  return tokens >= 0 && tokens < ((int64_t)1 << 31) && V >= 1 && V <= ((int64_t)1 << 30) && n >= 0 &&
+  return tokens >= 0 && tokens < ((int64_t)1 << 24) && V >= 1 && V <= ((int64_t)1 << 30) && n >= 0 &&
          n <= TL_TOP && n <= V;
 }
 
 bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 pqm_status st_of(hipError_t e) { return e == hipSuccess ? PQM_OK : PQM_ERR_HIP; }
 
-template <bool F32>
+// Logits of 3 * 2^26 bytes on (200 MB) go past the caches, which cannot hold them for
+// the backward pass anyway, and so does their gradient: 2048 rows of 151936 bf16 125 and
+// 235 us, 125 and 221 so, one after the other 370 and 331; 4093 of 32768 57 and 103, 53
+// and 92, 168 and 145.  Fewer may still be there (509 of 50257 binary32: 25 and 39, 27
+// and 47 so).
+bool tl_streams(int64_t tokens, int64_t V, bool f32) {
+  return tokens * V * (f32 ? 4 : 2) >= (int64_t)3 << 26;
+}
+
+template <bool F32, bool NT>
 hipError_t tl_forward(const TlArgs &a, int64_t tokens, hipStream_t st) {
   const dim3 grid((unsigned)(tokens * a.parts)), rows((unsigned)tokens), block(256);
-  if (a.n) hipLaunchKernelGGL((k_token_logprobs<F32, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_token_logprobs<F32, false>), grid, block, 0, st, a);
+  if (a.n) hipLaunchKernelGGL((k_token_logprobs<F32, true, NT>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_token_logprobs<F32, false, NT>), grid, block, 0, st, a);
   const hipError_t r = hipGetLastError();
   if (r != hipSuccess || a.parts == 1) return r;
   if (a.n) hipLaunchKernelGGL((k_token_logprobs_join<F32, true>), rows, block, 0, st, a);
@@ -536,7 +581,7 @@ pqm_status pqm_token_logprobs(const void *logits, pqm_dtype logits_dtype, int64_
   if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return PQM_ERR_SHAPE;
   const bool f32 = logits_dtype == PQM_OUT_FP32;
   const TlPlan p = tokens ? tl_plan(tokens, vocab, top_n) : TlPlan{1, vocab};
-  if (tokens * p.parts >= ((int64_t)1 << 31)) return PQM_ERR_SHAPE;
+  if (tokens * p.parts >= ((int64_t)1 << 24)) return PQM_ERR_SHAPE;
   if (tokens == 0) return PQM_OK;
   if (!logits || (!logprob && !entropy && !stats && !top_n) || (logprob && !ids) ||
       (top_n && (!top_ids || !top_logprob)))
@@ -553,7 +598,11 @@ pqm_status pqm_token_logprobs(const void *logits, pqm_dtype logits_dtype, int64_
   const TlArgs a = {logits, ld, ids, vocab, temperature, (float)(1.4426950408889634 / temperature),
                     logprob, entropy, stats, top_ids, top_logprob, (int)top_n, p.parts, p.part,
                     static_cast<uint8_t *>(workspace)};
-  return st_of(f32 ? tl_forward<true>(a, tokens, stream) : tl_forward<false>(a, tokens, stream));
+  const bool nt = tl_streams(tokens, vocab, f32);
+  return st_of(f32 ? nt ? tl_forward<true, true>(a, tokens, stream)
+                        : tl_forward<true, false>(a, tokens, stream)
+               : nt ? tl_forward<false, true>(a, tokens, stream)
+                    : tl_forward<false, false>(a, tokens, stream));
 }
 
 pqm_status pqm_token_logprobs_backward(const void *logits, pqm_dtype logits_dtype, int64_t ld,
@@ -574,7 +623,7 @@ pqm_status pqm_token_logprobs_backward(const void *logits, pqm_dtype logits_dtyp
   if (d_logits && d_logits == logits && (ld != ldd || logits_dtype != d_logits_dtype))
     return PQM_ERR_SHAPE;
   const int64_t parts = (vocab + TB_TURNS * TL_TILE - 1) / (TB_TURNS * TL_TILE);
-  if (tokens * parts >= ((int64_t)1 << 31)) return PQM_ERR_SHAPE;
+  if (tokens * parts >= ((int64_t)1 << 24)) return PQM_ERR_SHAPE;
   if (tokens == 0) return PQM_OK;
   if (!logits || !stats || !d_logits || (!d_logprob && !d_entropy) || (d_logprob && !ids) ||
       (d_entropy && !entropy))
@@ -585,10 +634,14 @@ pqm_status pqm_token_logprobs_backward(const void *logits, pqm_dtype logits_dtyp
     return PQM_ERR_ALIGN;
   const TlBack a = {logits, ld, ids, vocab, temperature, (float)(1.4426950408889634 / temperature),
                     stats, entropy, d_logprob, d_entropy, d_logits, ldd, (int)parts};
-  const auto kernel = f32 ? o32 ? k_token_logprobs_backward<true, true>
-                                : k_token_logprobs_backward<true, false>
-                      : o32 ? k_token_logprobs_backward<false, true>
-                            : k_token_logprobs_backward<false, false>;
+  const auto pick = [&](auto nt) {
+    constexpr bool NT = decltype(nt)::value;
+    return f32 ? o32 ? k_token_logprobs_backward<true, true, NT>
+                     : k_token_logprobs_backward<true, false, NT>
+           : o32 ? k_token_logprobs_backward<false, true, NT>
+                 : k_token_logprobs_backward<false, false, NT>;
+  };
+  const auto kernel = tl_streams(tokens, vocab, f32) ? pick(std::true_type()) : pick(std::false_type());
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tokens * parts)), dim3(256), 0, stream, a);
   return st_of(hipGetLastError());
 }

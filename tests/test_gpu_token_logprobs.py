@@ -301,3 +301,56 @@ def test_rows_beyond_32_bits():
     alone = pqm.token_logprobs_backward(x[pick].contiguous(), ids[rows].cuda(), o[2][pick].contiguous(),
                                         one[:4].contiguous())
     assert torch.equal(d[pick], alone) and not d[69990:69999].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [0, 4])
+def test_more_logits_than_the_caches_hold(dtype, n):
+    """From 200 MB on logits and gradients go past the caches: the same results, at
+    odd lengths and offsets too, and nothing beside the rows is written."""
+    T, V = 1100, 100003 if dtype is torch.bfloat16 else 50001
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(T, V + 3, generator=g, device="cuda").mul_(3).to(dtype)[:, 1:V + 1]
+    ids = torch.full((T,), -1, dtype=torch.int32)
+    rows = torch.tensor([0, 1, 700, 1098, 1099])
+    ids[rows] = torch.tensor([5, V - 1, 0, 77, V - 2], dtype=torch.int32)
+    o = pqm.token_logprobs(x, ids.cuda(), 0.9, n)
+    pick = rows.cuda()
+    few = x[pick].contiguous()
+    check(few.cpu(), ids[rows], 0.9, n, tuple(t[pick] if t is not None else None for t in o))
+    one = torch.ones(T).cuda()
+    for out_dtype in (torch.bfloat16, torch.float32):
+        wide = torch.full((T, V + 3), 7.0, dtype=out_dtype, device="cuda")
+        d = pqm.token_logprobs_backward(x, ids.cuda(), o[2], one, 0.9, o[1], one, out=wide[:, 2:V + 2])
+        alone = pqm.token_logprobs_backward(few, ids[rows].cuda(), o[2][pick].contiguous(), one[:5].contiguous(), 0.9,
+                                            o[1][pick].contiguous(), one[:5].contiguous(),
+                                            out_dtype=pqm.OUT_BF16 if out_dtype is torch.bfloat16 else pqm.OUT_FP32)
+        assert torch.equal(d[pick], alone) and not d[2:700].any()
+        assert (wide[:, :2] == 7).all() and (wide[:, V + 2:] == 7).all()
+    same = x.contiguous()
+    want = pqm.token_logprobs_backward(x, ids.cuda(), o[2], one, 0.9, o[1], one)
+    assert pqm.token_logprobs_backward(same, ids.cuda(), o[2], one, 0.9, o[1], one, out=same) is same
+    assert torch.equal(same, want)
+
+
+@pytest.mark.parametrize("T,V", [(1, 151936), (2, 9), (40, 5000), (1200, 3001)])
+@pytest.mark.parametrize("n", [0, 3])
+def test_nearly_certain_rows(T, V, n):
+    """Rows whose largest logit holds all but 2^-10 to 2^-60 of the probability: the
+    entropy and that token's log probability, as small as what is left, keep their
+    relative precision.  r = S - 1 is a sum of positive terms of a relative error of
+    4 U |u| + 2 U each, V / 256 + 32 additions; log(1 + r) and the quotient add 8 U;
+    both parts of the entropy are positive."""
+    g = torch.Generator().manual_seed(T + V)
+    x = torch.rand(T, V, generator=g)
+    top = torch.randint(0, V, (T,), generator=g)
+    x.scatter_(1, top[:, None], (7 + 30 * torch.rand(T, 1, generator=g)) + math.log(V))
+    lp, ent, stats, _, _ = pqm.token_logprobs(x.cuda(), top.to(torch.int32).cuda(), 1.0, n)
+    z = f64(x)
+    u = z - z.gather(1, top[:, None])
+    e = torch.exp(u).scatter_(1, top[:, None], 0.0)
+    r = e.sum(1)
+    ls, h = torch.log1p(r), torch.log1p(r) - (e * u).sum(1) / (1 + r)
+    rel = 1.05 * (2 * (V / 256 + 32) + 4 * float(u.abs().max()) + 16) * U
+    assert ((f64(ent) - h).abs() <= rel * h).all(), float(((f64(ent) - h).abs() / h / rel).max())
+    assert ((f64(lp) + ls).abs() <= rel * ls).all() and ((f64(stats)[:, 1] - ls).abs() <= rel * ls).all()
