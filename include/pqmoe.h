@@ -784,7 +784,7 @@ size_t pqm_linear_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
  * Gradients of that product (the residual's is dy itself):
- *   dz = bf16(dy act'(z)), the operand type of the products; without an
+ *   dz = bf16(dy act'(z)), the nearest value, the operand of the products; without an
  *        activation it is dy, and z and dz are not used
  *   dx = bf16(dz W + d_x), d_x (bf16 [M, K], row stride ldd, may be NULL): a
  *        gradient that reaches x past this product

@@ -9,6 +9,7 @@
 // dW).  act(z) = z / (1 + e^-s(z)), s(z) = z (SiLU) or 2 sqrt(2/pi)
 // (z + 0.044715 z^3) (GELU with its tanh, since (1 + tanh u) / 2 is the
 // sigmoid of 2 u).  Sums are binary32; y, z, dx and dz are rounded once.
+#include "norm_device.hpp"
 #include "pqm_device.hpp"
 #include "pqm_internal.hpp"
 #include "pqmoe.h"
@@ -60,7 +61,18 @@ __device__ __forceinline__ float ln_act(float z, int act) {
 }
 // act'(z) = v + z v (1 - v) s'(z) with v the sigmoid of s; v (1 - v) is even in
 // s, so it is formed with e^-|s|, which cannot overflow.
-__device__ __forceinline__ float ln_slope(float z, int act) {
+__device__ __attribute__((noinline)) float ln_dz_near(float g, float z, int act) {
+  constexpr double G = 1.5957691216057307;  // 2 sqrt(2 / pi)
+  const double x = z, s = act == PQM_ACT_SILU ? x : G * (x + 0.044715 * x * x * x);
+  const double ds = act == PQM_ACT_SILU ? 1.0 : G * (1.0 + 0.134145 * x * x);
+  const double t = exp(-__builtin_fabs(s)), r = 1.0 / (1.0 + t);
+  const double v = s < 0.0 ? t * r : r, w = t * r * r;
+  return before_bf16((double)g * (w == 0.0 ? v : v + x * ds * w));
+}
+// g act'(z), to be rounded to bf16: the nearest value.  dW and dbias keep binary32 sums
+// of it, in which one step of bf16 to the wrong side shows where there are few rows; so
+// a binary32 value within its own error of the middle of two is formed again in binary64.
+__device__ __forceinline__ float ln_dz(float g, float z, int act) {
   const float s = ln_squash(z, act);
   const float ds = act == PQM_ACT_SILU
                        ? 1.0f
@@ -68,7 +80,15 @@ __device__ __forceinline__ float ln_slope(float z, int act) {
   const float t = __builtin_amdgcn_exp2f(-fabsf(s)), r = __builtin_amdgcn_rcpf(1.0f + t);
   const float v = s > 0.0f ? t * r : r, w = t * r * r;
   // far out w is 0 and z ds may be infinite
-  return w == 0.0f && s == s ? v : v + z * ds * w;
+  const float a = w == 0.0f && s == s ? 0.0f : z * ds * w, d = g * (v + a);
+  // half steps (2^-24): three of the argument times ln 2 |s|; two of the exponential; two
+  // of the reciprocal, twice, and of 1 + t; the products and the sum
+  const float e = fabsf(g) * (v + fabsf(a)) *
+                  __builtin_fmaf(fminf(fabsf(s), 256.0f), 2.125f * 0x1p-24f, 14.0f * 0x1p-24f);
+  const uint32_t both = pk_bf16_rne(d - e, d + e);
+  // s over 99: e^-s is about to leave binary32, z s'(z) times it need not
+  if (((both ^ (both >> 16)) & 0xFFFFu) || s > 99.0f) return ln_dz_near(g, z, act);
+  return d;
 }
 
 // The output of row r, column c.
@@ -588,7 +608,8 @@ constexpr int LZ_ROWS = 32;  // rows of a workgroup's partial sums
 // dz = bf16(dy act'(z)) (act none: dy itself, not written) and, per LZ_ROWS
 // rows, the column sums of dz.  A thread takes eight columns of every 256 / CT-th
 // row, four rows asked for at once; CT threads a row, as many as fill it.  Bound by
-// memory: 8190 x 4096 in 40 us, 201 MB, a copy's rate.
+// memory and by the values formed again: 8190 x 4096 in 53 us (201 MB, 40 at a copy's
+// rate and without them).
 template <int CT>
 __global__ __launch_bounds__(256) void k_linear_dz(const uint16_t *__restrict__ dy, int64_t lddy,
                                                    const uint16_t *z, int act, int64_t M,
@@ -617,8 +638,8 @@ __global__ __launch_bounds__(256) void k_linear_dz(const uint16_t *__restrict__ 
       if (act != PQM_ACT_NONE) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          d[i][j] = pk_bf16_rne(bf16_lo_f32(d[i][j]) * ln_slope(bf16_lo_f32(zz[i][j]), act),
-                                bf16_hi_f32(d[i][j]) * ln_slope(bf16_hi_f32(zz[i][j]), act));
+          d[i][j] = pk_bf16_rne(ln_dz(bf16_lo_f32(d[i][j]), bf16_lo_f32(zz[i][j]), act),
+                                ln_dz(bf16_hi_f32(d[i][j]), bf16_hi_f32(zz[i][j]), act));
         if (col < N && r < M) *reinterpret_cast<ln_u4 *>(dz + r * N + col) = d[i];
       }
 #pragma unroll

@@ -318,3 +318,25 @@ def test_rows_beyond_32_bits():
     yc = f64(y[:, cols])
     check(dw[cols], yc.t() @ f64(x), (M + 96) * 2 * U * (yc.abs().t() @ f64(x).abs()), "dw")
     check(db[cols], yc.sum(0), 1.01 * (48 + M / 512) * U * yc.abs().sum(0), "db")
+
+
+@pytest.mark.parametrize("act", [pqm.ACT_SILU, pqm.ACT_GELU])
+def test_dz_is_the_nearest(act):
+    """dz = bf16(dy act'(z)) of every z from 2^-20 to 16 by all mantissas of dy: the
+    nearest value of binary64's, so that dW of one row is that row's outer product."""
+    z = torch.arange(0x3580, 0x4180, dtype=torch.int32)
+    z = torch.cat([z, z | 0x8000]).to(torch.int16).view(torch.bfloat16)
+    N = z.numel()
+    dy = (1 + torch.arange(128)[:, None] / 128).to(torch.bfloat16).expand(128, N).contiguous()
+    zz = z.expand(128, N).contiguous().cuda()
+    x, w = torch.ones(128, 8, dtype=torch.bfloat16).cuda(), torch.zeros(N, 8, dtype=torch.bfloat16).cuda()
+    dz = pqm.linear_backward(dy.cuda(), x, w, act, zz, need_dx=False, need_dbias=True)[3]
+    _, slope, _ = activation(f64(z)[None], act)
+    want = f64(dy) * slope
+    got = f64(dz)
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0 ** -126))) - 7)
+    # half a step, and the error of binary64 itself; below bf16's (binary32's) normal
+    # range a result may be flushed
+    assert ((got - want).abs() <= (0.5 + 1e-9) * step + TINY * (want.abs() < 2.0 ** -126)).all(), float(((got - want).abs() / step).max())
+    alone = pqm.linear_backward(dy[5:6].cuda(), x[:1], w, act, zz[:1], need_dx=False)
+    assert torch.equal(alone[1][:, 0], dz[5].float())
