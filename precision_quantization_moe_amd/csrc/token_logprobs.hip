@@ -461,8 +461,8 @@ __device__ __forceinline__ void tl_store8(void *row, int64_t i, int64_t end, con
 
 }  // namespace
 
-// Gradient: with l = log2 p, d x = [i = id] g / t - p (A + B l), A = (g + h H) / t,
-// B = h ln 2 / t.
+// Gradient: with l = log2 p, d x = -p (A + B l), A = (g + h H) / t, B = h ln 2 / t, but
+// for the taken token's.
 template <bool F32, bool OUTF32, bool NT>
 __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
   const int64_t row = blockIdx.x / a.parts;
@@ -483,7 +483,18 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
   const float ls = log_s * TL_LOG2E;
   const float g = a.d_logprob ? a.d_logprob[row] / a.temperature : 0.0f;
   const float h = a.d_entropy ? a.d_entropy[row] / a.temperature : 0.0f;
-  const float A = a.d_entropy ? __builtin_fmaf(h, a.entropy[row], g) : g, B = h * TL_LN2;
+  const float H = a.d_entropy ? a.entropy[row] : 0.0f;
+  const float A = __builtin_fmaf(h, H, g), B = h * TL_LN2;
+  // The taken token: g (1 - p) as -g (e^(log p) - 1), since p of a nearly certain token
+  // is 1 in binary32 long before 1 - p is 0 (what is left of 2^-30 came out as 0), and
+  // the entropy's term apart, which next to g would lose as much.
+  float taken = 0.0f;
+  if (id >= at && (id - at) % TL_TILE < 8 && id - at < TB_TURNS * TL_TILE) {
+    const float d = tl_one<F32>(x, id) - m;
+    const float l = __builtin_elementwise_maximum(__builtin_fmaf(d, a.c, -ls), -200.0f);
+    taken = -g * expm1f(d / a.temperature - log_s) -
+            __builtin_amdgcn_exp2f(l) * __builtin_fmaf(B, l, h * H);
+  }
   float v[TB_TURNS][8];
 #pragma unroll
   for (int u = 0; u < TB_TURNS; ++u) tl_load8<F32, NT>(x, at + u * TL_TILE, a.V, v[u]);
@@ -499,7 +510,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_backward(TlBack a) {
     if (rel >= 0 && rel < 8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (rel == j) v[u][j] += g;
+        if (rel == j) v[u][j] = taken;
     }
     tl_store8<OUTF32, NT>(dx, at + u * TL_TILE, a.V, v[u]);
   }

@@ -354,3 +354,35 @@ def test_nearly_certain_rows(T, V, n):
     rel = 1.05 * (2 * (V / 256 + 32) + 4 * float(u.abs().max()) + 16) * U
     assert ((f64(ent) - h).abs() <= rel * h).all(), float(((f64(ent) - h).abs() / h / rel).max())
     assert ((f64(lp) + ls).abs() <= rel * ls).all() and ((f64(stats)[:, 1] - ls).abs() <= rel * ls).all()
+
+
+@pytest.mark.parametrize("T,V", [(1, 151936), (2, 9), (40, 5000), (1200, 3001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("which", ["logprob", "entropy", "both"])
+def test_gradients_of_nearly_certain_rows(T, V, dtype, which):
+    """The taken token's gradient of such rows, g (1 - p) - h p (log p + H), is as
+    small as what is left and keeps its relative precision: 1 - p is that of log S
+    (rel above) and expm1's 4 U, and both terms of log p + H are off by rel of
+    themselves and 16 U for the factors."""
+    g = torch.Generator().manual_seed(T + V + 1)
+    x = torch.rand(T, V, generator=g)
+    top = torch.randint(0, V, (T,), generator=g)
+    x.scatter_(1, top[:, None], (7 + 30 * torch.rand(T, 1, generator=g)) + math.log(V))
+    x = x.to(dtype)
+    ids = top.to(torch.int32).cuda()
+    o = pqm.token_logprobs(x.cuda(), ids)
+    a = torch.randn(T, generator=g) if which != "entropy" else torch.zeros(T)
+    b = torch.randn(T, generator=g) if which != "logprob" else torch.zeros(T)
+    d = pqm.token_logprobs_backward(x.cuda(), ids, o[2], a.cuda() if which != "entropy" else None, 1.0,
+                                    o[1], b.cuda() if which != "logprob" else None, out_dtype=pqm.OUT_FP32)
+    got = f64(d).gather(1, top[:, None])[:, 0]
+    z = f64(x)
+    u = z - z.gather(1, top[:, None])
+    e = torch.exp(u).scatter_(1, top[:, None], 0.0)
+    r, ls = e.sum(1), torch.log1p(e.sum(1))
+    h = ls - (e * u).sum(1) / (1 + r)
+    p, left = 1 / (1 + r), r / (1 + r)
+    want = f64(a) * left - f64(b) * p * (h - ls)
+    rel = 1.05 * (2 * (V / 256 + 32) + 4 * float(u.abs().max()) + 32) * U
+    bound = rel * (f64(a).abs() * left + f64(b).abs() * (h + ls))
+    assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / bound).max())
