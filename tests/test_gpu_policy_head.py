@@ -262,3 +262,23 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(a, b) for o in got[i] for a, b in zip(o, want[i])), i
+
+
+@pytest.mark.parametrize("V,bad", [(1003, None), (1000, "d_h"), (1000, "norm_w"), (1000, "y")])
+def test_a_refused_gradient_leaves_the_logits(V, bad):
+    """A call over the saved logits that is refused has not written them."""
+    T = 6
+    norm_w, head_w, g = head(V)
+    x, r = tokens(T, 300)
+    ids = torch.randint(0, V, (T,), generator=g).to(torch.int32).cuda()
+    f = ph.policy_head_forward(x, r, norm_w, head_w, ids)
+    before = f["logits"].clone()
+    d_h = torch.zeros(T, H + 8, dtype=torch.bfloat16, device="cuda") if bad == "d_h" else None
+    if bad == "norm_w":
+        norm_w = norm_w[:-1]
+    if bad == "y":
+        f["y"] = torch.zeros(T * H + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H)
+    with pytest.raises((ValueError, TypeError)):
+        ph.policy_head_backward(f, norm_w, head_w, ids, torch.ones(T, device="cuda"), d_h=d_h, reuse_logits=True)
+    torch.cuda.synchronize()
+    assert torch.equal(f["logits"], before)
