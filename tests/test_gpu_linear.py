@@ -340,3 +340,24 @@ def test_dz_is_the_nearest(act):
     assert ((got - want).abs() <= (0.5 + 1e-9) * step + TINY * (want.abs() < 2.0 ** -126)).all(), float(((got - want).abs() / step).max())
     alone = pqm.linear_backward(dy[5:6].cuda(), x[:1], w, act, zz[:1], need_dx=False)
     assert torch.equal(alone[1][:, 0], dz[5].float())
+
+
+@pytest.mark.parametrize("act", [pqm.ACT_SILU, pqm.ACT_GELU])
+@pytest.mark.parametrize("M,K", [(2, 8), (1500, 512)])
+def test_activations_keep_their_small_values(act, M, K):
+    """z where e^-s leaves binary32 but z e^s does not, up to where it is below half the
+    smallest subnormal bf16: relative errors of 5 U |s| for the argument (constants,
+    square, sum, product), of 10 U for the rest (the exponential twice, five roundings,
+    the reciprocal), half a step of a subnormal bf16 value, and 2^-134 where the
+    reciprocal has left binary32."""
+    N = 520
+    far = torch.linspace(-110, -60, N) if act == pqm.ACT_SILU else torch.linspace(-10.6, -8.4, N)
+    x = torch.zeros(M, K, dtype=torch.bfloat16).cuda()
+    w = torch.zeros(N, K, dtype=torch.bfloat16).cuda()
+    a, _, _ = activation(f64(far), act)
+    rel = 1.01 * (5 * squash(f64(far), act).abs() + 10) * U
+    for dtype, half, step in ((pqm.OUT_FP32, 0.0, 2.0 ** -134), (pqm.OUT_BF16, HALF_BF16, 2.0 ** -133)):
+        y, _ = pqm.linear(x, w, far.cuda(), act, out_dtype=dtype)
+        bound = rel * a.abs() + half * a.abs() + step
+        assert ((f64(y) - a).abs() <= bound).all(), float(((f64(y) - a).abs() / bound).max())
+        assert f64(y).ne(0).sum() >= (a.abs() > 2 * step).sum() * M
