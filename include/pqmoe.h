@@ -795,7 +795,8 @@ size_t pqm_linear_workspace(int64_t M, int64_t N, int64_t K);
  * only, w for dx only.  dx may be the memory of d_x, with ldd == K, and dz that
  * of z; nothing else may overlap an output.  M == 0 writes dw = 0, dbias = 0.
  * workspace as above, of pqm_linear_backward_workspace bytes.
- * Requires the sizes above, N >= 8, N % 8 == 0, N <= lddy <= 2^22,
+ * Requires the sizes above, M <= 2^29 - 32, fewer than 2^24 tiles of 128 x 128 of
+ * dx and of dw too, N >= 8, N % 8 == 0, N <= lddy <= 2^22,
  * K <= ldx, ldd <= 2^22 (PQM_ERR_SHAPE); all tensors, lddy and ldx aligned to
  * 16 bytes, d_x to 2 (PQM_ERR_ALIGN).
  */

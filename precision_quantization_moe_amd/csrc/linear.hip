@@ -822,6 +822,13 @@ bool ln_sizes(int64_t M, int64_t N, int64_t K) {
          K <= LN_MAX && ln_tiles(M, N, 128, 128) < (1 << 24) && M <= ((int64_t)1 << 40) / (N + K);
 }
 
+// And their gradients: a launch holds fewer than 2^32 threads, 256 for each tile of dx
+// and of dW and for each LZ_ROWS rows of dz.
+bool ln_backward_sizes(int64_t M, int64_t N, int64_t K) {
+  return ln_sizes(M, N, K) && N >= 8 && N % 8 == 0 && M <= ((int64_t)1 << 29) - LZ_ROWS &&
+         ln_tiles(M, K, 128, 128) < (1 << 24) && ln_tiles(N, K, 128, 128) < (1 << 24);
+}
+
 size_t ln_forward_bytes(int64_t M, int64_t N, int64_t K) {
   return ln_is_few(M, N, K) ? 0 : ln_partial_bytes(ln_plan(LN_NT, M, N, K), M, N);
 }
@@ -845,7 +852,7 @@ size_t pqm_linear_workspace(int64_t M, int64_t N, int64_t K) {
 
 size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   using namespace pqm;
-  return !ln_sizes(M, N, K) || M == 0 || N == 0 || N % 8 ? 0 : ln_backward_bytes(M, N, K);
+  return !ln_backward_sizes(M, N, K) || M == 0 ? 0 : ln_backward_bytes(M, N, K);
 }
 
 pqm_status pqm_linear(const uint16_t *x, int64_t ldx, const uint16_t *w, const float *bias,
@@ -884,11 +891,11 @@ pqm_status pqm_linear_backward(const uint16_t *dy, int64_t lddy, const uint16_t 
                                void *workspace, size_t workspace_bytes, hipStream_t stream) {
   using namespace pqm;
   if (act != PQM_ACT_NONE && act != PQM_ACT_SILU && act != PQM_ACT_GELU) return PQM_ERR_ENUM;
-  if (!ln_sizes(M, N, K) || N % 8 || lddy < N || lddy > LN_MAX || (dw && (ldx < K || ldx > LN_MAX)) ||
-      (dx && d_x && (ldd < K || ldd > LN_MAX)) || (dx && d_x == dx && ldd != K))
+  if (!ln_backward_sizes(M, N, K) || lddy < N || lddy > LN_MAX ||
+      (dw && (ldx < K || ldx > LN_MAX)) || (dx && d_x && (ldd < K || ldd > LN_MAX)) ||
+      (dx && d_x == dx && ldd != K))
     return PQM_ERR_SHAPE;
   if (!dx && !dw && !dbias) return PQM_ERR_NULL;
-  if (N == 0) return PQM_ERR_SHAPE;
   if (M > 0 &&
       (!dy || (dw && !x) || (dx && !w) || (act != PQM_ACT_NONE && (!z || !dz))))
     return PQM_ERR_NULL;

@@ -111,3 +111,15 @@ def test_gradients_against_differences(gelu):
             # the differences' own error: h^2 / 6 of a third derivative below 100, and
             # 2^-52 of a loss below 50 over 2e-5
             assert abs(float(step[0] - step[1]) / 2e-5 - float(grad.view(-1)[at])) < 1e-8
+
+
+def test_gradients_of_more_than_one_launch_holds():
+    """2^24 groups of 32 rows, or 2^24 tiles of dx or of dw, are more workgroups
+    of 256 threads than one launch takes: refused as sizes, with no workspace."""
+    size = pqm.lib().pqm_linear_backward_workspace
+    c = caller("pqm_linear_backward",
+               [A, 8, A, 8, A, 1, A, None, 0, 1 << 20, 8, 8, D, D, D, D, A, 1 << 50, None])
+    assert size((1 << 29) - 31, 8, 8) == 0 and size((1 << 29) - 32, 8, 8) > 0
+    assert c(a9=(1 << 29) - 31) == 2 and c(a9=(1 << 29) - 1) == 2
+    assert size(1 << 24, 8, 65528) == 0 and c(a9=1 << 24, a11=65528, a3=65528) == 2
+    assert size(8, 1 << 22, 1 << 16) == 0 and c(a9=8, a10=1 << 22, a1=1 << 22, a11=1 << 16, a3=1 << 16) == 2
