@@ -52,3 +52,14 @@ def gpu_normal_bf16(rows: int, cols: int, std: float, seed: int) -> torch.Tensor
         n = min(step, rows - r)
         out[r:r + n] = (torch.randn(n, cols, generator=g, device="cuda") * std).to(torch.bfloat16)
     return out
+
+
+def kernels(call):
+    """The names of the library's kernels that call() launches, in their order."""
+    call()
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA], acc_events=True) as p:
+        call()
+        torch.cuda.synchronize()
+    found = [e for e in p.events() if "pqm::" in e.name]
+    return [e.name for e in sorted(found, key=lambda e: e.time_range.start)]
