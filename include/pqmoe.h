@@ -723,8 +723,10 @@ pqm_status pqm_moe_gemv_swiglu_nvfp4(const uint16_t *x, const int32_t *ids, cons
  *   pqm_quantize_nvfp4_per_token makes them with one outer scale per expert
  * The logits are sums of exact products, in binary64 over partial sums of 32,
  * so that two close ones keep their order; they are rounded to binary32.  d and
- * out are sums in binary32 of exact products.  A NaN in a token's row makes that
- * token's results NaN and no other's.  The last bits of d and out may depend on
+ * out are sums in binary32.  The weights are exact in their products; so are y and
+ * d down to 2^-31 of the largest value of their row, and smaller values are off by
+ * less than 2^-38 of it (they may enter in scaled binary16).  A NaN in a token's
+ * row makes that token's results NaN and no other's.  The last bits of d and out may depend on
  * how many tokens and which experts a call has, never on the run.
  * workspace (device, 16-byte aligned, contents irrelevant):
  * pqm_moe_decode_nvfp4_workspace bytes; calls that may run at the same time

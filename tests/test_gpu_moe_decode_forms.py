@@ -9,9 +9,11 @@ import math
 import pytest
 import torch
 
+import operators_ref as ref
 import precision_quantization_moe_amd as pqm
+from precision_quantization_moe_amd import moe_layer as ml
 from gpu_util import kernels, requires_gpu
-from operators_ref import HALF_BF16, f64
+from operators_ref import HALF_BF16, U, f64
 from test_gpu_moe_decode import check, tokens, weights
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
@@ -77,3 +79,36 @@ def test_the_last_experts_are_met():
     torch.cuda.synchronize()
     assert (o[3].cpu() == torch.arange(E - 1, E - 1 - k, -1)).all()
     check(o, x, None, norm_w.abs(), gate_w, q, k, I, True, True, True, 1.0)
+
+
+@pytest.mark.parametrize("T", [1, 6, 20])
+@pytest.mark.parametrize("power", [30, 40, 60])
+def test_one_value_far_above_its_row(T, power):
+    """y's first value 2^power times the others, with weights of 0 for it: the others
+    are exact down to 2^-31 of it, and off by less than 2^-38 of it below."""
+    E, k, H, I = 16, 4, 256, 128
+    g = torch.Generator().manual_seed(T + power)
+    w1 = (torch.randn(E * 2 * I, H, generator=g) * 0.05).to(torch.bfloat16)
+    w1[:, 0] = 0
+    w2 = (torch.randn(E * H, I, generator=g) * 0.05).to(torch.bfloat16).cuda()
+    q = ml.quantize_expert_weights_nvfp4(w1.cuda(), w2, I, H)
+    gate_w = (torch.randn(E, H, generator=g) / H ** 0.5).to(torch.bfloat16)
+    gate_w[:, 0] = 0
+    # the others between 1 and 2 of a power of two, so that all are 2^-31 of the first at 30
+    x = (1 + torch.rand(T, H, generator=g)) * (1 - 2.0 * torch.randint(0, 2, (T, H), generator=g))
+    norm_w = torch.ones(H)
+    norm_w[0] = 2.0 ** power
+    x, gate_w, norm_w = x.to(torch.bfloat16).cuda(), gate_w.cuda(), norm_w.cuda()
+    o = pqm.moe_decode_nvfp4(x, None, norm_w, gate_w, *q, k, I)
+    torch.cuda.synchronize()
+    y, ids, prob, d = o[2].cpu(), o[3].cpu(), f64(o[4]).reshape(-1, 1), f64(o[5])
+    s, size = ref.gemv(y, ids, *q[:3], 2 * I, 2 * I, k)
+    e = (H / 32 + 64) * 2 * U * size
+    if power > 30:
+        _, ones = ref.gemv(torch.ones_like(y), ids, *q[:3], 2 * I, 2 * I, k)
+        e = e + 2.0 ** -38 * f64(y).abs().amax(1).repeat_interleave(k)[:, None] * ones
+    gate, up, eg, eu = s[:, :I], s[:, I:], e[:, :I], e[:, I:]
+    want = gate * torch.sigmoid(gate) * up * prob
+    bound = prob * (1.1 * eg * (up.abs() + eu) + (gate * torch.sigmoid(gate)).abs() * eu) + \
+        (gate.abs() + 9) * 2 * U * want.abs()
+    assert ((d - want).abs() <= HALF_BF16 * (want.abs() + bound) + bound).all()
