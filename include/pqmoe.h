@@ -811,8 +811,8 @@ size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
  * What a policy's logits say of given tokens: the log probabilities that
- * rollout and training are compared by ([MT] 4.5: one formula and one order of
- * the sums on both sides), the entropy of each row, and its best alternatives.
+ * rollout and training are compared by ([MT] 4.5; one formula on both sides),
+ * the entropy of each row, and its best alternatives.
  * With x a row of logits, M its largest, u_i = (x_i - M) / temperature,
  * S = sum e^u:
  *   logprob = u_id - log S,   entropy = log S - (sum e^u u) / S,
@@ -828,7 +828,10 @@ size_t pqm_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
  * top_ids -1.  logprob, entropy, stats may be NULL (one result is required).
  * A logit of -inf is a token that cannot come; a row of -inf alone has
  * logprob -inf, entropy 0, stats (-inf, 0).  A NaN or +inf makes the row's
- * results NaN (M apart); a NaN ranks first.  The arithmetic is binary32.
+ * results NaN (M apart); a NaN ranks first.  The arithmetic is binary32; a row's
+ * results depend on tokens, vocab and top_n besides its own values, which decide
+ * the order of its sums: between calls of other sizes their last bits may differ,
+ * between runs or by the row's place they do not.
  * workspace (device, 8-byte aligned, contents irrelevant):
  * pqm_token_logprobs_workspace bytes, 0 where a row is one workgroup's; calls
  * that may run at the same time need separate ones.

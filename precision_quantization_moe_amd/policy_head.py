@@ -4,8 +4,11 @@ tokens that were taken, and back.
 Reinforcement learning compares the log probabilities that the rollout engine
 gave its tokens with the ones that training gives them; both sides run these
 passes, so that what differs between them is the layers below ("Towards
-Blackwell-Native 8-bit and 4-bit RL").  Each function only sequences calls into
-libpqmoe on torch's current stream.
+Blackwell-Native 8-bit and 4-bit RL"), and last bits: the order of the sums goes
+by the number of rows, so a call of 8 rows and one of 2048 give the same row's
+logits off by roundings of binary32, which now and then is a step of bf16
+(logits_dtype OUT_FP32 keeps it at binary32's).  Each function only sequences
+calls into libpqmoe on torch's current stream.
 """
 from __future__ import annotations
 

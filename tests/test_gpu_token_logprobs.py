@@ -386,3 +386,21 @@ def test_gradients_of_nearly_certain_rows(T, V, dtype, which):
     rel = 1.05 * (2 * (V / 256 + 32) + 4 * float(u.abs().max()) + 32) * U
     bound = rel * (f64(a).abs() * left + f64(b).abs() * (h + ls))
     assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / bound).max())
+
+
+@pytest.mark.parametrize("n", [0, 5])
+def test_rows_do_not_depend_on_their_place(n):
+    """In calls of the same sizes a row has the same bits wherever it stands; in calls
+    of other sizes they are within the bounds of both."""
+    T, V = 1500, 9001
+    x, ids, g = logits(T, V, torch.bfloat16, 5)
+    p = torch.randperm(T, generator=g)
+    a = pqm.token_logprobs(x.cuda(), ids.cuda(), 0.7, n)
+    b = pqm.token_logprobs(x[p].cuda(), ids[p].cuda(), 0.7, n)
+    one = torch.ones(T).cuda()
+    da = pqm.token_logprobs_backward(x.cuda(), ids.cuda(), a[2], one, 0.7, a[1], one)
+    db = pqm.token_logprobs_backward(x[p].cuda(), ids[p].cuda(), b[2], one, 0.7, b[1], one)
+    for u, v in zip(a + (da,), b + (db,)):
+        assert u is None and v is None or torch.equal(u[p.cuda()], v)
+    for few in (1, 3, 300):
+        check(x[:few], ids[:few], 0.7, n, pqm.token_logprobs(x[:few].cuda(), ids[:few].cuda(), 0.7, n))
