@@ -240,3 +240,32 @@ def test_dx_past_the_caches(M, N, K):
                                          torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert code == 0 and torch.equal(own, dx)
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_the_widest_row_strides(M):
+    """Rows 2^22 values apart, the most that is taken: a tile's offsets come close to
+    2^31 bytes."""
+    N, K, wide = 4096, 512, 1 << 22
+    x, w, b, r, g = operands(M, N, K)
+    dy = rand(g, M, N).cuda()
+    far = [torch.empty(M * wide, dtype=torch.bfloat16, device="cuda").view(M, wide) for _ in range(2)]
+    fx, fr = far[0][:, 64:64 + K], far[1][:, wide - N:]
+    fx.copy_(x)
+    fr.copy_(r)
+    want = pqm.linear(x, w, b, pqm.ACT_SILU, r, True)
+    got = pqm.linear(fx, w, b, pqm.ACT_SILU, fr, True)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    want = pqm.linear_backward(dy, x, w, d_x=x, need_dbias=True)
+    fr.copy_(dy)
+    got = pqm.linear_backward(fr, fx, w, d_x=fx, need_dbias=True)
+    assert all(torch.equal(a, c) for a, c in zip(got[:3], want[:3]))
+
+
+def test_binary32_outputs_beside_streamed_ones():
+    """y in binary32 with a streamed z and residual gives z the same bits as y in bf16,
+    whose values are y's rounded."""
+    x, w, b, r, _ = operands(8200, 8200, 264)
+    y, z = pqm.linear(x, w, b, pqm.ACT_GELU, r, True, pqm.OUT_FP32)
+    y16, z16 = pqm.linear(x, w, b, pqm.ACT_GELU, r, True)
+    assert torch.equal(z, z16) and torch.equal(y.to(torch.bfloat16), y16)

@@ -282,3 +282,17 @@ def test_a_refused_gradient_leaves_the_logits(V, bad):
         ph.policy_head_backward(f, norm_w, head_w, ids, torch.ones(T, device="cuda"), d_h=d_h, reuse_logits=True)
     torch.cuda.synchronize()
     assert torch.equal(f["logits"], before)
+
+
+def test_no_tokens():
+    V = 1000
+    norm_w, head_w, _ = head(V)
+    x = torch.zeros(0, H, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(0, dtype=torch.int32, device="cuda")
+    f = ph.policy_head_forward(x, x, norm_w, head_w, ids, 0.9, 4)
+    assert f["logits"].shape == (0, V) and f["top_ids"].shape == (0, 4) and f["logprob"].shape == (0,)
+    none = torch.zeros(0, device="cuda")
+    b = ph.policy_head_backward(f, norm_w, head_w, ids, none, none, x, 0.9, reuse_logits=True)
+    torch.cuda.synchronize()
+    assert b["dx"].shape == (0, H) and not b["d_head_w"].any() and not b["d_norm_w"].any()
+    assert b["d_head_w"].shape == (V, H) and b["d_norm_w"].shape == (H,)

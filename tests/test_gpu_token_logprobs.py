@@ -404,3 +404,29 @@ def test_rows_do_not_depend_on_their_place(n):
         assert u is None and v is None or torch.equal(u[p.cuda()], v)
     for few in (1, 3, 300):
         check(x[:few], ids[:few], 0.7, n, pqm.token_logprobs(x[:few].cuda(), ids[:few].cuda(), 0.7, n))
+
+
+def test_a_row_of_many_logits():
+    """2^28 + 5 logits in one row: places beyond 2^24, parts of many turns, the best
+    ones near the end.  A thread adds 2^28 / 128 / 256 = 8192 values and the joining 140
+    more; |u| is below 12."""
+    V = (1 << 28) + 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.rand(1, V, generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    best = [V - 1, V - 7, 5, V // 2 + 1]
+    for i, at in enumerate(best):
+        x[0, at] = 9.0 - i
+    id_ = torch.tensor([V - 7], dtype=torch.int32).cuda()
+    lp, ent, stats, ids, top = pqm.token_logprobs(x, id_, 1.0, 4)
+    u = x[0].double() - 9.0
+    s = torch.exp(u).sum()
+    h = torch.log(s) - (torch.exp(u) * u).sum() / s
+    rel = 1.05 * ((8192 + 156) * 2 + 4 * 12) * U
+    assert ids[0].tolist() == best and float(stats[0, 0]) == 9.0
+    assert abs(float(stats[0, 1]) - float(torch.log(s))) <= rel + 4 * U * 20
+    assert abs(float(lp) - float(-1.0 - torch.log(s))) <= rel + 8 * U * 20
+    assert abs(float(ent) - float(h)) <= rel + 12 * (2 * rel + 16 * U) + 8 * U * 32 + 144 * 4 * U
+    d = pqm.token_logprobs_backward(x, id_, stats, torch.ones(1, device="cuda"), out_dtype=pqm.OUT_FP32)
+    p = torch.exp(u[best] - torch.log(s))
+    want = -p + torch.tensor([0.0, 1.0, 0.0, 0.0], dtype=torch.float64, device="cuda")
+    assert ((d[0, best].double() - want).abs() <= p * (rel + 200 * U) + 4 * U * want.abs()).all()
