@@ -770,8 +770,9 @@ size_t pqm_moe_decode_nvfp4_workspace(int64_t tokens, int64_t hidden, int64_t in
  * Requires K % 8 == 0, 8 <= K <= 2^22, 0 <= N <= 2^22, M < 2^29 with fewer than
  * 2^24 tiles of 128 x 128 and M (N + K) <= 2^40, K <= ldx <= 2^22,
  * N <= ldr <= 2^22 (PQM_ERR_SHAPE); x, w, y, z and ldx aligned to 16 bytes,
- * bias 4, residual 2 (PQM_ERR_ALIGN).  N and ldr of whole 8 and residual
- * aligned to 16 bytes are stored faster.
+ * bias 4, residual 2 (PQM_ERR_ALIGN).  Beyond a few rows N and ldr of whole 8
+ * and a residual aligned to 16 bytes are faster (8190 x 4096 x 2048 141 us, 4095
+ * outputs 203; with everything in the epilogue 168 and 402).
  */
 typedef enum pqm_act {
     PQM_ACT_NONE = 0,

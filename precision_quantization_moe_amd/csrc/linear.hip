@@ -179,11 +179,14 @@ __device__ __forceinline__ void ln_put8(const LnEpi &e, int64_t r, int64_t c, fl
 // Four waves, 2 x 2, a tile; operands by DMA into a ring of LDS slots of 32 of the
 // contraction, fragments read one step ahead.  256 x 256: a wave's 128 x 128 outputs
 // take half the LDS bytes of 128 x 128 tiles a product, at one workgroup a CU.
-// 8190 x 4096 x 2048 with SiLU, bias, residual and z kept 162 us (the product alone by
+// 8190 x 4096 x 2048 with GELU, bias, residual and z kept 164 us (the product alone by
 // the library 111): the steps 131 (1050 TFLOP/s) and two epilogues of 16, in which all
-// CUs move their 384 KB of residual, y and z at once and multiply nothing.  Without
-// an epilogue dx of the same layer takes 123 (library 120), dW 152 (174).  The router,
-// 16384 x 128 x 2048, 22.7 us: 75 MB at 3.3 TB/s, one workgroup a CU; its dx 36, 138 MB.
+// CUs move their 384 KB of residual, y and z at once and multiply nothing.  The matrix
+// cores are busy 36 % of its cycles, 46 % without the epilogue (141 us), where a wave
+// waits for loads or the barrier 21 % of its time and no LDS access meets a conflict.
+// dx of the same layer takes 126 to 137 (library 120), dW 151 to 160 (174).  The router,
+// 16384 x 128 x 2048, 22.6 us: 75 MB at 3.3 TB/s, which is what its 128 workgroups, on
+// half of the CUs, draw; its dx 36, 138 MB.
 
 enum { LN_NT = 0, LN_NN = 1, LN_TN = 2 };  // y; dx (B is ML); dW (both are ML)
 
@@ -452,6 +455,8 @@ __global__ __launch_bounds__(256, NS * (TM + TN) * 64 > 81920 ? 1 : 2) void k_li
         }
       }
     } else {
+      // one output at a time: 8190 x 4095 x 2048 203 us where 4096 outputs take 141, with
+      // an activation, bias, residual and z 402 and 168
       const int n = (int)min((int64_t)8, t.J - col);
 #pragma unroll 1
       for (int r = 0; r < NR && row + r * RPI < t.I; ++r)
@@ -615,7 +620,7 @@ constexpr int LZ_ROWS = 32;  // rows of a workgroup's partial sums
 // dz = bf16(dy act'(z)) (act none: dy itself, not written) and, per LZ_ROWS
 // rows, the column sums of dz.  A thread takes eight columns of every 256 / CT-th
 // row, four rows asked for at once; CT threads a row, as many as fill it.  Bound by
-// memory and by the values formed again: 8190 x 4096 in 53 us (201 MB, 40 at a copy's
+// memory and by the values formed again: 8190 x 4096 in 54 us (201 MB, 40 at a copy's
 // rate and without them).
 template <int CT>
 __global__ __launch_bounds__(256) void k_linear_dz(const uint16_t *__restrict__ dy, int64_t lddy,

@@ -503,7 +503,9 @@ __device__ __forceinline__ int dc_sweep(DcSync *sync, int total) {
 // the parts in their order.
 //
 // Bound by the chain gate, weights, join, weights, join; one token, top-8 of 128 experts
-// of 2048 x 768: 21 MB in 15.2 to 17 us (4.2 at a copy's rate).
+// of 2048 x 768: 21 MB in 15.2 to 17 us (4.2 at a copy's rate).  Above 256 experts the 16
+// sets of those met leave the registers (44 bytes a lane in scratch): the whole layer
+// 24.2 us for 256 experts and 30.4 for 512, for three tokens 35.7 and 44.8.
 template <int VPL, bool WORDS1, bool WORDS2>
 __global__ __launch_bounds__(64 * DC_WAVES, 4) void k_decode_experts(DcArgs a) {
   __shared__ DcSets s;

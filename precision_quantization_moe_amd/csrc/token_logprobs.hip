@@ -13,8 +13,8 @@
 // u log2(e).
 //
 // Both directions are bound by memory where there are many rows: 4093 rows of 32768
-// bf16, a fifth of them left out, in 44 us (4.9 TB/s of the rows that are read);
-// gradient of 2048 rows of 151936 bf16, a fifth left out, in 192 us (5.8 TB/s, read and
+// bf16, a fifth of them left out, in 42 us (5.1 TB/s of the rows that are read);
+// gradient of 2048 rows of 151936 bf16, a fifth left out, in 190 us (5.8 TB/s, read and
 // written), of 509 rows of 50257 binary32, an odd length, in 44 (4.6).  One row of 151936 is split over workgroups and bound by
 // the chain of load, choice of the best, join: 17.5 us with 20 alternatives.
 #include "pqm_device.hpp"

@@ -258,8 +258,9 @@ def mxfp8_moe_block_forward(x, residual, norm_w, gate_w, w1q, w1s, w2q, w2s, k: 
     The weights are those of gate_w's E experts, as quantize_expert_weights_mxfp8
     returns them.  router: the entry point of the router's product, "grouped"
     (a grouped GEMM of one group) or "linear" (a dense product, the faster one;
-    the last bits of its binary32 logits differ).  Returns the experts' dict and
-    h, y, rstd, logits, ids, prob, counts, prob_sum, loss."""
+    the last bits of its binary32 logits differ; it takes any E here, of which
+    the backward pass needs E % 8 == 0 as "grouped" does).  Returns the experts'
+    dict and h, y, rstd, logits, ids, prob, counts, prob_sum, loss."""
     _linear_router(router)
     T, H = x.shape
     plan = _plan(plan, T, k, x.device)
